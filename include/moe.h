@@ -265,6 +265,82 @@ int moe_ctx_flags(moe_ctx *ctx, int32_t *flags, int32_t reset, void *stream);
  * NULL is a no-op. */
 void moe_ctx_destroy(moe_ctx *ctx);
 
+/* ------------------------------------------------------ expert operators
+ * Building blocks of an expert FFN on 16-bit and four-bit weights: products
+ * grouped by expert with their gradients, the microscaled four-bit format
+ * with its product, and SwiGLU with its gradient.  They work on the layer's
+ * pair order (moe_debug: perm, offsets): pairs sorted by expert, expert e's
+ * pairs being offsets[e] .. offsets[e+1] - 1, any number of them.
+ *
+ * The conventions above hold.  In addition:
+ *  - Nothing is allocated, no workspace is needed and nothing synchronises;
+ *    every call can be captured into a graph.  Results do not depend on
+ *    timing: the same call gives the same bits.
+ *  - Strides are in elements, between rows; a row's elements are consecutive.
+ *    Matrices start 16-byte aligned and their row strides are multiples of
+ *    16 bytes and at most 2^21 elements.  Banks b are dense.  Outputs must
+ *    not overlap inputs.
+ *  - Sums are held in fp32 and rounded once to the output type, which is the
+ *    operands' type or fp32. */
+enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_F16 = 3 };
+#define MOE_MAX_PAIRS (1 << 20) /* rows of a grouped call */
+
+/* The groups of a grouped product.  offsets is a device array; its entries
+ * are clamped to [0, pairs] where the kernels read them, and rows before
+ * offsets[0] or past offsets[n_experts] belong to no group: their outputs
+ * are zeros.  rows, if given, is a device array of one entry for each pair:
+ * pair p reads row rows[p] of a (src_rows rows; an entry outside [0,
+ * src_rows) reads a row of zeros); without it pair p reads row p. */
+typedef struct moe_grouped {
+    int32_t n_experts;      /* 1..1024 */
+    int32_t out_features;   /* N: multiple of 8, at most 65536 */
+    int32_t in_features;    /* K: multiple of 8 (four-bit operands: 32), at most 65536 */
+    int64_t pairs;          /* P: rows of c, dc, da */
+    const int32_t *offsets; /* [n_experts + 1] */
+    const int32_t *rows;    /* [pairs] or NULL */
+    int64_t src_rows;       /* rows of a when rows is given (a must then span less than 2 GiB) */
+} moe_grouped;
+
+/* c[p] = a[rows[p]] . b[e(p)]^T, b[n_experts][N][K]; dtype MOE_DT_BF16 or MOE_DT_F16. */
+int moe_grouped_mm(const moe_grouped *g, int32_t dtype, const void *a, int64_t a_stride, const void *b, void *c,
+                   int32_t c_dtype, int64_t c_stride, void *stream);
+/* da[p] = dc[p] . b[e(p)]: one row for each pair (g->rows is not looked at:
+ * the gradient of a row that several pairs read is the sum of theirs). */
+int moe_grouped_mm_grad_a(const moe_grouped *g, int32_t dtype, const void *dc, int64_t dc_stride, const void *b,
+                          void *da, int32_t da_dtype, int64_t da_stride, void *stream);
+/* db[e] = sum over the pairs p of e of dc[p]^T a[rows[p]], db[n_experts][N][K];
+ * zeros for an expert without pairs. */
+int moe_grouped_mm_grad_b(const moe_grouped *g, int32_t dtype, const void *dc, int64_t dc_stride, const void *a,
+                          int64_t a_stride, void *db, int32_t db_dtype, void *stream);
+
+/* Microscaled four-bit floating point.  A row of cols elements (a multiple of
+ * 32) is codes[cols / 2] and scales[cols / 32]: element 2 i is the low nibble
+ * of byte i; bit 3 of a nibble is the sign, bits 0..2 index {0, .5, 1, 1.5,
+ * 2, 3, 4, 6}; block j of 32 elements has the scale 2^(scales[j] - 127), 255
+ * meaning not a number.  Quantising takes 2^(floor(log2 max|x|) - 2) (not
+ * below 2^-127) and rounds to the nearest value, ties to the even code, past
+ * 6 to 6; a block with a NaN or an infinity gets scale 255.  x may be fp32,
+ * bf16 or fp16.  Codes and scales are dense, codes 16-byte aligned. */
+int moe_mxfp4_quantize(int32_t dtype, const void *x, int64_t x_stride, int64_t rows, int64_t cols, uint8_t *codes,
+                       uint8_t *scales, void *stream);
+int moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int32_t dtype,
+                         void *x, int64_t x_stride, void *stream);
+/* moe_grouped_mm with both operands in that format: a [a rows][K], b
+ * [n_experts][N][K]; c in bf16 or fp32. */
+int moe_mxfp4_grouped_mm(const moe_grouped *g, const uint8_t *a_codes, const uint8_t *a_scales,
+                         const uint8_t *b_codes, const uint8_t *b_scales, void *c, int32_t c_dtype, int64_t c_stride,
+                         void *stream);
+
+/* h = silu(gate) * up for rows of gu = [gate | up] (2 ffn elements; ffn a
+ * multiple of 8, for the four-bit output of 32), and its gradient dgu =
+ * [dgate | dup] from dh.  fp32, bf16 or fp16 in and out, computed in fp32. */
+int moe_swiglu(int32_t dtype, const void *gu, int64_t gu_stride, int64_t rows, int64_t ffn, void *h, int64_t h_stride,
+               void *stream);
+int moe_swiglu_mxfp4(int32_t dtype, const void *gu, int64_t gu_stride, int64_t rows, int64_t ffn, uint8_t *codes,
+                     uint8_t *scales, void *stream);
+int moe_swiglu_grad(int32_t dtype, const void *dh, int64_t dh_stride, const void *gu, int64_t gu_stride, int64_t rows,
+                    int64_t ffn, void *dgu, int64_t dgu_stride, void *stream);
+
 /* Per-stage timing with HIP events.  While a profiler is attached to the
  * calling thread, every kernel a forward call launches records its own start
  * and end into two events (hipExtLaunchKernelGGL; dispatch latency between

@@ -62,6 +62,12 @@ class Debug(ctypes.Structure):
                  "gate_sums", "up_sums", "down_sums")] + [("sum_row_stride", ctypes.c_int32)]
 
 
+class Grouped(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("pairs", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("src_rows", ctypes.c_int64)]
+
+
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "moe_abi_version": ([], ctypes.c_int),
@@ -84,6 +90,15 @@ _SIGS = {
     "moe_ctx_forward": ([_P, _P, _P, _I32, _P, _P], ctypes.c_int),
     "moe_ctx_flags": ([_P, ctypes.POINTER(_I32), _I32, _P], ctypes.c_int),
     "moe_ctx_destroy": ([_P], None),
+    "moe_grouped_mm": ([ctypes.POINTER(Grouped), _I32, _P, _I64, _P, _P, _I32, _I64, _P], ctypes.c_int),
+    "moe_grouped_mm_grad_a": ([ctypes.POINTER(Grouped), _I32, _P, _I64, _P, _P, _I32, _I64, _P], ctypes.c_int),
+    "moe_grouped_mm_grad_b": ([ctypes.POINTER(Grouped), _I32, _P, _I64, _P, _I64, _P, _I32, _P], ctypes.c_int),
+    "moe_mxfp4_quantize": ([_I32, _P, _I64, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "moe_mxfp4_dequantize": ([_P, _P, _I64, _I64, _I32, _P, _I64, _P], ctypes.c_int),
+    "moe_mxfp4_grouped_mm": ([ctypes.POINTER(Grouped), _P, _P, _P, _P, _P, _I32, _I64, _P], ctypes.c_int),
+    "moe_swiglu": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
+    "moe_swiglu_mxfp4": ([_I32, _P, _I64, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "moe_swiglu_grad": ([_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
     "moe_stage_name": ([_I32], ctypes.c_char_p),
     "moe_prof_create": ([ctypes.POINTER(_P), _I32], ctypes.c_int),
     "moe_prof_destroy": ([_P], None),
@@ -285,8 +300,11 @@ class Profiler:
 
 
 from .layer import MoELayer  # noqa: E402
+from .expert_ops import (grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_dequantize,  # noqa: E402
+                         mxfp4_grouped_mm, mxfp4_quantize, swiglu, swiglu_grad, swiglu_mxfp4)
 
 __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Profiler", "make_shape", "workspace_bytes",
            "pack_weights", "layer_forward", "layer_forward_static", "STATIC_SCRATCH_BYTES", "workspace_init", "workspace_flags", "check_hash_table", "matrix_bytes",
            "abi_version", "FMT_Q8", "FMT_Q2", "FLAG_BAD_TOKEN", "FLAG_BAD_TABLE_ENTRY", "FLAG_REPEATED_EXPERT", "ROUTE_LEARNED", "ROUTE_HASH", "ROUTE_HASH_SCORED", "EXPORTED",
-           "LIB_PATH"]
+           "LIB_PATH", "Grouped", "grouped_mm", "grouped_mm_grad_a", "grouped_mm_grad_b", "mxfp4_quantize",
+           "mxfp4_dequantize", "mxfp4_grouped_mm", "swiglu", "swiglu_mxfp4", "swiglu_grad"]

@@ -135,6 +135,8 @@ static thread_local moe_prof *t_prof = nullptr;
 static thread_local int t_stage = -1;  // stage of the forward call running on this thread, or -1
 
 namespace qrmoe {
+int status_of(hipError_t e) { return hip_status(e); }
+
 bool next_launch_events(hipEvent_t *start, hipEvent_t *stop) {
     moe_prof *p = t_prof;
     if (!p || t_stage < 0 || p->next + 2 > p->pool.size()) return false;

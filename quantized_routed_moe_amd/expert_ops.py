@@ -1,0 +1,285 @@
+"""Expert operators on 16-bit and four-bit weights: products grouped by expert
+with their gradients, the microscaled four-bit format with its product, SwiGLU
+with its gradient.
+
+Argument checks and marshalling only; the operators are HIP kernels behind the
+C ABI of include/moe.h.  Rows are (token, expert) pairs sorted by expert:
+expert e owns rows offsets[e] .. offsets[e+1] - 1 (any number), `offsets` and
+`rows` being int32 tensors on the GPU.  Work is enqueued on `stream` (the
+current stream by default) without synchronising; a result that is not passed
+in as `out` is allocated for that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import Grouped, _check, _layout, _lib, _on_gpu
+
+DT = {torch.float32: 1, torch.bfloat16: 2, torch.float16: 3}
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _dtype(t, name, allowed):
+    if t.dtype not in allowed:
+        raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {t.dtype}")
+
+
+def _matrix(t, name, dtype, rows, cols):
+    """Shape, type and layout of a 2-d operand whose rows may be strided; returns its row stride."""
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: expected shape ({'rows' if rows is None else rows}, {cols}), got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape[0] < 2:  # the stride of a single row says nothing
+        if t.shape[0] == 1 and cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: elements of a row must be consecutive")
+        return _single_stride(t, cols)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be consecutive")
+    if t.stride(0) < cols or t.stride(0) * t.element_size() % 16:
+        raise ValueError(f"{name}: row stride {t.stride(0)} must cover a row and be a multiple of 16 bytes")
+    return t.stride(0)
+
+
+def _single_stride(t, cols):
+    step = 16 // t.element_size()
+    return (cols + step - 1) // step * step
+
+
+def _pointer(t, name, index):
+    """Device pointer of t on GPU `index`, 16-byte aligned where it has elements."""
+    p = _on_gpu(t, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name}: is on GPU {t.get_device()}, the call is on GPU {index}")
+    if p % 16:
+        raise ValueError(f"{name}: must start 16-byte aligned")
+    return p
+
+
+def _target(first, name, stream):
+    """(GPU, raw stream, allocation context) of a call whose first operand is given."""
+    _on_gpu(first, name)
+    index = first.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name}: is on GPU {index}, the current GPU is {torch.cuda.current_device()}")
+    if stream is None:
+        return index, torch.cuda.current_stream(index).cuda_stream, contextlib.nullcontext()
+    return index, stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _output(out, name, shape, dtype, allowed, device, alloc):
+    """(out, its dtype, its row stride): a given output checked, or a new one."""
+    if out is None:
+        if dtype not in allowed:
+            raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {dtype}")
+        with alloc:
+            return torch.empty(shape, dtype=dtype, device=device), shape[-1]
+    if out.dtype not in allowed:
+        raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {out.dtype}")
+    if len(shape) == 2:
+        return out, _matrix(out, name, out.dtype, *shape)
+    _layout(out, name, out.dtype, shape)
+    return out, shape[-1]
+
+
+def _groups(offsets, rows, src, n_experts, pairs, n, k, index):
+    _layout(offsets, "offsets", torch.int32, (n_experts + 1,))
+    g = Grouped(n_experts, n, k, pairs, _on_gpu(offsets, "offsets"), None, 0)
+    if offsets.get_device() != index:
+        raise ValueError(f"offsets: is on GPU {offsets.get_device()}, the call is on GPU {index}")
+    if rows is not None:
+        _layout(rows, "rows", torch.int32, (pairs,))
+        # an empty tensor has no pointer; with no pairs nothing is read
+        g.rows, g.src_rows = _on_gpu(rows, "rows") or g.offsets, src
+        if rows.get_device() != index:
+            raise ValueError(f"rows: is on GPU {rows.get_device()}, the call is on GPU {index}")
+    return g
+
+
+def _bank(b, name, dtype):
+    if b.dim() != 3:
+        raise ValueError(f"{name}: expected [experts, out, in], got {tuple(b.shape)}")
+    _layout(b, name, dtype)
+    return b.shape
+
+
+def grouped_mm(a, b, offsets, rows=None, out=None, dtype=None, stream=None):
+    """c[p] = a[rows[p]] @ b[e(p)].T for the pairs p of every expert e.
+
+    a [R, K] bf16 or fp16 (rows may be strided), b [E, N, K] of the same type;
+    rows [P] int32 names the row of a that each pair reads (default: P = R,
+    pair p reads row p; an entry outside [0, R) reads zeros).  Returns c [P, N]
+    in `dtype` (a's type or fp32).  Rows of no group come out as zeros."""
+    _dtype(a, "a", _HALF)
+    E, N, K = _bank(b, "b", a.dtype)
+    lda = _matrix(a, "a", a.dtype, None, K)
+    index, raw, alloc = _target(a, "a", stream)
+    P = a.shape[0] if rows is None else rows.shape[0]
+    g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
+    out, ldc = _output(out, "out", (P, N), dtype or a.dtype, (a.dtype, torch.float32), a.device, alloc)
+    _check(_lib.moe_grouped_mm(ctypes.byref(g), DT[a.dtype], _pointer(a, "a", index), lda, _pointer(b, "b", index),
+                               _pointer(out, "out", index), DT[out.dtype], ldc, raw), "moe_grouped_mm")
+    return out
+
+
+def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
+    """The gradient of grouped_mm with respect to each pair's row of a: da[p] = dc[p] @ b[e(p)].
+
+    dc [P, N], b [E, N, K]; returns da [P, K] in `dtype` (dc's type or fp32).  Where pairs share a row of a,
+    that row's gradient is the sum of theirs."""
+    _dtype(dc, "dc", _HALF)
+    E, N, K = _bank(b, "b", dc.dtype)
+    ldd = _matrix(dc, "dc", dc.dtype, None, N)
+    index, raw, alloc = _target(dc, "dc", stream)
+    P = dc.shape[0]
+    g = _groups(offsets, None, 0, E, P, N, K, index)
+    out, lda = _output(out, "out", (P, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc.device, alloc)
+    _check(_lib.moe_grouped_mm_grad_a(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
+                                      _pointer(b, "b", index), _pointer(out, "out", index), DT[out.dtype], lda, raw),
+           "moe_grouped_mm_grad_a")
+    return out
+
+
+def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=None):
+    """The gradient of grouped_mm with respect to b: db[e] = sum over e's pairs of dc[p].T @ a[rows[p]].
+
+    dc [P, N], a [R, K] of the same type; returns db [E, N, K] in `dtype` (dc's type or fp32), zeros for an
+    expert without pairs."""
+    _dtype(dc, "dc", _HALF)
+    ldd = _matrix(dc, "dc", dc.dtype, None, dc.shape[-1])
+    P, N = dc.shape
+    lda = _matrix(a, "a", dc.dtype, None if rows is not None else P, a.shape[-1])
+    K = a.shape[1]
+    index, raw, alloc = _target(dc, "dc", stream)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets: expected [experts + 1], got {tuple(offsets.shape)}")
+    E = offsets.shape[0] - 1
+    g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
+    out, _ = _output(out, "out", (E, N, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc.device, alloc)
+    _check(_lib.moe_grouped_mm_grad_b(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
+                                      _pointer(a, "a", index), lda, _pointer(out, "out", index), DT[out.dtype], raw),
+           "moe_grouped_mm_grad_b")
+    return out
+
+
+def _code_outputs(shape, codes, scales, device, alloc):
+    with alloc:
+        if codes is None:
+            codes = torch.empty(*shape[:-1], shape[-1] // 2, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.empty(*shape[:-1], shape[-1] // 32, dtype=torch.uint8, device=device)
+    _layout(codes, "codes", torch.uint8, (*shape[:-1], shape[-1] // 2))
+    _layout(scales, "scales", torch.uint8, (*shape[:-1], shape[-1] // 32))
+    return codes, scales
+
+
+def _rows_of(x, name):
+    """x as (rows, cols, row stride): two dimensions with strided rows, or any number of them dense."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name}: expected rows of at least one element, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    if x.dim() == 2:
+        return x.shape[0], cols, _matrix(x, name, x.dtype, None, cols)
+    _layout(x, name)
+    return x.numel() // cols, cols, cols
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """x [.., n] (fp32, bf16 or fp16; n a multiple of 32) as (codes [.., n/2], scales [.., n/32]), both uint8.
+
+    The format is described in include/moe.h (moe_mxfp4_quantize)."""
+    _dtype(x, "x", tuple(DT))
+    rows, cols, ld = _rows_of(x, "x")
+    if cols % 32:
+        raise ValueError(f"x: rows of {cols} elements are not made of blocks of 32")
+    index, raw, alloc = _target(x, "x", stream)
+    codes, scales = _code_outputs(x.shape, codes, scales, x.device, alloc)
+    _check(_lib.moe_mxfp4_quantize(DT[x.dtype], _pointer(x, "x", index), ld, rows, cols,
+                                   _pointer(codes, "codes", index), _on_gpu(scales, "scales"), raw),
+           "moe_mxfp4_quantize")
+    return codes, scales
+
+
+def _format(codes, scales, c_name, s_name):
+    _layout(codes, c_name, torch.uint8)
+    if codes.dim() < 1 or codes.shape[-1] % 16 or codes.shape[-1] < 16:
+        raise ValueError(f"{c_name}: expected rows of a multiple of 16 bytes, got {tuple(codes.shape)}")
+    _layout(scales, s_name, torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16))
+    return codes.shape[-1] * 2
+
+
+def mxfp4_dequantize(codes, scales, out=None, dtype=torch.float32, stream=None):
+    """The values that codes [.., n/2] and scales [.., n/32] stand for, [.., n] in `dtype`."""
+    cols = _format(codes, scales, "codes", "scales")
+    shape = (*codes.shape[:-1], cols)
+    index, raw, alloc = _target(codes, "codes", stream)
+    out, ld = _output(out, "out", shape, dtype, tuple(DT), codes.device, alloc)
+    _check(_lib.moe_mxfp4_dequantize(_pointer(codes, "codes", index), _on_gpu(scales, "scales"),
+                                     codes.numel() * 2 // cols, cols, DT[out.dtype], _pointer(out, "out", index), ld,
+                                     raw), "moe_mxfp4_dequantize")
+    return out
+
+
+def mxfp4_grouped_mm(a_codes, a_scales, b_codes, b_scales, offsets, rows=None, out=None, dtype=torch.bfloat16,
+                     stream=None):
+    """grouped_mm with both operands in the four-bit format (a [R, K], b [E, N, K]); returns c [P, N] in `dtype`
+    (bf16 or fp32)."""
+    K = _format(a_codes, a_scales, "a_codes", "a_scales")
+    if a_codes.dim() != 2:
+        raise ValueError(f"a_codes: expected two dimensions, got {tuple(a_codes.shape)}")
+    E, N, half = _bank(b_codes, "b_codes", torch.uint8)
+    if _format(b_codes, b_scales, "b_codes", "b_scales") != K:
+        raise ValueError(f"b_codes: rows of {2 * half} elements, a has {K}")
+    index, raw, alloc = _target(a_codes, "a_codes", stream)
+    R = a_codes.shape[0]
+    P = R if rows is None else rows.shape[0]
+    g = _groups(offsets, rows, R, E, P, N, K, index)
+    out, ldc = _output(out, "out", (P, N), dtype, (torch.bfloat16, torch.float32), a_codes.device, alloc)
+    _check(_lib.moe_mxfp4_grouped_mm(ctypes.byref(g), _pointer(a_codes, "a_codes", index),
+                                     _on_gpu(a_scales, "a_scales"), _pointer(b_codes, "b_codes", index),
+                                     _on_gpu(b_scales, "b_scales"), _pointer(out, "out", index), DT[out.dtype], ldc,
+                                     raw), "moe_mxfp4_grouped_mm")
+    return out
+
+
+def _gate_up(gu):
+    _dtype(gu, "gu", tuple(DT))
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError(f"gu: expected [rows, 2 * ffn], got {tuple(gu.shape)}")
+    return gu.shape[0], gu.shape[1] // 2, _matrix(gu, "gu", gu.dtype, None, gu.shape[1])
+
+
+def swiglu(gu, out=None, stream=None):
+    """h = silu(gate) * up of gu [rows, 2 F] = [gate | up] (fp32, bf16 or fp16), [rows, F] of the same type."""
+    rows, ffn, ldg = _gate_up(gu)
+    index, raw, alloc = _target(gu, "gu", stream)
+    out, ldh = _output(out, "out", (rows, ffn), gu.dtype, (gu.dtype,), gu.device, alloc)
+    _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(out, "out", index), ldh,
+                           raw), "moe_swiglu")
+    return out
+
+
+def swiglu_mxfp4(gu, codes=None, scales=None, stream=None):
+    """swiglu with its result in the four-bit format: (codes [rows, F/2], scales [rows, F/32])."""
+    rows, ffn, ldg = _gate_up(gu)
+    if ffn % 32:
+        raise ValueError(f"gu: rows of {ffn} outputs are not made of blocks of 32")
+    index, raw, alloc = _target(gu, "gu", stream)
+    codes, scales = _code_outputs((rows, ffn), codes, scales, gu.device, alloc)
+    _check(_lib.moe_swiglu_mxfp4(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn,
+                                 _pointer(codes, "codes", index), _on_gpu(scales, "scales"), raw), "moe_swiglu_mxfp4")
+    return codes, scales
+
+
+def swiglu_grad(dh, gu, out=None, stream=None):
+    """The gradient of swiglu: dgu [rows, 2 F] = [dgate | dup] from dh [rows, F] and the gu of the forward call."""
+    rows, ffn, ldg = _gate_up(gu)
+    ldd = _matrix(dh, "dh", gu.dtype, rows, ffn)
+    index, raw, alloc = _target(gu, "gu", stream)
+    out, ldo = _output(out, "out", (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu.device, alloc)
+    _check(_lib.moe_swiglu_grad(DT[gu.dtype], _pointer(dh, "dh", index), ldd, _pointer(gu, "gu", index), ldg, rows,
+                                ffn, _pointer(out, "out", index), ldo, raw), "moe_swiglu_grad")
+    return out

@@ -1,0 +1,564 @@
+"""The expert operators (grouped products and their gradients, the four-bit
+format and its product, SwiGLU and its gradient) on the GPU, against plain
+64-bit computations.
+
+Tolerances.  A product's sum is held in fp32 and rounded once.  Its terms are
+exact in fp32 (at most 11 + 11 significant bits, or 3 + 3 and powers of two),
+so with D terms of absolute sum S the sum is off by at most D 2^-24 S when
+every addition rounds to nearest; D 2^-23 S allows for additions that
+truncate.  The output type adds half a unit of the last place: 2^-8 |y| for
+bf16, 2^-11 |y| + 2^-25 for fp16, 2^-24 |y| for fp32.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+BF16, FP16, FP32, FP64 = torch.bfloat16, torch.float16, torch.float32, torch.float64
+UNIT = {BF16: 2.0**-8, FP16: 2.0**-11, FP32: 2.0**-24}
+TINY = {BF16: 2.0**-130, FP16: 2.0**-25, FP32: 2.0**-149}
+
+
+def _qr():
+    import quantized_routed_moe_amd as qr
+    return qr
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def offsets_of(sizes, head=0):
+    o = [head]
+    for n in sizes:
+        o.append(o[-1] + n)
+    return o
+
+
+def close(got, want, mag, depth, where=""):
+    """got within the bound above of the 64-bit want; mag: the sum of the terms' magnitudes."""
+    got, u = got.cpu(), UNIT[got.dtype]
+    err = (got.to(FP64) - want).abs()
+    tol = u * want.abs() * (1 + 2.0**-10) + depth * 2.0**-23 * mag * (1 + u) + TINY[got.dtype]
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{where}: {int(bad.sum())} of {bad.numel()} off, worst {float((err - tol).max()):.3e} past its bound"
+
+
+def grouped_ref(a, b, offsets, rows, pairs):
+    """(c, sum of magnitudes) in 64 bits."""
+    a, b = a.to(FP64), b.to(FP64)
+    if rows is not None:
+        ok = (rows >= 0) & (rows < a.shape[0])
+        a = a[rows.long().clamp(0, a.shape[0] - 1)] * ok[:, None]
+    c = torch.zeros(pairs, b.shape[1], dtype=FP64)
+    m = torch.zeros_like(c)
+    for e in range(b.shape[0]):
+        i, j = offsets[e], offsets[e + 1]
+        c[i:j] = a[i:j] @ b[e].t()
+        m[i:j] = a[i:j].abs() @ b[e].abs().t()
+    return c, m
+
+
+def dev(offsets):
+    return torch.tensor(offsets, dtype=torch.int32, device="cuda")
+
+
+# group sizes (rows before the first group, rows past the last one): empty groups, one row, odd sizes, whole tiles,
+# groups longer than any tile, many groups, a single group, rows of no group
+GROUPS = {
+    "one_row": ([1], 0, 0),
+    "one_of_many": ([0, 0, 1, 0], 0, 0),
+    "ragged": ([3, 0, 17, 1, 64, 0, 130, 5], 0, 0),
+    "whole_tiles": ([128, 256, 64], 0, 0),
+    "long": ([700, 0, 333], 0, 0),
+    "many": ([i % 4 for i in range(300)], 0, 0),
+    "most_groups": ([1 if i % 7 == 0 else 0 for i in range(1024)], 0, 0),
+    "rows_outside": ([5, 0, 40], 3, 9),
+    "all_outside": ([0, 0], 0, 33),
+    "singles": ([1] * 37, 0, 0),
+}
+WIDTHS = [(8, 8), (72, 40), (136, 264), (264, 520), (128, 1032)]
+
+
+def make_case(name, n, k, dtype, gather, seed, pad=0):
+    sizes, head, tail = GROUPS[name]
+    g = gen(seed)
+    offsets = offsets_of(sizes, head)
+    pairs = offsets[-1] + tail
+    src = 29 if gather else pairs
+    a = torch.randn(src, k + pad, generator=g).to(dtype)
+    b = (torch.randn(len(sizes), n, k, generator=g) / k**0.5).to(dtype)
+    rows = torch.randint(0, src, (pairs,), generator=g, dtype=torch.int32) if gather else None
+    return a, b, offsets, rows, pairs
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("n,k", WIDTHS)
+@pytest.mark.parametrize("gather", [False, True])
+def test_forward(name, n, k, gather):
+    qr = _qr()
+    for dtype, out in ((BF16, BF16), (FP16, FP32)):
+        a, b, offsets, rows, pairs = make_case(name, n, k, dtype, gather, seed=n + k)
+        c = qr.grouped_mm(a.cuda(), b.cuda(), dev(offsets), rows=cuda(rows), dtype=out)
+        assert c.dtype == out and c.shape == (pairs, n)
+        want, mag = grouped_ref(a, b, offsets, rows, pairs)
+        close(c, want, mag, k, f"{name} {dtype} -> {out}")
+
+
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("n,k", WIDTHS)
+def test_grad_a(name, n, k):
+    qr = _qr()
+    for dtype, out in ((BF16, FP32), (FP16, FP16)):
+        dc, b, offsets, _, pairs = make_case(name, k, n, dtype, False, seed=2 * n + k)  # dc [P, n]
+        b = b.transpose(1, 2).contiguous()  # [E, n, k]
+        da = qr.grouped_mm_grad_a(dc.cuda(), b.cuda(), dev(offsets), dtype=out)
+        want, mag = grouped_ref(dc, b.transpose(1, 2), offsets, None, pairs)
+        close(da, want, mag, n, f"{name} {dtype} -> {out}")
+
+
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("n,k", WIDTHS)
+@pytest.mark.parametrize("gather", [False, True])
+def test_grad_b(name, n, k, gather):
+    qr = _qr()
+    if len(GROUPS[name][0]) * n * k > 3e7:
+        n, k = 40, 72  # many experts: narrow matrices
+    for dtype, out in ((BF16, BF16), (FP16, FP32)):
+        a, _, offsets, rows, pairs = make_case(name, n, k, dtype, gather, seed=3 * n + k)
+        dc = torch.randn(pairs, n, generator=gen(n * k)).to(dtype)
+        db = qr.grouped_mm_grad_b(dc.cuda(), a.cuda(), dev(offsets), rows=cuda(rows), dtype=out).cpu()
+        ra = (a if rows is None else a[rows.long()]).to(FP64)
+        for e in range(len(offsets) - 1):
+            i, j = offsets[e], offsets[e + 1]
+            if j == i:
+                assert not db[e].any()
+                continue
+            d = dc[i:j].to(FP64)
+            close(db[e], d.t() @ ra[i:j], d.abs().t() @ ra[i:j].abs(), j - i, f"{name} {dtype} expert {e}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_strided_operands_and_padding_are_not_read(dtype):
+    """Rows of a, dc and of the outputs may be strided; what lies between them, NaN here, is neither read into a
+    result nor written."""
+    qr = _qr()
+    n, k, pad = 136, 264, 24
+    a, b, offsets, _, pairs = make_case("ragged", n, k, dtype, False, 5, pad=pad)
+    a[:, k:] = float("nan")
+    wide = torch.full((pairs, n + pad), float("nan"), dtype=dtype, device="cuda")
+    qr.grouped_mm(a.cuda()[:, :k], b.cuda(), dev(offsets), out=wide[:, :n])
+    want, mag = grouped_ref(a[:, :k], b, offsets, None, pairs)
+    close(wide[:, :n], want, mag, k, "c")
+    assert wide[:, n:].isnan().all()
+    dc = torch.randn(pairs, n + pad, generator=gen(6)).to(dtype)
+    dc[:, n:] = float("nan")
+    d = dc[:, :n].to(FP64)
+    wide = torch.full((pairs, k + pad), float("nan"), dtype=dtype, device="cuda")
+    qr.grouped_mm_grad_a(dc.cuda()[:, :n], b.cuda(), dev(offsets), out=wide[:, :k])
+    want, mag = grouped_ref(dc[:, :n], b.transpose(1, 2), offsets, None, pairs)
+    close(wide[:, :k], want, mag, n, "da")
+    assert wide[:, k:].isnan().all()
+    db = qr.grouped_mm_grad_b(dc.cuda()[:, :n], a.cuda()[:, :k], dev(offsets), dtype=FP32)
+    for e in range(len(offsets) - 1):
+        i, j = offsets[e], offsets[e + 1]
+        x, y = d[i:j], a[i:j, :k].to(FP64)
+        close(db[e], x.t() @ y, x.abs().t() @ y.abs(), max(j - i, 1), f"db {e}")
+
+
+def test_not_finite_values_stay_in_their_rows():
+    """NaN and infinities in rows of no group, in other rows of the group and in experts without pairs reach no
+    other row's result, and reach their own."""
+    qr = _qr()
+    n, k = 72, 104
+    a, b, offsets, _, pairs = make_case("rows_outside", n, k, BF16, False, 7)
+    want, mag = grouped_ref(a, b, offsets, None, pairs)
+    bad = [0, 1, 4, 20, pairs - 1]
+    a[bad] = float("nan")
+    a[20] = float("inf")
+    b[1] = float("nan")  # the empty group's matrix
+    c = qr.grouped_mm(a.cuda(), b.cuda(), dev(offsets)).cpu()
+    fine = torch.ones(pairs, dtype=torch.bool)
+    fine[bad] = False
+    close(c[fine], want[fine], mag[fine], k, "rows of finite values")
+    assert c[4].isnan().all() and not c[20].isfinite().any()
+    assert not c[[0, 1, pairs - 1]].any()  # rows of no group
+
+
+def test_gathered_rows_out_of_range_read_zeros():
+    qr = _qr()
+    n, k = 72, 104
+    for name in ("ragged", "singles"):
+        a, b, offsets, rows, pairs = make_case(name, n, k, BF16, True, 8)
+        rows[::5] = torch.tensor([-1, 29, 2**31 - 1, -(2**31), 1000], dtype=torch.int32).repeat(pairs)[: len(rows[::5])]
+        c = qr.grouped_mm(a.cuda(), b.cuda(), dev(offsets), rows=rows.cuda())
+        want, mag = grouped_ref(a, b, offsets, rows, pairs)
+        close(c, want, mag, k, "c")
+        dc = torch.randn(pairs, n, generator=gen(9)).to(BF16)
+        db = qr.grouped_mm_grad_b(dc.cuda(), a.cuda(), dev(offsets), rows=rows.cuda(), dtype=FP32)
+        ok = (rows >= 0) & (rows < 29)
+        ra = a.to(FP64)[rows.long().clamp(0, 28)] * ok[:, None]
+        for e in range(len(offsets) - 1):
+            i, j = offsets[e], offsets[e + 1]
+            x = dc[i:j].to(FP64)
+            close(db[e], x.t() @ ra[i:j], x.abs().t() @ ra[i:j].abs(), max(j - i, 1), f"db {e}")
+
+
+def test_offsets_are_clamped():
+    """Offsets that run past the pairs or backwards leave the buffers alone; groups that lie inside come out right."""
+    qr = _qr()
+    n, k, pairs = 40, 72, 50
+    a = torch.randn(pairs, k, generator=gen(10)).to(BF16)
+    b = torch.randn(4, n, k, generator=gen(11)).to(BF16)
+    c = qr.grouped_mm(a.cuda(), b.cuda(), dev([-7, 20, 20, 45, 900]))
+    want, mag = grouped_ref(a, b, [0, 20, 20, 45, 50], None, pairs)
+    close(c, want, mag, k, "clamped")
+    c = qr.grouped_mm(a.cuda(), b.cuda(), dev([0, 30, 10, 10, 50]))
+    assert c.shape == (pairs, n)
+    qr.grouped_mm_grad_b(c, a.cuda(), dev([0, 30, 10, 10, 50]))
+    torch.cuda.synchronize()
+
+
+def test_no_pairs():
+    qr = _qr()
+    a, b = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.randn(3, 40, 64, device="cuda").to(BF16)
+    o = dev([0, 0, 0, 0])
+    assert qr.grouped_mm(a, b, o).shape == (0, 40)
+    assert qr.grouped_mm_grad_a(torch.empty(0, 40, dtype=BF16, device="cuda"), b, o).shape == (0, 64)
+    db = qr.grouped_mm_grad_b(torch.empty(0, 40, dtype=BF16, device="cuda"), a, o)
+    assert db.shape == (3, 40, 64) and not db.any()
+    assert qr.swiglu(torch.empty(0, 64, device="cuda")).shape == (0, 32)
+    codes, scales = qr.mxfp4_quantize(torch.empty(0, 64, device="cuda"))
+    assert codes.shape == (0, 32) and qr.mxfp4_dequantize(codes, scales).shape == (0, 64)
+    bc, bs = qr.mxfp4_quantize(b)
+    assert qr.mxfp4_grouped_mm(codes, scales, bc, bs, o).shape == (0, 40)
+    # pairs that all read from an empty source
+    rows = torch.zeros(5, dtype=torch.int32, device="cuda")
+    assert not qr.grouped_mm(a, b, dev([0, 2, 2, 5]), rows=rows).any()
+
+
+def test_a_bank_past_32_bits():
+    """The last expert of a bank of more than 2^32 bytes and elements past 2^31: offsets that 32 bits do not hold."""
+    qr = _qr()
+    E, n, k = 132, 4096, 4096
+    b = torch.zeros(E, n, k, dtype=BF16, device="cuda")
+    assert b.numel() > 2**31
+    last = (torch.randn(n, k, generator=gen(12)) / 64).to(BF16)
+    b[-1] = last.cuda()
+    for pairs in (2, 200):  # a few rows, and a tile and more
+        a = torch.randn(pairs, k, generator=gen(13)).to(BF16)
+        o = dev([0] * E + [pairs])
+        c = qr.grouped_mm(a.cuda(), b, o, dtype=FP32)
+        x, y = a.to(FP64), last.to(FP64)
+        close(c, x @ y.t(), x.abs() @ y.abs().t(), k, f"c of {pairs}")
+        da = qr.grouped_mm_grad_a(a.cuda(), b, o, dtype=FP32)
+        close(da, x @ y, x.abs() @ y.abs(), n, f"da of {pairs}")
+    dc = torch.randn(3, n, generator=gen(14)).to(BF16)
+    qr.grouped_mm_grad_b(dc.cuda(), a[:3].cuda(), dev([0] * E + [3]), out=b)
+    assert not b[:-1].any()
+    x, y = dc.to(FP64), a[:3].to(FP64)
+    close(b[-1], x.t() @ y, x.abs().t() @ y.abs(), 3, "db")
+
+
+def test_gradients_against_differences():
+    """The product is linear in a and in b, so a central difference of its fp32 output along a direction is the
+    gradient's product with it, up to the sums' rounding.  Inputs are multiples of 1/4 and the step is 1/4: exact."""
+    qr = _qr()
+    sizes = [3, 0, 70, 1, 150]
+    offsets, n, k, h = offsets_of(sizes), 72, 136, 0.25
+    g = gen(15)
+    pairs = offsets[-1]
+
+    def grid(*shape):
+        return (torch.randint(-8, 9, shape, generator=g) / 4).to(BF16).cuda()
+
+    a, b, dc, o = grid(pairs, k), grid(len(sizes), n, k), grid(pairs, n), dev(offsets)
+    da = qr.grouped_mm_grad_a(dc, b, o, dtype=FP32).double()
+    db = qr.grouped_mm_grad_b(dc, a, o, dtype=FP32).double()
+
+    def loss(x, y):
+        return float((qr.grouped_mm(x, y, o, dtype=FP32).double() * dc.double()).sum())
+
+    for seed in range(3):
+        va = (torch.randint(0, 2, (pairs, k), generator=g) * 2 - 1).to(BF16).cuda()
+        vb = (torch.randint(0, 2, (len(sizes), n, k), generator=g) * 2 - 1).to(BF16).cuda()
+        for num, ana in (((loss(a + h * va, b) - loss(a - h * va, b)) / (2 * h), float((da * va.double()).sum())),
+                         ((loss(a, b + h * vb) - loss(a, b - h * vb)) / (2 * h), float((db * vb.double()).sum()))):
+            # products of multiples of 1/16 below 2^24: every sum here is exact
+            assert num == ana
+
+
+# -------------------------------------------------------- four-bit format
+VALUES = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def quantize_ref(x):
+    """(codes, scales) by comparing with the midpoints of the representable values, in 64 bits."""
+    b = x.to(FP64).reshape(-1, 32)
+    amax = b.abs().amax(1)
+    bad = ~amax.isfinite()  # NaN or infinity in the block
+    _, e = torch.frexp(torch.where(bad, torch.zeros_like(amax), amax))
+    s = torch.where(amax > 0, (e - 1 - 2 + 127).clamp(0, 254), torch.zeros_like(e))
+    m = torch.where(bad[:, None], torch.zeros_like(b), b.abs() / torch.exp2(s.to(FP64) - 127)[:, None])
+    v = torch.tensor(VALUES, dtype=FP64)
+    mid = (v[1:] + v[:-1]) / 2
+    lo, hi = torch.bucketize(m, mid, right=False), torch.bucketize(m, mid, right=True)
+    code = torch.where(lo % 2 == 0, lo, hi) | (torch.signbit(x.reshape(-1, 32)).int() << 3)
+    s = torch.where(bad, torch.full_like(s, 255), s)
+    code = code.reshape(*x.shape[:-1], -1, 2)
+    return (code[..., 0] | code[..., 1] << 4).to(torch.uint8), s.reshape(*x.shape[:-1], -1).to(torch.uint8), bad
+
+
+def values_ref(codes, scales):
+    v = torch.tensor(VALUES + [-x for x in VALUES], dtype=FP64)
+    x = torch.stack([v[(codes & 15).long()], v[(codes >> 4).long()]], -1).reshape(*scales.shape, 32)
+    s = torch.exp2(scales.to(FP64) - 127)
+    s[scales == 255] = float("nan")
+    return (x * s[..., None]).reshape(*codes.shape[:-1], -1)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 64), (7, 96), (130, 352), (5, 4096), (1000, 32)])
+def test_quantize_is_exact(dtype, rows, cols):
+    qr = _qr()
+    g = gen(rows + cols)
+    x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-12, 12, (rows, 1), generator=g).float())
+    x = x.to(dtype)
+    codes, scales = qr.mxfp4_quantize(x.cuda())
+    wc, ws, _ = quantize_ref(x)
+    assert torch.equal(codes.cpu(), wc) and torch.equal(scales.cpu(), ws)
+    for out in (FP32, BF16, FP16):
+        y = qr.mxfp4_dequantize(codes, scales, dtype=out).cpu()
+        assert torch.equal(y, values_ref(wc, ws).to(out))
+
+
+def test_quantize_ties_extremes_and_not_finite():
+    """Every tie and its neighbours at scales from the smallest to the largest, zeros of both signs, subnormals,
+    values past 6, blocks with NaN or infinity; the block beside stays as it is."""
+    qr = _qr()
+    pts = [0.0, -0.0]
+    for i in range(7):
+        m = (VALUES[i] + VALUES[i + 1]) / 2
+        pts += [m, -m, VALUES[i + 1], -VALUES[i + 1], m * (1 + 2.0**-20), m * (1 - 2.0**-20)]
+    pts += [7.0, -7.0, 7.999, 5.0000005]
+    pts = torch.tensor(pts, dtype=FP64)
+    blocks = []
+    for e in (-149, -140, -130, -127, -126, -125, -60, -1, 0, 1, 60, 124, 125):
+        for i in range(0, len(pts), 31):
+            blk = torch.zeros(32, dtype=FP64)
+            part = pts[i : i + 31]
+            blk[: len(part)] = part
+            blk[31] = 4.0  # fixes the scale at 2^e unless a larger value does not fit
+            blocks.append((blk * 2.0**e).to(FP32))
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        blk = torch.ones(32)
+        blk[17] = bad
+        blocks += [blk, torch.arange(32.0)]
+    blocks.append(torch.zeros(32))
+    blocks.append(torch.full((32,), torch.finfo(FP32).max))
+    x = torch.stack(blocks)
+    codes, scales = qr.mxfp4_quantize(x.cuda())
+    wc, ws, bad = quantize_ref(x)
+    codes, scales = codes.cpu(), scales.cpu()
+    assert torch.equal(scales, ws)
+    assert torch.equal(codes[~bad], wc[~bad])
+    y = qr.mxfp4_dequantize(codes.cuda(), scales.cuda()).cpu()
+    assert y[bad].isnan().all() and torch.equal(y[~bad], values_ref(wc, ws)[~bad].to(FP32))
+
+
+def test_quantize_strided_rows_and_many_dimensions():
+    qr = _qr()
+    x = torch.randn(9, 160, generator=gen(16))
+    codes, scales = qr.mxfp4_quantize(x.cuda()[:, :96])
+    wc, ws, _ = quantize_ref(x[:, :96])
+    assert torch.equal(codes.cpu(), wc) and torch.equal(scales.cpu(), ws)
+    wide = torch.full((9, 128), 7.0, device="cuda")
+    qr.mxfp4_dequantize(codes, scales, out=wide[:, :96])
+    assert torch.equal(wide[:, :96].cpu(), values_ref(wc, ws).to(FP32)) and (wide[:, 96:] == 7).all()
+    x = torch.randn(3, 5, 64, generator=gen(17)).to(BF16)
+    codes, scales = qr.mxfp4_quantize(x.cuda())
+    assert codes.shape == (3, 5, 32) and scales.shape == (3, 5, 2)
+    wc, ws, _ = quantize_ref(x)
+    assert torch.equal(codes.cpu(), wc) and torch.equal(scales.cpu(), ws)
+
+
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("n,k", [(8, 32), (72, 96), (136, 224), (264, 544), (128, 1024)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_mxfp4_product(name, n, k, gather):
+    qr = _qr()
+    sizes, head, tail = GROUPS[name]
+    offsets = offsets_of(sizes, head)
+    pairs, g = offsets[-1] + tail, gen(n + k)
+    src = 29 if gather else pairs
+    ac = torch.randint(0, 256, (src, k // 2), generator=g, dtype=torch.uint8)
+    as_ = torch.randint(118, 132, (src, k // 32), generator=g, dtype=torch.uint8)
+    bc = torch.randint(0, 256, (len(sizes), n, k // 2), generator=g, dtype=torch.uint8)
+    bs = torch.randint(118, 132, (len(sizes), n, k // 32), generator=g, dtype=torch.uint8)
+    rows = torch.randint(0, src, (pairs,), generator=g, dtype=torch.int32) if gather else None
+    want, mag = grouped_ref(values_ref(ac, as_), values_ref(bc, bs), offsets, rows, pairs)
+    for out in (BF16, FP32):
+        c = qr.mxfp4_grouped_mm(ac.cuda(), as_.cuda(), bc.cuda(), bs.cuda(), dev(offsets), rows=cuda(rows), dtype=out)
+        close(c, want, mag, k, f"{name} {out}")
+
+
+@pytest.mark.parametrize("pairs", [1, 5, 200])
+def test_mxfp4_product_not_a_number_and_extreme_scales(pairs):
+    """A block of scale 255 makes its row's (its column's) results NaN and no others; the smallest and the largest
+    scales meet without under- or overflow of the product."""
+    qr = _qr()
+    n, k = 72, 160
+    x, w = torch.randn(pairs, k, generator=gen(18)), torch.randn(2, n, k, generator=gen(19))
+    (ac, as_), (bc, bs) = qr.mxfp4_quantize(x.cuda()), qr.mxfp4_quantize(w.cuda())
+    o = dev([0, 0, pairs])
+    want, mag = grouped_ref(values_ref(ac.cpu(), as_.cpu()), values_ref(bc.cpu(), bs.cpu()), [0, 0, pairs], None, pairs)
+    bad_a, bad_b = as_.clone(), bs.clone()
+    bad_a[0, 3], bad_b[1, 5, 4], bad_b[0] = 255, 255, 255
+    c = qr.mxfp4_grouped_mm(ac, bad_a, bc, bad_b, o, dtype=FP32).cpu()
+    assert c[0].isnan().all() and c[:, 5].isnan().all()
+    keep = [i for i in range(n) if i != 5]
+    close(c[1:, keep], want[1:, keep], mag[1:, keep], k, "others")
+    low, high = torch.zeros_like(as_), torch.full_like(bs, 254)
+    v = values_ref(ac.cpu(), torch.full_like(as_, 127).cpu()), values_ref(bc.cpu(), torch.full_like(bs, 127).cpu())
+    want, mag = grouped_ref(*v, [0, 0, pairs], None, pairs)
+    close(qr.mxfp4_grouped_mm(ac, low, bc, high, o, dtype=FP32), want, mag, k, "scales 0 and 254")
+
+
+# ------------------------------------------------------------------ swiglu
+def swiglu_ref(gu):
+    f = gu.shape[1] // 2
+    g, u = gu[:, :f].to(FP64), gu[:, f:].to(FP64)
+    s = torch.sigmoid(g)
+    return g, u, s
+
+
+# exp and the division are good to a few units of 2^-24 and the argument's rounding adds |g| 2^-24 of e^-g, of which
+# the sigmoid keeps at most the same share; the formula's further products round once each
+def swiglu_tol(want, g, dtype, terms):
+    return UNIT[dtype] * want.abs() * 1.001 + (12 + 2 * g.abs()) * 2.0**-23 * terms + TINY[dtype] + 2.0**-120
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("rows,ffn", [(1, 8), (3, 40), (65, 136), (192, 2048), (1000, 24)])
+def test_swiglu_and_gradient(dtype, rows, ffn):
+    qr = _qr()
+    gu = (torch.randn(rows, 2 * ffn, generator=gen(rows + ffn)) * 4).to(dtype)
+    dh = torch.randn(rows, ffn, generator=gen(rows * ffn)).to(dtype)
+    g, u, s = swiglu_ref(gu)
+    h = qr.swiglu(gu.cuda()).cpu()
+    want = g * s * u
+    assert ((h.to(FP64) - want).abs() <= swiglu_tol(want, g, dtype, want.abs())).all()
+    dgu = qr.swiglu_grad(dh.cuda(), gu.cuda()).cpu().to(FP64)
+    d = dh.to(FP64)
+    du, dg = d * g * s, d * u * s * (1 + g * (1 - s))
+    assert ((dgu[:, ffn:] - du).abs() <= swiglu_tol(du, g, dtype, du.abs())).all()
+    terms = d.abs() * u.abs() * s * (1 + g.abs())  # 1 + g (1 - s) cancels for negative gates
+    assert ((dgu[:, :ffn] - dg).abs() <= swiglu_tol(dg, g, dtype, terms)).all()
+
+
+def test_swiglu_gradient_against_differences():
+    """Central differences of the 64-bit formula with step 2^-12: the third derivative of silu is below 1, so they
+    are within h^2 / 6 of the gradient (times dh and the other factor)."""
+    qr = _qr()
+    gu = torch.randn(20, 128, generator=gen(20)) * 3
+    dh = torch.randn(20, 64, generator=gen(21))
+    dgu = qr.swiglu_grad(dh.cuda(), gu.cuda()).cpu().to(FP64)
+    h = 2.0**-12
+
+    def f(x):
+        g, u, s = swiglu_ref(x)
+        return g * s * u * dh.to(FP64)
+
+    x = gu.to(FP64)
+    for half in range(2):
+        v = torch.zeros_like(x)
+        v[:, 64 * half : 64 * half + 64] = h
+        num = (f(x + v) - f(x - v)) / (2 * h)
+        other = x[:, :64] if half else x[:, 64:]
+        tol = (h * h / 6 + 40 * 2.0**-23) * dh.abs().to(FP64) * (other.abs() + 1) * (1 + x[:, :64].abs()) + 1e-9
+        assert ((dgu[:, 64 * half : 64 * half + 64] - num).abs() <= tol).all()
+
+
+def test_swiglu_extreme_gates_and_strides():
+    qr = _qr()
+    gate = [0.0, -0.0, 88.0, -88.0, 100.0, -100.0, 1e4, -1e4]
+    gu = torch.tensor([gate + [2.0] * 8])
+    h = qr.swiglu(gu.cuda()).cpu()
+    g, u, s = swiglu_ref(gu)
+    assert ((h.to(FP64) - g * s * u).abs() <= 2.0**-20 * (g * s * u).abs() + 2.0**-120).all()
+    dgu = qr.swiglu_grad(torch.ones(1, 8).cuda(), gu.cuda()).cpu()
+    assert dgu.isfinite().all()
+    want = torch.cat([u * s * (1 + g * (1 - s)), g * s], 1)
+    assert ((dgu.to(FP64) - want).abs() <= 2.0**-18 * want.abs() + 1e-30).all()
+    # strided rows in and out; NaN in between stays there
+    wide = torch.full((5, 2 * 24 + 8), float("nan"), dtype=BF16)
+    wide[:, :48] = torch.randn(5, 48, generator=gen(22)).to(BF16)
+    out = torch.full((5, 40), float("nan"), dtype=BF16, device="cuda")
+    qr.swiglu(wide.cuda()[:, :48], out=out[:, :24])
+    assert out[:, :24].isfinite().all() and out[:, 24:].isnan().all()
+    assert torch.equal(out[:, :24], qr.swiglu(wide.cuda()[:, :48].contiguous()))
+    grad = torch.full((5, 56), float("nan"), dtype=BF16, device="cuda")
+    dh = torch.randn(5, 32, generator=gen(23)).to(BF16).cuda()[:, :24]
+    qr.swiglu_grad(dh, wide.cuda()[:, :48], out=grad[:, :48])
+    assert grad[:, 48:].isnan().all()
+    assert torch.equal(grad[:, :48], qr.swiglu_grad(dh.contiguous(), wide.cuda()[:, :48].contiguous()))
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("rows,ffn", [(1, 32), (7, 96), (130, 2048)])
+def test_swiglu_to_four_bits(dtype, rows, ffn):
+    """The four-bit result is the quantisation of the activation in fp32: it equals that of swiglu's fp32 output."""
+    qr = _qr()
+    gu = (torch.randn(rows, 2 * ffn, generator=gen(rows + ffn)) * 3).to(dtype)
+    codes, scales = qr.swiglu_mxfp4(gu.cuda())
+    wc, ws = qr.mxfp4_quantize(qr.swiglu(gu.float().cuda()))
+    assert torch.equal(codes, wc) and torch.equal(scales, ws)
+
+
+# ----------------------------------------------------------- calling them
+def test_other_streams_graphs_and_repeated_calls():
+    """A call on a side stream, the same call captured into a graph and replayed with eager work between, and
+    repeated calls give the same bits."""
+    qr = _qr()
+    n, k = 264, 544
+    a, b, offsets, rows, pairs = make_case("ragged", n, k, BF16, True, 24)
+    a, b, rows, o = a.cuda(), b.cuda(), rows.cuda(), dev(offsets)
+    bq = qr.mxfp4_quantize(b)
+    gu = torch.randn(pairs, 256, device="cuda").to(BF16)
+
+    def chain(stream=None):
+        c = qr.grouped_mm(a, b, o, rows=rows, stream=stream)
+        da = qr.grouped_mm_grad_a(c, b, o, stream=stream)
+        db = qr.grouped_mm_grad_b(c, a, o, rows=rows, stream=stream)
+        q = qr.mxfp4_quantize(a, stream=stream)
+        c4 = qr.mxfp4_grouped_mm(*q, *bq, o, rows=rows, stream=stream)
+        h = qr.swiglu(gu, stream=stream)
+        dg = qr.swiglu_grad(h, gu, stream=stream)
+        h4 = qr.mxfp4_dequantize(*qr.swiglu_mxfp4(gu, stream=stream), stream=stream)
+        return [c, da, db, *q, c4, h, dg, h4]
+
+    want = chain()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = chain(side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for i in range(4):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want)), f"replay {i}"
+        again = chain()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(again, want)), f"eager call {i}"
