@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libqrmoe.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "pack.hip", "route.hip", "expert_vec.hip", "decode.hip", "expert_mfma.hip",
-           "expert_ops.cpp", "grouped_mm.hip", "mxfp4.hip", "swiglu.hip"]
+           "expert_ops.cpp", "grouped_mm.hip", "grouped_vec.hip", "mxfp4.hip", "swiglu.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # -ffp-contract=off: floating-point operations round exactly as written (fused
 # multiply-adds only where the source asks for one), so every kernel that

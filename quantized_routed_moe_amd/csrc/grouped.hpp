@@ -30,12 +30,14 @@ struct GroupedArgs {
     int32_t depth;             // contraction length, elements (not grad_b)
     void *out;
     int64_t out_ld;            // elements
+    int32_t sweep;             // column tiles of one workgroup (few rows an expert)
     int32_t n_tiles, m_tiles;  // column tiles; row tiles per expert (grad_b only)
 };
 
 // moe_status of a HIP result (recorded for moe_last_hip_error; api.cpp)
 int status_of(hipError_t e);
 
+hipError_t launch_grouped_vec(GroupedArgs a, Elt elt, bool f32_out, hipStream_t s);
 hipError_t launch_grouped_mm(const GroupedArgs &a, Elt elt, bool f32_out, hipStream_t s);
 hipError_t launch_grouped_grad_a(const GroupedArgs &a, Elt elt, bool f32_out, hipStream_t s);
 hipError_t launch_grouped_grad_b(const GroupedArgs &a, Elt elt, bool f32_out, hipStream_t s);

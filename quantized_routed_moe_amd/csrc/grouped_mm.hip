@@ -364,6 +364,8 @@ __global__ __launch_bounds__(WM *WN * 64) void grouped_gemm_kernel(GroupedArgs a
 // --------------------------------------------------------------- launches
 namespace {
 
+constexpr int kVecRowsPerGroup = 4;
+
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN>
@@ -386,6 +388,7 @@ hipError_t launch_tiles(GroupedArgs a, bool f32, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_grouped_mm(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
+    if (a.P <= kVecRowsPerGroup * a.E) return launch_grouped_vec(a, elt, f32, s);
     switch (elt) {
         case Elt::Bf16: return launch_tiles<Elt::Bf16, false, false, 128, 128, 2, 2>(a, f32, s);
         case Elt::F16: return launch_tiles<Elt::F16, false, false, 128, 128, 2, 2>(a, f32, s);

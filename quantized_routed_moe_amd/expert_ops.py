@@ -11,12 +11,11 @@ in as `out` is allocated for that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
-from . import Grouped, _check, _layout, _lib, _on_gpu
+from . import Grouped, _check, _layout, _lib
 
 DT = {torch.float32: 1, torch.bfloat16: 2, torch.float16: 3}
 _HALF = (torch.bfloat16, torch.float16)
@@ -29,74 +28,89 @@ def _dtype(t, name, allowed):
 
 def _matrix(t, name, dtype, rows, cols):
     """Shape, type and layout of a 2-d operand whose rows may be strided; returns its row stride."""
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: expected shape ({'rows' if rows is None else rows}, {cols}), got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name}: expected shape ({'rows' if rows is None else rows}, {cols}), got {tuple(shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape[0] < 2:  # the stride of a single row says nothing
-        if t.shape[0] == 1 and cols > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        stride = cols
+        if shape[0] < 2:  # nothing lies behind a single row: any stride will do
+            step = 16 // t.element_size()
+            return (cols + step - 1) // step * step
+    else:
+        stride, inner = t.stride()
+        if cols > 1 and inner != 1:
             raise ValueError(f"{name}: elements of a row must be consecutive")
-        return _single_stride(t, cols)
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: elements of a row must be consecutive")
-    if t.stride(0) < cols or t.stride(0) * t.element_size() % 16:
-        raise ValueError(f"{name}: row stride {t.stride(0)} must cover a row and be a multiple of 16 bytes")
-    return t.stride(0)
-
-
-def _single_stride(t, cols):
-    step = 16 // t.element_size()
-    return (cols + step - 1) // step * step
+    if stride < cols or stride * t.element_size() % 16:
+        raise ValueError(f"{name}: row stride {stride} must cover a row and be a multiple of 16 bytes")
+    return stride
 
 
 def _pointer(t, name, index):
-    """Device pointer of t on GPU `index`, 16-byte aligned where it has elements."""
-    p = _on_gpu(t, name)
+    """Device pointer of t on GPU `index`, 16-byte aligned."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be in GPU memory")
+    p = t.data_ptr()
     if t.get_device() != index:
         raise ValueError(f"{name}: is on GPU {t.get_device()}, the call is on GPU {index}")
-    if p % 16:
+    if p & 15:
         raise ValueError(f"{name}: must start 16-byte aligned")
     return p
 
 
+def _plain(t, name, index):
+    """_pointer without the alignment."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be in GPU memory")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: is on GPU {t.get_device()}, the call is on GPU {index}")
+    return t.data_ptr()
+
+
 def _target(first, name, stream):
-    """(GPU, raw stream, allocation context) of a call whose first operand is given."""
-    _on_gpu(first, name)
+    """(GPU, raw stream, stream to allocate for or None) of a call whose first operand is given."""
+    if not first.is_cuda:
+        raise ValueError(f"{name}: must be in GPU memory")
     index = first.get_device()
     if index != torch.cuda.current_device():
         raise ValueError(f"{name}: is on GPU {index}, the current GPU is {torch.cuda.current_device()}")
     if stream is None:
-        return index, torch.cuda.current_stream(index).cuda_stream, contextlib.nullcontext()
-    return index, stream.cuda_stream, torch.cuda.stream(stream)
+        # the handle alone: building a Stream object costs more than the rest of a small call
+        return index, torch._C._cuda_getCurrentRawStream(index), None
+    return index, stream.cuda_stream, stream
 
 
-def _output(out, name, shape, dtype, allowed, device, alloc):
-    """(out, its dtype, its row stride): a given output checked, or a new one."""
+def _new(like, shape, dtype, stream):
+    """A new tensor on like's GPU whose memory belongs to `stream` (None: the current one)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _output(out, shape, dtype, allowed, like, stream):
+    """(out, its row stride): a given output checked, or a new one."""
     if out is None:
         if dtype not in allowed:
-            raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {dtype}")
-        with alloc:
-            return torch.empty(shape, dtype=dtype, device=device), shape[-1]
+            raise ValueError(f"out: expected one of {', '.join(map(str, allowed))}, got {dtype}")
+        return _new(like, shape, dtype, stream), shape[-1]
     if out.dtype not in allowed:
-        raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {out.dtype}")
+        raise ValueError(f"out: expected one of {', '.join(map(str, allowed))}, got {out.dtype}")
     if len(shape) == 2:
-        return out, _matrix(out, name, out.dtype, *shape)
-    _layout(out, name, out.dtype, shape)
+        return out, _matrix(out, "out", out.dtype, *shape)
+    _layout(out, "out", out.dtype, shape)
     return out, shape[-1]
 
 
 def _groups(offsets, rows, src, n_experts, pairs, n, k, index):
     _layout(offsets, "offsets", torch.int32, (n_experts + 1,))
-    g = Grouped(n_experts, n, k, pairs, _on_gpu(offsets, "offsets"), None, 0)
-    if offsets.get_device() != index:
-        raise ValueError(f"offsets: is on GPU {offsets.get_device()}, the call is on GPU {index}")
-    if rows is not None:
-        _layout(rows, "rows", torch.int32, (pairs,))
-        # an empty tensor has no pointer; with no pairs nothing is read
-        g.rows, g.src_rows = _on_gpu(rows, "rows") or g.offsets, src
-        if rows.get_device() != index:
-            raise ValueError(f"rows: is on GPU {rows.get_device()}, the call is on GPU {index}")
-    return g
+    at = _plain(offsets, "offsets", index)
+    if rows is None:
+        return Grouped(n_experts, n, k, pairs, at, None, 0)
+    _layout(rows, "rows", torch.int32, (pairs,))
+    # an empty tensor has no pointer; with no pairs nothing is read
+    return Grouped(n_experts, n, k, pairs, at, _plain(rows, "rows", index) or at, src)
 
 
 def _bank(b, name, dtype):
@@ -116,10 +130,10 @@ def grouped_mm(a, b, offsets, rows=None, out=None, dtype=None, stream=None):
     _dtype(a, "a", _HALF)
     E, N, K = _bank(b, "b", a.dtype)
     lda = _matrix(a, "a", a.dtype, None, K)
-    index, raw, alloc = _target(a, "a", stream)
+    index, raw, side = _target(a, "a", stream)
     P = a.shape[0] if rows is None else rows.shape[0]
     g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
-    out, ldc = _output(out, "out", (P, N), dtype or a.dtype, (a.dtype, torch.float32), a.device, alloc)
+    out, ldc = _output(out, (P, N), dtype or a.dtype, (a.dtype, torch.float32), a, side)
     _check(_lib.moe_grouped_mm(ctypes.byref(g), DT[a.dtype], _pointer(a, "a", index), lda, _pointer(b, "b", index),
                                _pointer(out, "out", index), DT[out.dtype], ldc, raw), "moe_grouped_mm")
     return out
@@ -133,10 +147,10 @@ def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
     _dtype(dc, "dc", _HALF)
     E, N, K = _bank(b, "b", dc.dtype)
     ldd = _matrix(dc, "dc", dc.dtype, None, N)
-    index, raw, alloc = _target(dc, "dc", stream)
+    index, raw, side = _target(dc, "dc", stream)
     P = dc.shape[0]
     g = _groups(offsets, None, 0, E, P, N, K, index)
-    out, lda = _output(out, "out", (P, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc.device, alloc)
+    out, lda = _output(out, (P, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
     _check(_lib.moe_grouped_mm_grad_a(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(b, "b", index), _pointer(out, "out", index), DT[out.dtype], lda, raw),
            "moe_grouped_mm_grad_a")
@@ -153,26 +167,28 @@ def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=No
     P, N = dc.shape
     lda = _matrix(a, "a", dc.dtype, None if rows is not None else P, a.shape[-1])
     K = a.shape[1]
-    index, raw, alloc = _target(dc, "dc", stream)
+    index, raw, side = _target(dc, "dc", stream)
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets: expected [experts + 1], got {tuple(offsets.shape)}")
     E = offsets.shape[0] - 1
     g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
-    out, _ = _output(out, "out", (E, N, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc.device, alloc)
+    out, _ = _output(out, (E, N, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
     _check(_lib.moe_grouped_mm_grad_b(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(a, "a", index), lda, _pointer(out, "out", index), DT[out.dtype], raw),
            "moe_grouped_mm_grad_b")
     return out
 
 
-def _code_outputs(shape, codes, scales, device, alloc):
-    with alloc:
-        if codes is None:
-            codes = torch.empty(*shape[:-1], shape[-1] // 2, dtype=torch.uint8, device=device)
-        if scales is None:
-            scales = torch.empty(*shape[:-1], shape[-1] // 32, dtype=torch.uint8, device=device)
-    _layout(codes, "codes", torch.uint8, (*shape[:-1], shape[-1] // 2))
-    _layout(scales, "scales", torch.uint8, (*shape[:-1], shape[-1] // 32))
+def _code_outputs(shape, codes, scales, like, stream):
+    c, s = (*shape[:-1], shape[-1] // 2), (*shape[:-1], shape[-1] // 32)
+    if codes is None:
+        codes = _new(like, c, torch.uint8, stream)
+    else:
+        _layout(codes, "codes", torch.uint8, c)
+    if scales is None:
+        scales = _new(like, s, torch.uint8, stream)
+    else:
+        _layout(scales, "scales", torch.uint8, s)
     return codes, scales
 
 
@@ -195,10 +211,10 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     rows, cols, ld = _rows_of(x, "x")
     if cols % 32:
         raise ValueError(f"x: rows of {cols} elements are not made of blocks of 32")
-    index, raw, alloc = _target(x, "x", stream)
-    codes, scales = _code_outputs(x.shape, codes, scales, x.device, alloc)
+    index, raw, side = _target(x, "x", stream)
+    codes, scales = _code_outputs(x.shape, codes, scales, x, side)
     _check(_lib.moe_mxfp4_quantize(DT[x.dtype], _pointer(x, "x", index), ld, rows, cols,
-                                   _pointer(codes, "codes", index), _on_gpu(scales, "scales"), raw),
+                                   _pointer(codes, "codes", index), _plain(scales, "scales", index), raw),
            "moe_mxfp4_quantize")
     return codes, scales
 
@@ -215,9 +231,9 @@ def mxfp4_dequantize(codes, scales, out=None, dtype=torch.float32, stream=None):
     """The values that codes [.., n/2] and scales [.., n/32] stand for, [.., n] in `dtype`."""
     cols = _format(codes, scales, "codes", "scales")
     shape = (*codes.shape[:-1], cols)
-    index, raw, alloc = _target(codes, "codes", stream)
-    out, ld = _output(out, "out", shape, dtype, tuple(DT), codes.device, alloc)
-    _check(_lib.moe_mxfp4_dequantize(_pointer(codes, "codes", index), _on_gpu(scales, "scales"),
+    index, raw, side = _target(codes, "codes", stream)
+    out, ld = _output(out, shape, dtype, tuple(DT), codes, side)
+    _check(_lib.moe_mxfp4_dequantize(_pointer(codes, "codes", index), _plain(scales, "scales", index),
                                      codes.numel() * 2 // cols, cols, DT[out.dtype], _pointer(out, "out", index), ld,
                                      raw), "moe_mxfp4_dequantize")
     return out
@@ -233,14 +249,14 @@ def mxfp4_grouped_mm(a_codes, a_scales, b_codes, b_scales, offsets, rows=None, o
     E, N, half = _bank(b_codes, "b_codes", torch.uint8)
     if _format(b_codes, b_scales, "b_codes", "b_scales") != K:
         raise ValueError(f"b_codes: rows of {2 * half} elements, a has {K}")
-    index, raw, alloc = _target(a_codes, "a_codes", stream)
+    index, raw, side = _target(a_codes, "a_codes", stream)
     R = a_codes.shape[0]
     P = R if rows is None else rows.shape[0]
     g = _groups(offsets, rows, R, E, P, N, K, index)
-    out, ldc = _output(out, "out", (P, N), dtype, (torch.bfloat16, torch.float32), a_codes.device, alloc)
+    out, ldc = _output(out, (P, N), dtype, (torch.bfloat16, torch.float32), a_codes, side)
     _check(_lib.moe_mxfp4_grouped_mm(ctypes.byref(g), _pointer(a_codes, "a_codes", index),
-                                     _on_gpu(a_scales, "a_scales"), _pointer(b_codes, "b_codes", index),
-                                     _on_gpu(b_scales, "b_scales"), _pointer(out, "out", index), DT[out.dtype], ldc,
+                                     _plain(a_scales, "a_scales", index), _pointer(b_codes, "b_codes", index),
+                                     _plain(b_scales, "b_scales", index), _pointer(out, "out", index), DT[out.dtype], ldc,
                                      raw), "moe_mxfp4_grouped_mm")
     return out
 
@@ -255,8 +271,8 @@ def _gate_up(gu):
 def swiglu(gu, out=None, stream=None):
     """h = silu(gate) * up of gu [rows, 2 F] = [gate | up] (fp32, bf16 or fp16), [rows, F] of the same type."""
     rows, ffn, ldg = _gate_up(gu)
-    index, raw, alloc = _target(gu, "gu", stream)
-    out, ldh = _output(out, "out", (rows, ffn), gu.dtype, (gu.dtype,), gu.device, alloc)
+    index, raw, side = _target(gu, "gu", stream)
+    out, ldh = _output(out, (rows, ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(out, "out", index), ldh,
                            raw), "moe_swiglu")
     return out
@@ -267,10 +283,10 @@ def swiglu_mxfp4(gu, codes=None, scales=None, stream=None):
     rows, ffn, ldg = _gate_up(gu)
     if ffn % 32:
         raise ValueError(f"gu: rows of {ffn} outputs are not made of blocks of 32")
-    index, raw, alloc = _target(gu, "gu", stream)
-    codes, scales = _code_outputs((rows, ffn), codes, scales, gu.device, alloc)
+    index, raw, side = _target(gu, "gu", stream)
+    codes, scales = _code_outputs((rows, ffn), codes, scales, gu, side)
     _check(_lib.moe_swiglu_mxfp4(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn,
-                                 _pointer(codes, "codes", index), _on_gpu(scales, "scales"), raw), "moe_swiglu_mxfp4")
+                                 _pointer(codes, "codes", index), _plain(scales, "scales", index), raw), "moe_swiglu_mxfp4")
     return codes, scales
 
 
@@ -278,8 +294,8 @@ def swiglu_grad(dh, gu, out=None, stream=None):
     """The gradient of swiglu: dgu [rows, 2 F] = [dgate | dup] from dh [rows, F] and the gu of the forward call."""
     rows, ffn, ldg = _gate_up(gu)
     ldd = _matrix(dh, "dh", gu.dtype, rows, ffn)
-    index, raw, alloc = _target(gu, "gu", stream)
-    out, ldo = _output(out, "out", (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu.device, alloc)
+    index, raw, side = _target(gu, "gu", stream)
+    out, ldo = _output(out, (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu_grad(DT[gu.dtype], _pointer(dh, "dh", index), ldd, _pointer(gu, "gu", index), ldg, rows,
                                 ffn, _pointer(out, "out", index), ldo, raw), "moe_swiglu_grad")
     return out
