@@ -19,16 +19,19 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # multiply-adds only where the source asks for one), so every kernel that
 # shares a computation produces the same bits.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-I", os.path.join(ROOT, "include"),
-         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wno-unused-result",
-         # MFMA results in ordinary VGPRs: the epilogues read every result, and
-         # from AGPRs each read would be one more VALU instruction.
-         "-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wno-unused-result"]
+# MFMA results in ordinary VGPRs: the epilogues read every result, and from
+# AGPRs each read would be one more VALU instruction.
+VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+# Except where a wave's 256 accumulators leave no ordinary VGPRs to work with.
+AGPR_MFMA = {"grouped_mm.hip"}
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    form = [] if src in AGPR_MFMA else VGPR_MFMA
+    cmd = [HIPCC, *FLAGS, *form, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)

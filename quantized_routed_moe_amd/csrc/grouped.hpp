@@ -53,14 +53,8 @@ hipError_t launch_swiglu_grad(int dt, const void *dh, int64_t dh_ld, const void 
                               int64_t ffn, void *dgu, int64_t dgu_ld, hipStream_t s);
 
 // --------------------------------------------------------- group search
-// The row tiles of all groups in order: the rows before the first group, the
-// E groups, the rows past the last one (index i = 0 .. E+1; expert i - 1).
-__device__ __forceinline__ int group_bound(const int32_t *off, int E, int P, int i) {
-    if (i == 0) return 0;
-    if (i > E + 1) return P;
-    return min(max(off[i - 1], 0), P);
-}
-
+// Groups are counted with the rows before the first one and past the last one
+// as groups of their own: index 0 .. E + 1, expert index - 1.
 __device__ __forceinline__ int wave_incl_scan(int v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -76,43 +70,64 @@ struct RowTile {
     int row0, rows;
 };
 
-// Tile lists by one wave (every wave of a workgroup computes the same): lane
-// l counts the tiles of (E + 2) / 64 consecutive groups, a wave scan orders
-// them, and find() repeats the scan inside the lane's groups that hold tile t.
+// The row tiles of all groups in order, kept by one wave in registers (every
+// wave of a workgroup keeps the same): lane l holds the bounds of (E + 2) / 64
+// consecutive groups, a wave scan orders the lanes' tiles.  Up to 318 experts
+// the bounds stay in registers; beyond, find() reads them again.
 template <int BM>
 struct TileList {
+    static constexpr int kHeld = 5;
     const int32_t *off;
     int E, P, per, inc, total;
+    int held[kHeld + 1];
 
-    __device__ __forceinline__ int tiles(int i, int &lo, int &n) const {
-        lo = n = 0;
-        if (i > E + 1) return 0;
-        lo = group_bound(off, E, P, i);
-        n = max(group_bound(off, E, P, i + 1) - lo, 0);
-        return (n + BM - 1) / BM;
+    __device__ __forceinline__ int bound(int i) const {  // of group i of this lane's, 0 .. per
+        const int g = min((int)(threadIdx.x & 63) * per + i, E + 2);
+        const int v = min(max(off[min(max(g - 1, 0), E)], 0), P);
+        return g == 0 ? 0 : g > E + 1 ? P : v;
     }
     __device__ __forceinline__ TileList(const int32_t *o, int e, int p) : off(o), E(e), P(p) {
-        const int lane = threadIdx.x & 63;
         per = (E + 2 + 63) / 64;
-        int c = 0, lo, n;
-        for (int j = 0; j < per; ++j) c += tiles(lane * per + j, lo, n);
+        int c = 0;
+        if (per <= kHeld) {
+#pragma unroll
+            for (int i = 0; i <= kHeld; ++i) held[i] = bound(min(i, per));
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) c += (max(held[i + 1] - held[i], 0) + BM - 1) / BM;
+        } else {
+#pragma unroll
+            for (int i = 0; i <= kHeld; ++i) held[i] = 0;
+            for (int i = 0; i < per; ++i) c += (max(bound(i + 1) - bound(i), 0) + BM - 1) / BM;
+        }
         inc = wave_incl_scan(c);
         total = __builtin_amdgcn_readlane(inc, 63);
     }
     // t < total
     __device__ __forceinline__ RowTile find(int t) const {
-        const int lane = threadIdx.x & 63;
         const int l = __ffsll((long long)__ballot(inc > t)) - 1;
-        const int before = l > 0 ? __builtin_amdgcn_readlane(inc, l - 1) : 0;
-        int lo, n;
-        const int c = lane < per ? tiles(l * per + lane, lo, n) : (lo = n = 0);
-        const int inc2 = wave_incl_scan(c);
-        const int j = __ffsll((long long)__ballot(inc2 > t - before)) - 1;
-        const int skip = (t - before - (j > 0 ? __builtin_amdgcn_readlane(inc2, j - 1) : 0)) * BM;
-        RowTile r;
-        r.expert = l * per + j - 1;
-        r.row0 = __builtin_amdgcn_readlane(lo, j) + skip;
-        r.rows = min(__builtin_amdgcn_readlane(n, j) - skip, BM);
+        int skip = t - (l > 0 ? __builtin_amdgcn_readlane(inc, l - 1) : 0);  // tiles of the lane's groups before it
+        RowTile r{-1, 0, 0};
+        bool found = false;
+        auto look = [&](int i, int lo, int n) {
+            const int c = (n + BM - 1) / BM;
+            if (!found && skip < c) {
+                found = true;
+                r = RowTile{l * per + i - 1, lo + skip * BM, min(n - skip * BM, BM)};
+            }
+            skip -= c;
+        };
+        if (per <= kHeld) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int lo = __builtin_amdgcn_readlane(held[i], l);
+                look(i, lo, max(__builtin_amdgcn_readlane(held[i + 1], l) - lo, 0));
+            }
+        } else {
+            for (int i = 0; i < per && !found; ++i) {
+                const int lo = __builtin_amdgcn_readlane(bound(i), l);
+                look(i, lo, max(__builtin_amdgcn_readlane(bound(i + 1), l) - lo, 0));
+            }
+        }
         return r;
     }
 };
@@ -153,7 +168,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ i32x8 fp4_operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+// Four-bit operands fill the first half of the instruction's register tuple; the rest is not looked at.
+__device__ __forceinline__ i32x8 fp4_operand(i32x4 v) {
+    return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
 
 // 32x32 outer tile; 32 bytes of each row: 16 elements of 16 bits or 64 of four.
 // S: which byte of the scale words holds this step's block scale.

@@ -7,7 +7,13 @@
 // All three are out[m][n] = sum over d of x(m, d) y(n, d).  An operand is
 // stored either along d ("row" operand: x and y of forward, x of grad_a) or
 // across it ("column" operand: y of grad_a, both of grad_b).
+//
+// One workgroup a CU (or two) stays for the whole call and takes tile after
+// tile.  A stream of copies (global -> LDS, no registers) runs ahead of the
+// arithmetic by the depth of an LDS ring, from one tile into the next: the
+// first steps of a tile arrive while the tile before is stored.
 #include <type_traits>
+#include <cstdlib>
 
 #include "grouped.hpp"
 
@@ -15,6 +21,16 @@ namespace qrmoe {
 
 constexpr int kSlab = 128;  // bytes of one row operand's row, per K step: 64 elements of 16 bits, 256 of four
 constexpr int kStep = 64;   // rows of a column operand per K step
+constexpr int kCus = 256, kXcds = 8;
+
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unroll(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, I + 1>(f);
+    }
+}
 
 // ---------------------------------------------------------------- tiles
 // LDS image of one K step of an operand, R rows (columns) wide, 128 R bytes.
@@ -29,36 +45,43 @@ struct Stager {
     static constexpr int kLoads = R / 8 / NW;  // 1 KB copies of each wave and step
     static_assert(kLoads >= 1, "every wave copies");
     uint32_t off[kLoads];  // byte offset of this lane's piece, or kOob
-    uint32_t rem[kLoads];  // row operand: byte position of the piece inside the K step; column: its row of the step
 
-    // row operand
-    __device__ __forceinline__ int row(int i) const {
-        return ((threadIdx.x >> 6) * kLoads + i) * 8 + ((threadIdx.x & 63) >> 3);
-    }
-    static __device__ __forceinline__ int piece(int r) { return (threadIdx.x & 7) ^ ((r >> 1) & 7); }
+    // row operand: row of copy i's piece, and the piece
+    static __device__ __forceinline__ int row(int tid, int i) { return ((tid >> 6) * kLoads + i) * 8 + ((tid & 63) >> 3); }
+    static __device__ __forceinline__ int piece(int tid, int r) { return (tid & 7) ^ ((r >> 1) & 7); }
     // column operand
     static constexpr int kPer = R / 8;  // pieces of one row
-    __device__ __forceinline__ int col_row(int i) const {
-        return ((threadIdx.x >> 6) * kLoads + i) * (64 / kPer) + (threadIdx.x & 63) / kPer;
+    static __device__ __forceinline__ int col_row(int tid, int i) {
+        return ((tid >> 6) * kLoads + i) * (64 / kPer) + (tid & 63) / kPer;
     }
-    static __device__ __forceinline__ int col_piece(int d) { return ((threadIdx.x & 63) % kPer) ^ ((d & 3) << 2); }
-};
-
-struct Frag {
-    i32x4 v;
+    static __device__ __forceinline__ int col_piece(int tid, int d) { return ((tid & 63) % kPer) ^ ((d & 3) << 2); }
+    // where copy i's piece lies in the step: byte of the row, or row
+    static __device__ __forceinline__ uint32_t pos(int tid, int i) {
+        return COL ? col_row(tid, i) : 16 * piece(tid, row(tid, i));
+    }
 };
 
 typedef __attribute__((address_space(3))) i16x4 *lds_i16x4;
 
-// Where workgroup b's tile lies: tiles are dealt in contiguous runs to the
-// eight XCDs (workgroups go round them in turn), so that the tiles that share
-// an operand run behind the same L2; inside a run kGroupM row tiles advance
-// together through the columns.
-constexpr int kXcds = 8, kGroupM = 4;
-__device__ __forceinline__ bool xcd_tile(int b, int total, int &t) {
-    const int per = (total + kXcds - 1) / kXcds;
-    t = (b % kXcds) * per + b / kXcds;
-    return b / kXcds < per && t < total;
+// The same value, computed from anew by whoever uses it: keeps what is needed
+// once a tile out of the registers that the multiplication lives on.
+__device__ __forceinline__ int afresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Place in the list of tiles of a workgroup's b-th turn.  Workgroups go round
+// the eight XCDs; runs of RUN consecutive tiles (kGroupM row tiles advancing
+// together through RUN / kGroupM column tiles) go to one XCD, so that the
+// tiles that run behind one L2 at a time share their operands, and long and
+// short groups spread over all XCDs.  (Whole experts to each XCD instead: the
+// gradient of eight experts of 710 .. 4702 rows took 794 us, the XCDs being
+// done after 215 .. 1034.)
+constexpr int kGroupM = 4;
+template <int RUN>
+__device__ __forceinline__ int xcd_tile(int b) {
+    const int i = b / kXcds;
+    return (i / RUN * kXcds + b % kXcds) * RUN + i % RUN;
 }
 __device__ __forceinline__ void tile_mn(int t, int m_tiles, int n_tiles, int &m, int &n) {
     const int g = t / (kGroupM * n_tiles), first = g * kGroupM, gm = min(kGroupM, m_tiles - first);
@@ -67,191 +90,258 @@ __device__ __forceinline__ void tile_mn(int t, int m_tiles, int n_tiles, int &m,
     n = r / gm;
 }
 
-template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN, bool F32>
-__global__ __launch_bounds__(WM *WN * 64) void grouped_gemm_kernel(GroupedArgs a) {
+// A tile: its expert, first row and column, its rows (forward, grad_a: pairs;
+// grad_b: of the output, row0 .. row0 + depth being its pairs) and its depth
+// (0: zeros, rows of no group or an expert without pairs).
+struct Tile {
+    int e, row0, rows, m0, n0, depth;
+};
+
+template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN, int PER_CU, bool F32>
+__global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void grouped_gemm_kernel(GroupedArgs a) {
     constexpr int NW = WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr bool FP4 = ELT == Elt::Fp4;
     constexpr int kStages = 2;
     constexpr int XB = BM * kSlab, YB = BN * kSlab;
+    constexpr int kRun = kCus / kXcds * PER_CU;
     typedef Stager<BM, NW, XCOL> SX;
     typedef Stager<BN, NW, YCOL> SY;
-    __shared__ __align__(1024) uint8_t smem[kStages * (XB + YB)];
-    __shared__ __align__(16) uint8_t sscale[FP4 ? kStages * (BM + BN) * 8 : 16];
+    typedef typename Out<ELT, F32>::T T;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    // out goes through LDS in blocks of 32 rows; of half a row each where space is short
+    constexpr int kHalves = F32 && FP4 && NI > 1 ? 2 : 1;
+    constexpr int kOutCols = BN / kHalves, kOutBytes = 32 * kOutCols * (int)sizeof(T);
+    constexpr int kScaleBytes = FP4 ? 2 * (BM + BN) * 16 : 0;
+    __shared__ __align__(1024) uint8_t smem[kStages * (XB + YB) + kOutBytes + kScaleBytes];
+    uint8_t *const sout = smem + kStages * (XB + YB), *const sscale = sout + kOutBytes;
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
-    // ---- this workgroup's tile
-    int e, row0, rows, m0, n0, depth;
-    bool none = false;  // rows of no group
-    if constexpr (XCOL) {
-        int t, mt, nt;
-        if (!xcd_tile(blockIdx.x, a.E * a.m_tiles * a.n_tiles, t)) return;
-        e = t / (a.m_tiles * a.n_tiles);
-        tile_mn(t - e * a.m_tiles * a.n_tiles, a.m_tiles, a.n_tiles, mt, nt);
-        m0 = mt * BM;
-        n0 = nt * BN;
-        row0 = min(max(a.offsets[e], 0), a.P);
-        rows = max(min(max(a.offsets[e + 1], 0), a.P) - row0, 0);
-        depth = rows;
-    } else {
-        const TileList<BM> list(a.offsets, a.E, a.P);
-        int t, mt, nt;
-        if (!xcd_tile(blockIdx.x, list.total * a.n_tiles, t)) return;
-        tile_mn(t, list.total, a.n_tiles, mt, nt);
-        const RowTile r = list.find(mt);
-        none = r.expert < 0 || r.expert >= a.E;
-        e = none ? 0 : r.expert;
-        row0 = m0 = r.row0;
-        rows = r.rows;
-        n0 = nt * BN;
-        depth = none ? 0 : a.depth;
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
-    rows = __builtin_amdgcn_readfirstlane(rows);
-    depth = __builtin_amdgcn_readfirstlane(depth);
-    n0 = __builtin_amdgcn_readfirstlane(n0);
-    m0 = __builtin_amdgcn_readfirstlane(m0);
+    // ---- the list of tiles
+    const TileList<BM> list(a.offsets, XCOL ? 0 : a.E, XCOL ? 0 : a.P);
+    const int total = XCOL ? a.E * a.m_tiles * a.n_tiles : list.total * a.n_tiles;
+    auto find = [&](int turn, Tile &t) -> bool {
+        const int at = xcd_tile<kRun>(blockIdx.x + turn * gridDim.x);
+        if (at >= total) {
+            t = Tile{0, 0, 0, 0, 0, 0};
+            return false;
+        }
+        int mt, nt;
+        if constexpr (XCOL) {
+            const int each = a.m_tiles * a.n_tiles;
+            t.e = at / each;
+            tile_mn(at - t.e * each, a.m_tiles, a.n_tiles, mt, nt);
+            t.row0 = min(max(a.offsets[t.e], 0), a.P);
+            t.depth = max(min(max(a.offsets[t.e + 1], 0), a.P) - t.row0, 0);
+            t.m0 = mt * BM;
+            t.rows = min(a.M - t.m0, BM);
+        } else {
+            tile_mn(at, list.total, a.n_tiles, mt, nt);
+            const RowTile r = list.find(mt);
+            const bool none = r.expert < 0 || r.expert >= a.E;
+            t.e = none ? 0 : r.expert;
+            t.row0 = t.m0 = r.row0;
+            t.rows = r.rows;
+            t.depth = none ? 0 : a.depth;
+        }
+        t.n0 = nt * BN;
+        t.e = __builtin_amdgcn_readfirstlane(t.e);
+        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+        t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+        t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+        t.depth = __builtin_amdgcn_readfirstlane(t.depth);
+        return true;
+    };
     constexpr int kElems = FP4 ? 256 : kStep;  // contraction elements of one K step
-    const int steps = (depth + kElems - 1) / kElems;
+    auto steps_of = [&](const Tile &t) { return (t.depth + kElems - 1) / kElems; };
 
-    // ---- copies of one K step
+    // ---- the stream of copies: tile `ct`, of which `cleft` bytes of a row (with a column operand: rows) are still to
+    // be sent for, cstep steps having been; `nt` (this workgroup's turn `cturn`) is the tile after it
     SX sx;
     SY sy;
-    const uint8_t *xb, *yb;  // bases, advanced by one step at a time
-    int64_t x_step, y_step;
-    if constexpr (XCOL) {
-        xb = a.x + (int64_t)row0 * a.x_ld + (int64_t)m0 * 2;
-        x_step = kStep * a.x_ld;
-#pragma unroll
-        for (int i = 0; i < SX::kLoads; ++i) {
-            const int d = sx.col_row(i), c = SX::col_piece(d);
-            sx.rem[i] = d;
-            sx.off[i] = m0 + 8 * c < a.M ? (uint32_t)(d * a.x_ld + 16 * c) : kOob;
-        }
-    } else {
-        x_step = kSlab;
-        xb = a.rows ? a.x : a.x + (int64_t)row0 * a.x_ld;
-#pragma unroll
-        for (int i = 0; i < SX::kLoads; ++i) {
-            const int r = sx.row(i), c = SX::piece(r);
-            int src = r;
-            bool ok = r < rows && !none;
-            if (a.rows && ok) {
-                src = a.rows[row0 + r];
-                ok = (uint32_t)src < (uint32_t)a.src_rows;
+    Tile ct, nt;
+    int cturn = 0, cleft = 0, cstep = 0;
+    bool more = false;           // nt is a tile
+    const uint8_t *cx, *cy;      // bases, advanced by one step at a time
+    int64_t cx_step, cy_step;
+    constexpr int kScaleRows = FP4 ? (BM + BN + NW * 64 - 1) / (NW * 64) : 1;  // scale rows of this thread
+    const uint8_t *ps[kScaleRows];                                           // null: no row
+    i32x4 ws[kScaleRows];
+    int nsrc[SX::kLoads], nsrc_scale[kScaleRows];  // gathered: the next tile's source rows, -1 for none
+    int src[SY::kLoads];                           // grad_b, gathered: the next step's source rows
+
+    // The tile after ct and, where rows are gathered, what its copies will read from.
+    auto look_ahead = [&] {
+        const int tid = afresh(threadIdx.x);
+        more = false;
+        while (true) {  // tiles without depth need no copies
+            if (!find(++cturn, nt)) break;
+            if (nt.depth > 0) {
+                more = true;
+                break;
             }
-            sx.rem[i] = 16 * c;
-            sx.off[i] = ok ? (uint32_t)(src * a.x_ld + 16 * c) : kOob;
         }
-    }
-    if constexpr (YCOL) {
-        const bool rows_y = XCOL;  // grad_b: y is a, whose rows are the contraction
-        yb = rows_y ? (a.rows ? a.y : a.y + (int64_t)row0 * a.y_ld) + (int64_t)n0 * 2
-                    : a.y + e * a.y_mat + (int64_t)n0 * 2;
-        y_step = rows_y && a.rows ? 0 : kStep * a.y_ld;
+        if constexpr (!XCOL) {
+            if (a.rows && more) {
 #pragma unroll
-        for (int i = 0; i < SY::kLoads; ++i) {
-            const int d = sy.col_row(i), c = SY::col_piece(d);
-            sy.rem[i] = d;
-            sy.off[i] = n0 + 8 * c < a.N ? (uint32_t)((rows_y && a.rows ? 0 : d * a.y_ld) + 16 * c) : kOob;
-        }
-    } else {
-        yb = a.y + e * a.y_mat + (int64_t)n0 * a.y_ld;
-        y_step = kSlab;
+                for (int i = 0; i < SX::kLoads; ++i) {
+                    const int r = SX::row(tid, i);
+                    nsrc[i] = r < nt.rows ? a.rows[nt.row0 + r] : -1;
+                }
+                if constexpr (FP4) {
 #pragma unroll
-        for (int i = 0; i < SY::kLoads; ++i) {
-            const int r = sy.row(i), c = SY::piece(r);
-            sy.rem[i] = 16 * c;
-            sy.off[i] = n0 + r < a.N ? (uint32_t)(r * a.y_ld + 16 * c) : kOob;
-        }
-    }
-    // grad_b with gathered rows: the source row of each copy, one step ahead
-    int src[SY::kLoads];
-    auto load_src = [&](int k) {
-        if constexpr (XCOL && YCOL) {
-            if (a.rows) {
-#pragma unroll
-                for (int i = 0; i < SY::kLoads; ++i) {
-                    const int d = k * kStep + (int)sy.rem[i];
-                    src[i] = d < depth ? a.rows[row0 + d] : -1;
+                    for (int i = 0; i < kScaleRows; ++i) {
+                        const int r = i * NW * 64 + tid;
+                        nsrc_scale[i] = r < BM && r < nt.rows ? a.rows[nt.row0 + r] : -1;
+                    }
                 }
             }
         }
     };
-    // four-bit operands: block scales of a step, 8 bytes a row; thread t holds the word t % 2 of row t / 2
-    constexpr int kSX = FP4 ? (BM * 2 + NW * 64 - 1) / (NW * 64) : 1, kSY = FP4 ? (BN * 2 + NW * 64 - 1) / (NW * 64) : 1;
-    uint32_t wsx[kSX], wsy[kSY];
-    const uint8_t *px[kSX], *py[kSY];
-    const int blocks = depth / 32;
-    if constexpr (FP4) {
+    auto load_src = [&] {  // source rows of the step at cstep of ct
+        if constexpr (XCOL && YCOL) {
+            if (a.rows) {
 #pragma unroll
-        for (int i = 0; i < kSX; ++i) {
-            const int r = (i * NW * 64 + tid) >> 1;
-            int s = -1;
-            if (r < rows && !none) s = a.rows ? a.rows[row0 + r] : row0 + r;
-            if (a.rows && (uint32_t)s >= (uint32_t)a.src_rows) s = -1;
-            px[i] = s < 0 ? nullptr : a.xs + (int64_t)s * blocks;
-        }
-#pragma unroll
-        for (int i = 0; i < kSY; ++i) {
-            const int r = (i * NW * 64 + tid) >> 1;
-            py[i] = r < BN && n0 + r < a.N ? a.ys + ((int64_t)e * a.N + n0 + r) * blocks : nullptr;
-        }
-    }
-    auto load_word = [&](const uint8_t *p, int b) -> uint32_t {  // scales b .. b+3 of a row, zeros past its end
-        uint32_t w = 0;
-        if (p && b < blocks) {
-            if (b + 4 <= blocks)
-                __builtin_memcpy(&w, p + b, 4);
-            else
-                for (int j = 0; j < blocks - b; ++j) w |= (uint32_t)p[b + j] << (8 * j);
-        }
-        return w;
-    };
-    auto load_scales = [&](int k) {
-        if constexpr (FP4) {
-#pragma unroll
-            for (int i = 0; i < kSX; ++i) wsx[i] = load_word(px[i], 8 * k + 4 * (tid & 1));
-#pragma unroll
-            for (int i = 0; i < kSY; ++i) wsy[i] = load_word(py[i], 8 * k + 4 * (tid & 1));
-        }
-    };
-    auto store_scales = [&](int stg) {
-        if constexpr (FP4) {
-            uint32_t *d = reinterpret_cast<uint32_t *>(sscale + stg * (BM + BN) * 8);
-#pragma unroll
-            for (int i = 0; i < kSX; ++i) {
-                const int w = i * NW * 64 + tid;
-                if (w < BM * 2) d[w] = wsx[i];
-            }
-#pragma unroll
-            for (int i = 0; i < kSY; ++i) {
-                const int w = i * NW * 64 + tid;
-                if (w < BN * 2) d[BM * 2 + w] = wsy[i];
+                for (int i = 0; i < SY::kLoads; ++i) {
+                    const int d = SY::col_row(tid, i);
+                    src[i] = d < cleft ? a.rows[ct.row0 + cstep * kStep + d] : -1;
+                }
             }
         }
     };
-    const int row_bytes = FP4 ? depth / 2 : depth * 2;
+    // The stream goes on to nt (nothing to copy if there is none).
+    auto next_tile = [&] {
+        const int tid = afresh(threadIdx.x);
+        ct = nt;
+        cstep = 0;
+        cleft = !more ? 0 : XCOL || YCOL ? ct.depth : FP4 ? ct.depth / 2 : ct.depth * 2;
+        if constexpr (XCOL) {
+            cx = a.x + (int64_t)ct.row0 * a.x_ld + (int64_t)ct.m0 * 2;
+            cx_step = kStep * a.x_ld;
+#pragma unroll
+            for (int i = 0; i < SX::kLoads; ++i) {
+                const int d = SX::col_row(tid, i), c = SX::col_piece(tid, d);
+                sx.off[i] = ct.m0 + 8 * c < a.M ? (uint32_t)(d * a.x_ld + 16 * c) : kOob;
+            }
+        } else {
+            cx_step = kSlab;
+            cx = a.rows ? a.x : a.x + (int64_t)ct.row0 * a.x_ld;
+#pragma unroll
+            for (int i = 0; i < SX::kLoads; ++i) {
+                const int r = SX::row(tid, i);
+                const int s = !a.rows ? r : nsrc[i];
+                const bool ok = r < ct.rows && (!a.rows || (uint32_t)s < (uint32_t)a.src_rows);
+                sx.off[i] = ok ? (uint32_t)(s * a.x_ld + SX::pos(tid, i)) : kOob;
+            }
+        }
+        if constexpr (YCOL) {
+            const bool gathered = XCOL && a.rows;  // grad_b: y is a, whose rows are the contraction
+            cy = XCOL ? (gathered ? a.y : a.y + (int64_t)ct.row0 * a.y_ld) + (int64_t)ct.n0 * 2
+                      : a.y + ct.e * a.y_mat + (int64_t)ct.n0 * 2;
+            cy_step = gathered ? 0 : kStep * a.y_ld;
+#pragma unroll
+            for (int i = 0; i < SY::kLoads; ++i) {
+                const int d = SY::col_row(tid, i), c = SY::col_piece(tid, d);
+                sy.off[i] = ct.n0 + 8 * c < a.N ? (uint32_t)((gathered ? 0 : d * a.y_ld) + 16 * c) : kOob;
+            }
+        } else {
+            cy = a.y + ct.e * a.y_mat + (int64_t)ct.n0 * a.y_ld;
+            cy_step = kSlab;
+#pragma unroll
+            for (int i = 0; i < SY::kLoads; ++i) {
+                const int r = SY::row(tid, i);
+                sy.off[i] = ct.n0 + r < a.N ? (uint32_t)(r * a.y_ld + SY::pos(tid, i)) : kOob;
+            }
+        }
+        if constexpr (FP4) {
+            const int blocks = a.depth / 32;
+#pragma unroll
+            for (int i = 0; i < kScaleRows; ++i) {
+                const int r = i * NW * 64 + tid;
+                ps[i] = nullptr;
+                if (r < BM) {
+                    const int s = !a.rows ? (r < ct.rows ? ct.row0 + r : -1) : nsrc_scale[i];
+                    if (more && s >= 0 && (!a.rows || (uint32_t)s < (uint32_t)a.src_rows))
+                        ps[i] = a.xs + (int64_t)s * blocks;
+                } else if (more && r < BM + BN && ct.n0 + r - BM < a.N) {
+                    ps[i] = a.ys + ((int64_t)ct.e * a.N + ct.n0 + r - BM) * blocks;
+                }
+            }
+        }
+        look_ahead();
+    };
+
+    // One step's copies into ring stage stg: begin, kCopies times send, end.
+    constexpr int kCopies = SX::kLoads + SY::kLoads;
+    struct Copy {
+        i32x4 rx, ry;
+        uint32_t lx, ly;
+    };
     const uint32_t lds0 = lds_addr(smem);
-    auto issue = [&](int k, int stg) {
-        const i32x4 rx = dma_rsrc(xb + k * x_step), ry = dma_rsrc(yb + k * y_step);
-        const uint32_t lx = lds0 + stg * (XB + YB) + wave * (SX::kLoads * 1024);
-        const uint32_t ly = lds0 + stg * (XB + YB) + XB + wave * (SY::kLoads * 1024);
-        const uint32_t left_x = XCOL ? depth - k * kStep : row_bytes - k * kSlab;
-        const uint32_t left_y = YCOL ? depth - k * kStep : row_bytes - k * kSlab;
-#pragma unroll
-        for (int i = 0; i < SX::kLoads; ++i) dma16_async(rx, lx + i * 1024, sx.rem[i] < left_x ? sx.off[i] : kOob);
-#pragma unroll
-        for (int i = 0; i < SY::kLoads; ++i) {
-            uint32_t o = sy.rem[i] < left_y ? sy.off[i] : kOob;
+    auto begin_copy = [&](int stg) {
+        const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + stg * (XB + YB));
+        return Copy{dma_rsrc(cx), dma_rsrc(cy), base + wave * (SX::kLoads * 1024),
+                    base + XB + wave * (SY::kLoads * 1024)};
+    };
+    auto send = [&](const Copy &c, auto idx) {
+        constexpr int I = decltype(idx)::value;
+        const uint32_t left = (uint32_t)cleft;
+        if constexpr (I < SX::kLoads) {
+            const uint32_t left_x = !XCOL && YCOL ? 2 * left : left;
+            dma16_async(c.rx, c.lx + I * 1024, SX::pos(tid, I) < left_x ? sx.off[I] : kOob);
+        } else {
+            constexpr int i = I - SX::kLoads;
+            uint32_t o = SY::pos(tid, i) < left ? sy.off[i] : kOob;
             if constexpr (XCOL && YCOL)
                 if (a.rows)
-                    o = sy.off[i] != kOob && (uint32_t)src[i] < (uint32_t)a.src_rows
-                            ? (uint32_t)(src[i] * a.y_ld + sy.off[i]) : kOob;
-            dma16_async(ry, ly + i * 1024, o);
+                    o = o != kOob && (uint32_t)src[i] < (uint32_t)a.src_rows ? (uint32_t)(src[i] * a.y_ld + o) : kOob;
+            dma16_async(c.ry, c.ly + i * 1024, o);
+        }
+    };
+    auto end_copy = [&] {
+        cx += cx_step;
+        cy += cy_step;
+        ++cstep;
+        cleft = max(cleft - (XCOL || YCOL ? kStep : kSlab), 0);
+        if (cleft == 0 && more) next_tile();
+        load_src();
+    };
+
+    // four-bit operands: block scales, 16 bytes (two steps) of each row at a time, as words
+    // [step][half]: the blocks half, 2 + half, 4 + half, 6 + half that a lane's four MFMAs of a step need
+    auto load_scales = [&](int pair) {  // zeros past the row's end and for no row
+        if constexpr (FP4) {
+            const int blocks = a.depth / 32;
+#pragma unroll
+            for (int i = 0; i < kScaleRows; ++i) {
+                ws[i] = i32x4{};
+                if (!ps[i]) continue;
+                if (16 * pair + 16 <= blocks) {
+                    __builtin_memcpy(&ws[i], ps[i] + 16 * pair, 16);
+                } else {
+#pragma unroll 1
+                    for (int j = blocks - 16 * pair - 1; j >= 0; --j)  // shift in from the last to the first
+                        ws[i] = i32x4{ws[i].x << 8 | ps[i][16 * pair + j],
+                                      (int)__builtin_amdgcn_alignbyte(ws[i].y, ws[i].x, 3),
+                                      (int)__builtin_amdgcn_alignbyte(ws[i].z, ws[i].y, 3),
+                                      (int)__builtin_amdgcn_alignbyte(ws[i].w, ws[i].z, 3)};
+                }
+            }
+        }
+    };
+    auto store_scales = [&](int buf) {
+        if constexpr (FP4) {
+            i32x4 *d = reinterpret_cast<i32x4 *>(sscale + buf * (BM + BN) * 16);
+#pragma unroll
+            for (int i = 0; i < kScaleRows; ++i)
+                if (i * NW * 64 + tid < BM + BN)
+                    d[i * NW * 64 + tid] = i32x4{(int)__builtin_amdgcn_perm(ws[i].y, ws[i].x, 0x06040200),
+                                                 (int)__builtin_amdgcn_perm(ws[i].y, ws[i].x, 0x07050301),
+                                                 (int)__builtin_amdgcn_perm(ws[i].w, ws[i].z, 0x06040200),
+                                                 (int)__builtin_amdgcn_perm(ws[i].w, ws[i].z, 0x07050301)};
         }
     };
 
@@ -273,92 +363,171 @@ __global__ __launch_bounds__(WM *WN * 64) void grouped_gemm_kernel(GroupedArgs a
         return __builtin_bit_cast(i32x4, both);
     };
 
-    f32x16 acc[MI][NI];
+    // ---- a tile's product
+    // K steps in four groups of MFMAs (32 bytes of every row each), the operands
+    // of a group being read while the group before is multiplied.  The stage of
+    // a step is free once every wave has read its last group, which is before
+    // the last quarter of the step's arithmetic: there the waves meet, the next
+    // step (of this tile or the next) has arrived, and one more is sent for.
+    // Reads and copies are spread between the MFMAs (an MFMA keeps its unit
+    // busy for 32 cycles and the wave goes on issuing).
+    //
+    // LIVE: row blocks of 32 that a wave covers; a short tile takes fewer.
+    int stg = 0, sbuf = 0;  // ring stage of the step being multiplied; scale buffer of its pair of steps
+    auto product = [&](const Tile &t, auto live_c) {
+        constexpr int LIVE = decltype(live_c)::value;
+        constexpr int kReads = LIVE + NI, kMf = LIVE * NI;
+        const int wrow = wm * LIVE * 32, wcol = wn * NI * 32;
+        const int steps = steps_of(t);
+        i32x4 xf[2][LIVE], yf[2][NI];
+        int qx[2][LIVE], qy[2][NI];
+        f32x16 acc[LIVE][NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < LIVE; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
-
-    auto compute = [&](int stg) {
-        const uint8_t *tx = smem + stg * (XB + YB), *ty = tx + XB;
-        uint64_t qx[MI], qy[NI];
-        if constexpr (FP4) {
-            const uint8_t *s = sscale + stg * (BM + BN) * 8;
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-                qx[i] = *reinterpret_cast<const uint64_t *>(s + (wm * MI * 32 + i * 32 + l32) * 8) >> (8 * half);
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                qy[j] = *reinterpret_cast<const uint64_t *>(s + (BM + wn * NI * 32 + j * 32 + l32) * 8) >> (8 * half);
-        }
-        auto step = [&](auto kk_c) {
-            constexpr int kk = decltype(kk_c)::value, S = (kk & 1) * 2;
-            i32x4 xf[MI], yf[NI];
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-                xf[i] = XCOL ? read_col(tx, BM, wm * MI * 32 + i * 32, kk) : read_row(tx, wm * MI * 32 + i * 32, kk);
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                yf[j] = YCOL ? read_col(ty, BN, wn * NI * 32 + j * 32, kk) : read_row(ty, wn * NI * 32 + j * 32, kk);
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    acc[i][j] = mfma32<ELT, S>(yf[j], xf[i], acc[i][j], FP4 ? (int)(qy[j] >> (kk >> 1) * 32) : 0,
-                                               FP4 ? (int)(qx[i] >> (kk >> 1) * 32) : 0);
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
+        auto read_one = [&](auto buf, auto idx, int s, int kk) {
+            constexpr int B = decltype(buf)::value, I = decltype(idx)::value;
+            const uint8_t *tx = smem + s * (XB + YB), *ty = tx + XB;
+            if constexpr (I < NI)
+                yf[B][I] = YCOL ? read_col(ty, BN, wcol + I * 32, kk) : read_row(ty, wcol + I * 32, kk);
+            else
+                xf[B][I - NI] = XCOL ? read_col(tx, BM, wrow + (I - NI) * 32, kk) : read_row(tx, wrow + (I - NI) * 32, kk);
         };
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
-    };
-
-    // ---- K steps: while step k is multiplied, step k + 1 arrives in the other half
-    if (steps > 0) {
-        load_src(0);
-        load_scales(0);
-        issue(0, 0);
-        load_src(1);
-        store_scales(0);
-    }
+        auto read_scale = [&](auto buf, auto idx, int sb, int odd) {
+            constexpr int B = decltype(buf)::value, I = decltype(idx)::value;
+            const uint8_t *s = sscale + sb * (BM + BN) * 16 + odd * 8 + half * 4;
+            const int r = I < NI ? BM + wcol + I * 32 + l32 : wrow + (I - NI) * 32 + l32;
+            const int v = *reinterpret_cast<const int *>(s + r * 16);
+            if constexpr (I < NI) qy[B][I] = v;
+            else qx[B][I - NI] = v;
+        };
+        // group kk out of buffer kk & 1; meanwhile group `next` of stage s into the other, in the step's last group the
+        // next step's scales, and this wave's copies
+        auto group = [&](auto kk_c, int s, int next, int sb, int odd, const Copy &c) {
+            constexpr int kk = decltype(kk_c)::value, B = kk & 1;
+            constexpr bool kLast = kk == 3;
+            constexpr int kSend = kLast ? kCopies : 0;
+            unroll<kMf>([&](auto m_c) {
+                constexpr int m = decltype(m_c)::value, i = m / NI, j = m % NI;
+                acc[i][j] = mfma32<ELT, kk>(yf[B][j], xf[B][i], acc[i][j], FP4 ? qy[0][j] : 0, FP4 ? qx[0][i] : 0);
+                unroll<(m + 1) * kReads / kMf - m * kReads / kMf>([&](auto r_c) {
+                    constexpr std::integral_constant<int, m * kReads / kMf + decltype(r_c)::value> idx{};
+                    read_one(std::integral_constant<int, B ^ 1>{}, idx, s, next);
+                    if constexpr (FP4 && kLast) read_scale(std::integral_constant<int, 1>{}, idx, sb, odd);
+                });
+                unroll<(m + 1) * kSend / kMf - m * kSend / kMf>([&](auto c_c) {
+                    send(c, std::integral_constant<int, m * kSend / kMf + decltype(c_c)::value>{});
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        constexpr std::integral_constant<int, 0> c0{};
+        constexpr std::integral_constant<int, 1> c1{};
+        constexpr std::integral_constant<int, 2> c2{};
+        constexpr std::integral_constant<int, 3> c3{};
+        if (steps > 0)
+            unroll<kReads>([&](auto i) {
+                read_one(c0, i, stg, 0);
+                if constexpr (FP4) read_scale(c0, i, sbuf, 0);
+            });
+        // (after the tile's last step the operands read ahead are not used: the next tile reads its own)
 #pragma unroll 1
-    for (int k = 0; k < steps; ++k) {
-        const int stg = k & 1;
-        wait_vm<0>();
-        lds_barrier();
-        if (k + 1 < steps) {
-            load_scales(k + 1);
-            issue(k + 1, stg ^ 1);
-            load_src(k + 2);
-        }
-        compute(stg);
-        if (k + 1 < steps) store_scales(stg ^ 1);
-    }
-
-    // ---- out: register 4 q + i of a tile holds column 8 q + 4 half + i of row l32
-    typedef typename Out<ELT, F32>::T T;
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    T *out = (T *)a.out;
-    if constexpr (XCOL) out += (int64_t)e * a.M * a.out_ld;
-    const int m_end = XCOL ? a.M : m0 + rows;
+        for (int k = 0; k < steps; ++k) {
+            // the copies of the step after this one are under way: ct is its tile, cstep - 1 its place there
+            const bool fresh = FP4 && ((cstep - 1) & 1) == 0;  // it begins a pair
+            if (fresh) load_scales((cstep - 1) >> 1);
+            group(c0, stg, 1, 0, 0, Copy{});
+            group(c1, stg, 2, 0, 0, Copy{});
+            group(c2, stg, 3, 0, 0, Copy{});
+            if (fresh) store_scales(sbuf ^= 1);
+            wait_vm<0>();
+            lds_barrier();
+            const Copy c = begin_copy(stg);
+            stg ^= 1;
+            group(c3, stg, 0, sbuf, (k + 1) & 1, c);
+            end_copy();
+            if constexpr (FP4) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int m = m0 + (wm * MI + i) * 32 + l32;
-        if (m >= m_end) continue;
-        T *o = out + (int64_t)m * a.out_ld;
+                for (int i = 0; i < LIVE; ++i) qx[0][i] = qx[1][i];
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int n = n0 + (wn * NI + j) * 32 + 4 * half;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (n + 8 * q >= a.N) continue;
-                T4 v;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = Out<ELT, F32>::cvt(acc[i][j][4 * q + u]);
-                *reinterpret_cast<T4 *>(o + n + 8 * q) = v;
+                for (int j = 0; j < NI; ++j) qy[0][j] = qy[1][j];
             }
         }
+
+        // ---- out, through LDS in blocks of 32 rows, so that a wave stores
+        // whole stretches of them.  Register 4 q + i of a 32x32 tile holds
+        // column 8 q + 4 half + i of row l32.  Piece c (16 bytes) of row r lies
+        // in slot c ^ (r & (kPieces - 1)): the 32 rows of a write and the
+        // pieces of a read fall on different banks.
+        constexpr int kPer = 16 / (int)sizeof(T), kPieces = kOutCols / kPer;  // elements of a piece, pieces of a row
+        constexpr int kNh = NI / kHalves;
+        const int tid = afresh(threadIdx.x), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
+        T *out = (T *)a.out + (XCOL ? ((int64_t)t.e * a.M + t.m0) * a.out_ld : (int64_t)t.m0 * a.out_ld) + t.n0;
+        unroll<LIVE * WM * kHalves>([&](auto part_c) {
+            constexpr int part = decltype(part_c)::value, h = part % kHalves, i = part / kHalves % LIVE,
+                          w = part / kHalves / LIVE;
+            const int r0 = (w * LIVE + i) * 32;
+            if (r0 >= t.rows) return;
+            if (wm == w) {
+#pragma unroll
+                for (int j = 0; j < kNh; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = (wn * kNh + j) * 32 + 8 * q + 4 * half;
+                        T4 v;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) v[u] = Out<ELT, F32>::cvt(acc[i][h * kNh + j][4 * q + u]);
+                        const int slot = (n / kPer) ^ (l32 & (kPieces - 1));
+                        *reinterpret_cast<T4 *>(sout + (l32 * kPieces + slot) * 16 + (n % kPer) * (int)sizeof(T)) = v;
+                    }
+            }
+            lds_barrier();
+#pragma unroll
+            for (int s = 0; s < 32 * kPieces / (NW * 64); ++s) {
+                const int p = s * NW * 64 + tid, r = p / kPieces, c = p % kPieces;
+                // column of piece c: pieces of a wave column's half stand together
+                const int n = kHalves == 1 ? c * kPer
+                                           : (c * kPer / (kNh * 32) * NI + h * kNh) * 32 + c * kPer % (kNh * 32);
+                if (r0 + r < t.rows && t.n0 + n < a.N)
+                    *reinterpret_cast<i32x4 *>(out + (int64_t)(r0 + r) * a.out_ld + n) =
+                        *reinterpret_cast<const i32x4 *>(sout + (r * kPieces + (c ^ (r & (kPieces - 1)))) * 16);
+            }
+            lds_barrier();
+        });
+    };
+
+    // ---- first copies, then tile after tile
+    cturn = -1;
+    look_ahead();
+    next_tile();
+    load_src();
+    auto copy_step = [&](int s) {
+        const Copy c = begin_copy(s);
+        unroll<kCopies>([&](auto i) { send(c, i); });
+        end_copy();
+    };
+    if (FP4) {
+        load_scales(0);
+        store_scales(0);
     }
+    copy_step(0);
+    wait_vm<0>();
+    copy_step(1);
+    lds_barrier();
+    Tile t;
+    for (int turn = 0; find(turn, t); ++turn) {
+        const int need = XCOL ? BM : t.rows;
+        if (need <= BM / MI)
+            product(t, std::integral_constant<int, 1>{});
+        else if (MI > 2 && need <= BM / MI * 2)
+            product(t, std::integral_constant<int, MI < 2 ? MI : 2>{});
+        else if (MI > 3 && need <= BM / MI * 3)
+            product(t, std::integral_constant<int, MI < 3 ? MI : 3>{});
+        else
+            product(t, std::integral_constant<int, MI>{});
+    }
+    wait_vm<0>();
 }
 
 // --------------------------------------------------------------- launches
@@ -368,42 +537,60 @@ constexpr int kVecRowsPerGroup = 4;
 
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN>
+template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN, int PER_CU>
 hipError_t launch_tiles(GroupedArgs a, bool f32, hipStream_t s) {
     a.n_tiles = ceil_div(a.N, BN);
     a.m_tiles = ceil_div(a.M, BM);
     // row tiles of the ragged groups: at most one part tile for each group and for the rows before and past them
     const int64_t tiles = XCOL ? (int64_t)a.E * a.m_tiles * a.n_tiles : ((int64_t)a.P / BM + a.E + 2) * a.n_tiles;
-    const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (tiles > 0x3fffffff) return hipErrorInvalidValue;
+    constexpr int kRun = kCus / kXcds * PER_CU;
+    const int64_t all = (tiles + kXcds * kRun - 1) / (kXcds * kRun) * (kXcds * kRun);
+    const dim3 grid((unsigned)(all < kCus * PER_CU ? all : kCus * PER_CU));
     if (f32)
-        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, true>, dim3((unsigned)grid), dim3(WM * WN * 64), s,
-                a);
+        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, true>, grid, dim3(WM * WN * 64), s, a);
     else
-        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, false>, dim3((unsigned)grid), dim3(WM * WN * 64),
-                s, a);
+        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, false>, grid, dim3(WM * WN * 64), s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+#define VARIANTS(E, XC, YC) \
+    switch (getenv("TILE") ? atoi(getenv("TILE")) : 0) { \
+        case 0: return launch_tiles<E, XC, YC, 128, 128, 2, 2, 2>(a, f32, s); \
+        case 1: return launch_tiles<E, XC, YC, 256, 256, 2, 4, 1>(a, f32, s); \
+        case 5: return launch_tiles<E, XC, YC, 256, 256, 2, 2, 1>(a, f32, s); \
+        default: break; \
+    }
 hipError_t launch_grouped_mm(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
     if (a.P <= kVecRowsPerGroup * a.E) return launch_grouped_vec(a, elt, f32, s);
-    switch (elt) {
-        case Elt::Bf16: return launch_tiles<Elt::Bf16, false, false, 128, 128, 2, 2>(a, f32, s);
-        case Elt::F16: return launch_tiles<Elt::F16, false, false, 128, 128, 2, 2>(a, f32, s);
-        default: return launch_tiles<Elt::Fp4, false, false, 128, 128, 2, 2>(a, f32, s);
+    if (getenv("TILE") && atoi(getenv("TILE")) == 7) {
+    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, false, false, 64, 256, 1, 4, 1>(a, f32, s);
+    if (elt == Elt::F16) return launch_tiles<Elt::F16, false, false, 64, 256, 1, 4, 1>(a, f32, s);
+    return launch_tiles<Elt::Fp4, false, false, 64, 256, 1, 4, 1>(a, f32, s);
     }
+    if (getenv("TILE") && atoi(getenv("TILE")) == 6) {
+    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, false, false, 64, 128, 1, 4, 2>(a, f32, s);
+    if (elt == Elt::F16) return launch_tiles<Elt::F16, false, false, 64, 128, 1, 4, 2>(a, f32, s);
+    return launch_tiles<Elt::Fp4, false, false, 64, 128, 1, 4, 2>(a, f32, s);
+    }
+    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, false, false) }
+    if (elt == Elt::F16) { VARIANTS(Elt::F16, false, false) }
+    if (elt == Elt::Fp4) { VARIANTS(Elt::Fp4, false, false) }
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_grouped_grad_a(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, false, true, 128, 128, 2, 2>(a, f32, s);
-    return launch_tiles<Elt::F16, false, true, 128, 128, 2, 2>(a, f32, s);
+    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, false, true) }
+    VARIANTS(Elt::F16, false, true)
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_grouped_grad_b(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, true, true, 128, 128, 2, 2>(a, f32, s);
-    return launch_tiles<Elt::F16, true, true, 128, 128, 2, 2>(a, f32, s);
+    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, true, true) }
+    VARIANTS(Elt::F16, true, true)
+    return hipErrorInvalidValue;
 }
 
 }  // namespace qrmoe
