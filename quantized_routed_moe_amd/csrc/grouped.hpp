@@ -31,6 +31,7 @@ struct GroupedArgs {
     void *out;
     int64_t out_ld;            // elements
     int32_t sweep;             // column tiles of one workgroup (few rows an expert)
+    int32_t group_m, run;      // order of the tiles (grouped_mm.hip)
     int32_t n_tiles, m_tiles;  // column tiles; row tiles per expert (grad_b only)
 };
 
@@ -101,6 +102,16 @@ struct TileList {
         }
         inc = wave_incl_scan(c);
         total = __builtin_amdgcn_readlane(inc, 63);
+    }
+    // Where group g (of 0 .. E + 2) begins.
+    __device__ __forceinline__ int bound_of(int g) const {
+        const int l = g / per, i = g - l * per;
+        if (per > kHeld) return __builtin_amdgcn_readlane(bound(i), l);
+        int v = 0;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (j == i) v = __builtin_amdgcn_readlane(held[j], l);
+        return v;
     }
     // t < total
     __device__ __forceinline__ RowTile find(int t) const {

@@ -12,8 +12,8 @@
 // tile.  A stream of copies (global -> LDS, no registers) runs ahead of the
 // arithmetic by the depth of an LDS ring, from one tile into the next: the
 // first steps of a tile arrive while the tile before is stored.
+#include <algorithm>
 #include <type_traits>
-#include <cstdlib>
 
 #include "grouped.hpp"
 
@@ -70,22 +70,16 @@ __device__ __forceinline__ int afresh(int v) {
     return v;
 }
 
-// Place in the list of tiles of a workgroup's b-th turn.  Workgroups go round
-// the eight XCDs; runs of RUN consecutive tiles (kGroupM row tiles advancing
-// together through RUN / kGroupM column tiles) go to one XCD, so that the
-// tiles that run behind one L2 at a time share their operands, and long and
-// short groups spread over all XCDs.  (Whole experts to each XCD instead: the
-// gradient of eight experts of 710 .. 4702 rows took 794 us, the XCDs being
-// done after 215 .. 1034.)
-constexpr int kGroupM = 4;
-template <int RUN>
-__device__ __forceinline__ int xcd_tile(int b) {
+// Place in the list of tiles of turn b.  Workgroups go round the eight XCDs;
+// runs of `run` consecutive tiles go to one XCD, in which group_m row tiles
+// advance together through the columns.
+__device__ __forceinline__ int xcd_tile(int b, int run) {
     const int i = b / kXcds;
-    return (i / RUN * kXcds + b % kXcds) * RUN + i % RUN;
+    return (i / run * kXcds + b % kXcds) * run + i % run;
 }
-__device__ __forceinline__ void tile_mn(int t, int m_tiles, int n_tiles, int &m, int &n) {
-    const int g = t / (kGroupM * n_tiles), first = g * kGroupM, gm = min(kGroupM, m_tiles - first);
-    const int r = t - g * kGroupM * n_tiles;
+__device__ __forceinline__ void tile_mn(int t, int group_m, int m_tiles, int n_tiles, int &m, int &n) {
+    const int g = t / (group_m * n_tiles), first = g * group_m, gm = min(group_m, m_tiles - first);
+    const int r = t - g * group_m * n_tiles;
     m = first + r % gm;
     n = r / gm;
 }
@@ -103,7 +97,6 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
     constexpr bool FP4 = ELT == Elt::Fp4;
     constexpr int kStages = 2;
     constexpr int XB = BM * kSlab, YB = BN * kSlab;
-    constexpr int kRun = kCus / kXcds * PER_CU;
     typedef Stager<BM, NW, XCOL> SX;
     typedef Stager<BN, NW, YCOL> SY;
     typedef typename Out<ELT, F32>::T T;
@@ -112,18 +105,21 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
     constexpr int kHalves = F32 && FP4 && NI > 1 ? 2 : 1;
     constexpr int kOutCols = BN / kHalves, kOutBytes = 32 * kOutCols * (int)sizeof(T);
     constexpr int kScaleBytes = FP4 ? 2 * (BM + BN) * 16 : 0;
-    __shared__ __align__(1024) uint8_t smem[kStages * (XB + YB) + kOutBytes + kScaleBytes];
-    uint8_t *const sout = smem + kStages * (XB + YB), *const sscale = sout + kOutBytes;
+    constexpr int kLds = 163840 / PER_CU;
+    constexpr int kOutBlocks = kStages * (XB + YB) + WM * kOutBytes + kScaleBytes <= kLds ? WM : 1;  // at a time
+    __shared__ __align__(1024) uint8_t smem[kStages * (XB + YB) + kOutBlocks * kOutBytes + kScaleBytes];
+    uint8_t *const sout = smem + kStages * (XB + YB), *const sscale = sout + kOutBlocks * kOutBytes;
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
     // ---- the list of tiles
-    const TileList<BM> list(a.offsets, XCOL ? 0 : a.E, XCOL ? 0 : a.P);
+    const TileList<BM> list(a.offsets, a.E, a.P);
     const int total = XCOL ? a.E * a.m_tiles * a.n_tiles : list.total * a.n_tiles;
+    const int run = a.run ? a.run : max((total + kXcds - 1) / kXcds, 1);
     auto find = [&](int turn, Tile &t) -> bool {
-        const int at = xcd_tile<kRun>(blockIdx.x + turn * gridDim.x);
+        const int at = xcd_tile(blockIdx.x + turn * gridDim.x, run);
         if (at >= total) {
             t = Tile{0, 0, 0, 0, 0, 0};
             return false;
@@ -132,13 +128,13 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         if constexpr (XCOL) {
             const int each = a.m_tiles * a.n_tiles;
             t.e = at / each;
-            tile_mn(at - t.e * each, a.m_tiles, a.n_tiles, mt, nt);
-            t.row0 = min(max(a.offsets[t.e], 0), a.P);
-            t.depth = max(min(max(a.offsets[t.e + 1], 0), a.P) - t.row0, 0);
+            tile_mn(at - t.e * each, a.group_m, a.m_tiles, a.n_tiles, mt, nt);
+            t.row0 = list.bound_of(t.e + 1);
+            t.depth = max(list.bound_of(t.e + 2) - t.row0, 0);
             t.m0 = mt * BM;
             t.rows = min(a.M - t.m0, BM);
         } else {
-            tile_mn(at, list.total, a.n_tiles, mt, nt);
+            tile_mn(at, a.group_m, list.total, a.n_tiles, mt, nt);
             const RowTile r = list.find(mt);
             const bool none = r.expert < 0 || r.expert >= a.E;
             t.e = none ? 0 : r.expert;
@@ -274,7 +270,9 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         look_ahead();
     };
 
-    // One step's copies into ring stage stg: begin, kCopies times send, end.
+    // One step's copies into ring stage stg: begin, kCopies times send, end.  The stream goes on to the next tile when a
+    // tile's last step has been sent for; with four-bit operands only when the next step is, because that last step's
+    // scales are still to be read.
     constexpr int kCopies = SX::kLoads + SY::kLoads;
     struct Copy {
         i32x4 rx, ry;
@@ -282,6 +280,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
     };
     const uint32_t lds0 = lds_addr(smem);
     auto begin_copy = [&](int stg) {
+        if (FP4 && cleft == 0 && more) next_tile();
         const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + stg * (XB + YB));
         return Copy{dma_rsrc(cx), dma_rsrc(cy), base + wave * (SX::kLoads * 1024),
                     base + XB + wave * (SY::kLoads * 1024)};
@@ -306,7 +305,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         cy += cy_step;
         ++cstep;
         cleft = max(cleft - (XCOL || YCOL ? kStep : kSlab), 0);
-        if (cleft == 0 && more) next_tile();
+        if (!FP4 && cleft == 0 && more) next_tile();
         load_src();
     };
 
@@ -380,7 +379,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         const int wrow = wm * LIVE * 32, wcol = wn * NI * 32;
         const int steps = steps_of(t);
         i32x4 xf[2][LIVE], yf[2][NI];
-        int qx[2][LIVE], qy[2][NI];
+        int qx[LIVE], qy[NI];  // block scales of this step, read for the next as soon as they have served
         f32x16 acc[LIVE][NI];
 #pragma unroll
         for (int i = 0; i < LIVE; ++i)
@@ -394,13 +393,13 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
             else
                 xf[B][I - NI] = XCOL ? read_col(tx, BM, wrow + (I - NI) * 32, kk) : read_row(tx, wrow + (I - NI) * 32, kk);
         };
-        auto read_scale = [&](auto buf, auto idx, int sb, int odd) {
-            constexpr int B = decltype(buf)::value, I = decltype(idx)::value;
+        auto read_scale = [&](auto idx, int sb, int odd) {
+            constexpr int I = decltype(idx)::value;
             const uint8_t *s = sscale + sb * (BM + BN) * 16 + odd * 8 + half * 4;
             const int r = I < NI ? BM + wcol + I * 32 + l32 : wrow + (I - NI) * 32 + l32;
             const int v = *reinterpret_cast<const int *>(s + r * 16);
-            if constexpr (I < NI) qy[B][I] = v;
-            else qx[B][I - NI] = v;
+            if constexpr (I < NI) qy[I] = v;
+            else qx[I - NI] = v;
         };
         // group kk out of buffer kk & 1; meanwhile group `next` of stage s into the other, in the step's last group the
         // next step's scales, and this wave's copies
@@ -410,12 +409,15 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
             constexpr int kSend = kLast ? kCopies : 0;
             unroll<kMf>([&](auto m_c) {
                 constexpr int m = decltype(m_c)::value, i = m / NI, j = m % NI;
-                acc[i][j] = mfma32<ELT, kk>(yf[B][j], xf[B][i], acc[i][j], FP4 ? qy[0][j] : 0, FP4 ? qx[0][i] : 0);
+                acc[i][j] = mfma32<ELT, kk>(yf[B][j], xf[B][i], acc[i][j], FP4 ? qy[j] : 0, FP4 ? qx[i] : 0);
                 unroll<(m + 1) * kReads / kMf - m * kReads / kMf>([&](auto r_c) {
                     constexpr std::integral_constant<int, m * kReads / kMf + decltype(r_c)::value> idx{};
                     read_one(std::integral_constant<int, B ^ 1>{}, idx, s, next);
-                    if constexpr (FP4 && kLast) read_scale(std::integral_constant<int, 1>{}, idx, sb, odd);
                 });
+                if constexpr (FP4 && kLast) {
+                    if constexpr (j == NI - 1) read_scale(std::integral_constant<int, NI + i>{}, sb, odd);
+                    if constexpr (i == LIVE - 1) read_scale(std::integral_constant<int, j>{}, sb, odd);
+                }
                 unroll<(m + 1) * kSend / kMf - m * kSend / kMf>([&](auto c_c) {
                     send(c, std::integral_constant<int, m * kSend / kMf + decltype(c_c)::value>{});
                 });
@@ -429,7 +431,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         if (steps > 0)
             unroll<kReads>([&](auto i) {
                 read_one(c0, i, stg, 0);
-                if constexpr (FP4) read_scale(c0, i, sbuf, 0);
+                if constexpr (FP4) read_scale(i, sbuf, 0);
             });
         // (after the tile's last step the operands read ahead are not used: the next tile reads its own)
 #pragma unroll 1
@@ -447,12 +449,6 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
             stg ^= 1;
             group(c3, stg, 0, sbuf, (k + 1) & 1, c);
             end_copy();
-            if constexpr (FP4) {
-#pragma unroll
-                for (int i = 0; i < LIVE; ++i) qx[0][i] = qx[1][i];
-#pragma unroll
-                for (int j = 0; j < NI; ++j) qy[0][j] = qy[1][j];
-            }
         }
 
         // ---- out, through LDS in blocks of 32 rows, so that a wave stores
@@ -464,12 +460,11 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         constexpr int kNh = NI / kHalves;
         const int tid = afresh(threadIdx.x), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
         T *out = (T *)a.out + (XCOL ? ((int64_t)t.e * a.M + t.m0) * a.out_ld : (int64_t)t.m0 * a.out_ld) + t.n0;
-        unroll<LIVE * WM * kHalves>([&](auto part_c) {
+        unroll<LIVE * (WM / kOutBlocks) * kHalves>([&](auto part_c) {
             constexpr int part = decltype(part_c)::value, h = part % kHalves, i = part / kHalves % LIVE,
-                          w = part / kHalves / LIVE;
-            const int r0 = (w * LIVE + i) * 32;
-            if (r0 >= t.rows) return;
-            if (wm == w) {
+                          w0 = part / kHalves / LIVE * kOutBlocks;  // blocks i of the wave rows w0 .. w0 + kOutBlocks - 1
+            if ((w0 * LIVE + i) * 32 >= t.rows) return;
+            if (wm >= w0 && wm < w0 + kOutBlocks) {
 #pragma unroll
                 for (int j = 0; j < kNh; ++j)
 #pragma unroll
@@ -479,19 +474,23 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
 #pragma unroll
                         for (int u = 0; u < 4; ++u) v[u] = Out<ELT, F32>::cvt(acc[i][h * kNh + j][4 * q + u]);
                         const int slot = (n / kPer) ^ (l32 & (kPieces - 1));
-                        *reinterpret_cast<T4 *>(sout + (l32 * kPieces + slot) * 16 + (n % kPer) * (int)sizeof(T)) = v;
+                        *reinterpret_cast<T4 *>(sout + (((wm - w0) * 32 + l32) * kPieces + slot) * 16 +
+                                                (n % kPer) * (int)sizeof(T)) = v;
                     }
             }
             lds_barrier();
 #pragma unroll
-            for (int s = 0; s < 32 * kPieces / (NW * 64); ++s) {
+            for (int s = 0; s < kOutBlocks * 32 * kPieces / (NW * 64); ++s) {
                 const int p = s * NW * 64 + tid, r = p / kPieces, c = p % kPieces;
+                const int m = ((w0 + r / 32) * LIVE + i) * 32 + r % 32;
                 // column of piece c: pieces of a wave column's half stand together
                 const int n = kHalves == 1 ? c * kPer
                                            : (c * kPer / (kNh * 32) * NI + h * kNh) * 32 + c * kPer % (kNh * 32);
-                if (r0 + r < t.rows && t.n0 + n < a.N)
-                    *reinterpret_cast<i32x4 *>(out + (int64_t)(r0 + r) * a.out_ld + n) =
-                        *reinterpret_cast<const i32x4 *>(sout + (r * kPieces + (c ^ (r & (kPieces - 1)))) * 16);
+                // not kept in the caches, which hold the operands
+                if (m < t.rows && t.n0 + n < a.N)
+                    __builtin_nontemporal_store(
+                        *reinterpret_cast<const i32x4 *>(sout + (r * kPieces + (c ^ (r & (kPieces - 1)))) * 16),
+                        reinterpret_cast<i32x4 *>(out + (int64_t)m * a.out_ld + n));
             }
             lds_barrier();
         });
@@ -533,64 +532,83 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
 // --------------------------------------------------------------- launches
 namespace {
 
-constexpr int kVecRowsPerGroup = 4;
-
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// Row tiles of the ragged groups, at most: one part tile for each group and for the rows before and past them, and no
+// more than there are rows.
+inline int64_t row_tiles(const GroupedArgs &a, int bm) { return std::min<int64_t>(a.P, (int64_t)a.P / bm + a.E + 2); }
+
 template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN, int PER_CU>
-hipError_t launch_tiles(GroupedArgs a, bool f32, hipStream_t s) {
+hipError_t launch_tiles(GroupedArgs a, bool streaming, bool f32, hipStream_t s) {
     a.n_tiles = ceil_div(a.N, BN);
     a.m_tiles = ceil_div(a.M, BM);
-    // row tiles of the ragged groups: at most one part tile for each group and for the rows before and past them
-    const int64_t tiles = XCOL ? (int64_t)a.E * a.m_tiles * a.n_tiles : ((int64_t)a.P / BM + a.E + 2) * a.n_tiles;
+    const int64_t tiles = XCOL ? (int64_t)a.E * a.m_tiles * a.n_tiles : row_tiles(a, BM) * a.n_tiles;
     if (tiles > 0x3fffffff) return hipErrorInvalidValue;
-    constexpr int kRun = kCus / kXcds * PER_CU;
-    const int64_t all = (tiles + kXcds * kRun - 1) / (kXcds * kRun) * (kXcds * kRun);
-    const dim3 grid((unsigned)(all < kCus * PER_CU ? all : kCus * PER_CU));
+    a.group_m = streaming ? 1 : 8;
+    a.run = streaming ? 0 : kCus / kXcds * PER_CU;
+    const dim3 grid(kCus * PER_CU), block(WM * WN * 64);
     if (f32)
-        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, true>, grid, dim3(WM * WN * 64), s, a);
+        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, true>, grid, block, s, a);
     else
-        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, false>, grid, dim3(WM * WN * 64), s, a);
+        klaunch(grouped_gemm_kernel<ELT, XCOL, YCOL, BM, BN, WM, WN, PER_CU, false>, grid, block, s, a);
     return hipGetLastError();
+}
+
+// Mean rows of a group up to which the weights, read for each group anew, are
+// what a call waits for: tiles then follow the weights through memory, one row
+// tile at a time, an eighth of the list to each XCD.  Above, the XCDs share
+// the list in runs of one tile a CU, eight row tiles by a few columns, which
+// share operands behind one L2 whatever the groups' sizes.  Measured, bf16:
+// 48 rows of 4096 x 2048 795 us against 925, 192 rows of 4096 x 4096 748
+// against 683.  (Whole experts to each XCD: the gradient of eight experts of
+// 710 .. 4702 rows took 794 us, the XCDs being done after 215 .. 1034.)
+constexpr int kStreamRows = 96;
+
+template <Elt ELT, bool YCOL>
+hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
+    const bool streaming = a.P < (int64_t)kStreamRows * a.E;
+    // The largest tile moves the least between L2 and LDS for its arithmetic,
+    // the smallest wastes the least on short groups and fills the chip with
+    // few tiles.  48 rows of 4096 x 2048 by 64x128 / 128x128 / 256x256 tiles:
+    // 795 / 860 / 980 us; 192 rows of 4096 x 4096: 930 / 690 / 600.
+    // Four-bit operands stop at 128x256, of which all registers hold (192 rows
+    // of 4096 x 4096 by 64x128 / 128x256: 1163 / 883 us; 48 rows 538 / 497).
+    constexpr int BM = ELT == Elt::Fp4 ? 128 : 256;
+    const bool fills = row_tiles(a, BM) * ceil_div(a.N, 256) >= kCus;
+    if (fills && (ELT == Elt::Fp4 || !streaming)) return launch_tiles<ELT, false, YCOL, BM, 256, 2, 4, 1>(a, streaming, f32, s);
+    return launch_tiles<ELT, false, YCOL, 64, 128, 1, 4, 2>(a, streaming, f32, s);
 }
 
 }  // namespace
 
-#define VARIANTS(E, XC, YC) \
-    switch (getenv("TILE") ? atoi(getenv("TILE")) : 0) { \
-        case 0: return launch_tiles<E, XC, YC, 128, 128, 2, 2, 2>(a, f32, s); \
-        case 1: return launch_tiles<E, XC, YC, 256, 256, 2, 4, 1>(a, f32, s); \
-        case 5: return launch_tiles<E, XC, YC, 256, 256, 2, 2, 1>(a, f32, s); \
-        default: break; \
-    }
 hipError_t launch_grouped_mm(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    if (a.P <= kVecRowsPerGroup * a.E) return launch_grouped_vec(a, elt, f32, s);
-    if (getenv("TILE") && atoi(getenv("TILE")) == 7) {
-    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, false, false, 64, 256, 1, 4, 1>(a, f32, s);
-    if (elt == Elt::F16) return launch_tiles<Elt::F16, false, false, 64, 256, 1, 4, 1>(a, f32, s);
-    return launch_tiles<Elt::Fp4, false, false, 64, 256, 1, 4, 1>(a, f32, s);
-    }
-    if (getenv("TILE") && atoi(getenv("TILE")) == 6) {
-    if (elt == Elt::Bf16) return launch_tiles<Elt::Bf16, false, false, 64, 128, 1, 4, 2>(a, f32, s);
-    if (elt == Elt::F16) return launch_tiles<Elt::F16, false, false, 64, 128, 1, 4, 2>(a, f32, s);
-    return launch_tiles<Elt::Fp4, false, false, 64, 128, 1, 4, 2>(a, f32, s);
-    }
-    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, false, false) }
-    if (elt == Elt::F16) { VARIANTS(Elt::F16, false, false) }
-    if (elt == Elt::Fp4) { VARIANTS(Elt::Fp4, false, false) }
-    return hipErrorInvalidValue;
+    // Few tiles leave CUs idle; the streaming kernel spreads a few rows' weights
+    // over all of them, but reads them again for every 16 rows.  Tiles of 64x128
+    // against it, 4096 x 4096 of 256 experts top-6, bf16: one token 62 / 41 us,
+    // four 154 / 144, eight 253 / 266, 32 719 / 762; four-bit: one token 23 /
+    // 17, two 25 / 29, 32 224 / 250.  One expert, bf16: 16 rows 40 / 18, 64 rows
+    // 40 / 58.
+    const int64_t tiles = row_tiles(a, 64) * ceil_div(a.N, 128);
+    if (tiles <= kCus * (elt == Elt::Fp4 ? 1 : 3) && a.P <= 16 * (int64_t)a.E) return launch_grouped_vec(a, elt, f32, s);
+    if (elt == Elt::Bf16) return launch_ragged<Elt::Bf16, false>(a, f32, s);
+    if (elt == Elt::F16) return launch_ragged<Elt::F16, false>(a, f32, s);
+    return launch_ragged<Elt::Fp4, false>(a, f32, s);
 }
 
 hipError_t launch_grouped_grad_a(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, false, true) }
-    VARIANTS(Elt::F16, false, true)
-    return hipErrorInvalidValue;
+    if (elt == Elt::Bf16) return launch_ragged<Elt::Bf16, true>(a, f32, s);
+    return launch_ragged<Elt::F16, true>(a, f32, s);
 }
 
 hipError_t launch_grouped_grad_b(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    if (elt == Elt::Bf16) { VARIANTS(Elt::Bf16, true, true) }
-    VARIANTS(Elt::F16, true, true)
-    return hipErrorInvalidValue;
+    // 64 experts of 192 rows, 4096 x 4096, by 128x128 / 256x256 tiles: 1147 / 862 us.
+    const bool fills = (int64_t)a.E * ceil_div(a.M, 256) * ceil_div(a.N, 256) >= kCus;
+    auto go = [&](auto e) {
+        constexpr Elt E = decltype(e)::value;
+        return fills ? launch_tiles<E, true, true, 256, 256, 2, 4, 1>(a, false, f32, s)
+                     : launch_tiles<E, true, true, 128, 128, 2, 2, 2>(a, false, f32, s);
+    };
+    return elt == Elt::Bf16 ? go(std::integral_constant<Elt, Elt::Bf16>{}) : go(std::integral_constant<Elt, Elt::F16>{});
 }
 
 }  // namespace qrmoe
