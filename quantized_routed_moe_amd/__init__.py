@@ -302,9 +302,11 @@ class Profiler:
 from .layer import MoELayer  # noqa: E402
 from .expert_ops import (grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_dequantize,  # noqa: E402
                          mxfp4_grouped_mm, mxfp4_quantize, swiglu, swiglu_grad, swiglu_mxfp4)
+from .experts import Mxfp4Experts, Routing, expert_ffn  # noqa: E402
 
 __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Profiler", "make_shape", "workspace_bytes",
            "pack_weights", "layer_forward", "layer_forward_static", "STATIC_SCRATCH_BYTES", "workspace_init", "workspace_flags", "check_hash_table", "matrix_bytes",
            "abi_version", "FMT_Q8", "FMT_Q2", "FLAG_BAD_TOKEN", "FLAG_BAD_TABLE_ENTRY", "FLAG_REPEATED_EXPERT", "ROUTE_LEARNED", "ROUTE_HASH", "ROUTE_HASH_SCORED", "EXPORTED",
            "LIB_PATH", "Grouped", "grouped_mm", "grouped_mm_grad_a", "grouped_mm_grad_b", "mxfp4_quantize",
-           "mxfp4_dequantize", "mxfp4_grouped_mm", "swiglu", "swiglu_mxfp4", "swiglu_grad"]
+           "mxfp4_dequantize", "mxfp4_grouped_mm", "swiglu", "swiglu_mxfp4", "swiglu_grad",
+           "Routing", "expert_ffn", "Mxfp4Experts"]

@@ -145,6 +145,65 @@ def test_grad_b(name, n, k, gather):
             close(db[e], d.t() @ ra[i:j], d.abs().t() @ ra[i:j].abs(), j - i, f"{name} {dtype} expert {e}")
 
 
+def many_tiles(sizes, n, k, seed):
+    """Operands on the GPU for groups of more tiles than there are CUs, with gathered rows."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    offsets = offsets_of(sizes)
+    pairs, src = offsets[-1], 901
+    a = torch.randn(src, k, device="cuda", generator=g).to(BF16)
+    b = (torch.randn(len(sizes), n, k, device="cuda", generator=g) / k**0.5).to(BF16)
+    dc = torch.randn(pairs, n, device="cuda", generator=g).to(BF16)
+    rows = torch.randint(0, src, (pairs,), device="cuda", generator=g, dtype=torch.int32)
+    return a, b, dc, rows, offsets
+
+
+def close_each(got, want_of, sizes, offsets, depth_of, whole):
+    """close() group by group, the 64-bit product on the GPU; whole: got[e] is a group's matrix, else rows of it."""
+    for e, n in enumerate(sizes):
+        if n or whole:
+            x, y = want_of(e, slice(offsets[e], offsets[e + 1]))
+            part = got[e] if whole else got[offsets[e] : offsets[e + 1]]
+            close(part, (x @ y).cpu(), (x.abs() @ y.abs()).cpu(), max(depth_of(e), 1), f"group {e}")
+
+
+MANY = [
+    ([3000, 0, 517, 2100, 260, 1, 900], 2056, 200),                 # long groups: the largest tiles, several a workgroup
+    ([2900, 1031], 2056, 72),                                       # tiles of two steps
+    ([1200, 1900], 2824, 40),                                       # tiles of one step, the ring deeper than the tile
+    ([(i * 37) % 61 for i in range(200)], 520, 328),                # short groups, many empty
+    ([(i * 53) % 290 for i in range(64)], 1032, 136),               # groups around a tile's size
+]
+
+
+@pytest.mark.parametrize("sizes,n,k", MANY)
+def test_more_tiles_than_workgroups(sizes, n, k):
+    """Every workgroup takes several tiles in turn, of unlike groups: forward, both gradients."""
+    qr = _qr()
+    a, b, dc, rows, offsets = many_tiles(sizes, n, k, n + k)
+    o, at = dev(offsets), rows.long()
+    c = qr.grouped_mm(a, b, o, rows=rows)
+    close_each(c, lambda e, s: (a[at[s]].double(), b[e].double().t()), sizes, offsets, lambda e: k, False)
+    da = qr.grouped_mm_grad_a(dc, b, o, dtype=FP32)
+    close_each(da, lambda e, s: (dc[s].double(), b[e].double()), sizes, offsets, lambda e: n, False)
+    for gather in (True, False):
+        x = a[at] if not gather else a
+        db = qr.grouped_mm_grad_b(dc, x, o, rows=rows if gather else None)
+        close_each(db, lambda e, s: (dc[s].double().t(), a[at[s]].double()), sizes, offsets, lambda e: sizes[e], True)
+
+
+@pytest.mark.parametrize("sizes,n,k", [(s, n, 32 * k) for (s, n, _), k in zip(MANY, (7, 16, 25, 33, 17))])
+def test_mxfp4_more_tiles_than_workgroups(sizes, n, k):
+    """The same for the four-bit product, with one to five steps a tile (odd counts end in half a pair of scales)."""
+    qr = _qr()
+    a, b, _, rows, offsets = many_tiles(sizes, n, k, n + k)
+    qa, qb = qr.mxfp4_quantize(a), qr.mxfp4_quantize(b)
+    va, vb = qr.mxfp4_dequantize(*qa, dtype=BF16), qr.mxfp4_dequantize(*qb, dtype=BF16)
+    at = rows.long()
+    for out in (BF16, FP32):
+        c = qr.mxfp4_grouped_mm(*qa, *qb, dev(offsets), rows=rows, dtype=out)
+        close_each(c, lambda e, s: (va[at[s]].double(), vb[e].double().t()), sizes, offsets, lambda e: k, False)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 def test_strided_operands_and_padding_are_not_read(dtype):
     """Rows of a, dc and of the outputs may be strided; what lies between them, NaN here, is neither read into a
