@@ -12,6 +12,15 @@
 // tile.  A stream of copies (global -> LDS, no registers) runs ahead of the
 // arithmetic by the depth of an LDS ring, from one tile into the next: the
 // first steps of a tile arrive while the tile before is stored.
+//
+// What bounds them on an MI355X.  Long groups: the matrix units at the clock
+// the power limit leaves (8192^3 bf16: 1290 TFLOP/s, the library 1311 with the
+// units 87% busy at 1.58 GHz), and how fast 64 KB a step come from the L2s
+// (1.7 us a step of a 256x256 tile; 1.2 us with nothing to fetch).  Short
+// groups: reading the weights (48 rows an expert, 4096 x 2048 of 256: 5.2 TB/s).
+// grad_b of short groups: writing the gradients and, with three steps a tile,
+// the copies' latency (64 experts of 192 rows, 4096 x 4096: 865 us; without
+// fetching 592, without storing 786).
 #include <algorithm>
 #include <type_traits>
 
@@ -95,8 +104,11 @@ template <Elt ELT, bool XCOL, bool YCOL, int BM, int BN, int WM, int WN, int PER
 __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void grouped_gemm_kernel(GroupedArgs a) {
     constexpr int NW = WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr bool FP4 = ELT == Elt::Fp4;
-    constexpr int kStages = 2;
     constexpr int XB = BM * kSlab, YB = BN * kSlab;
+    // LDS ring of two steps.  (Three, which the 64x128 tile leaves room for: 48 rows an expert 966 us against 866, 161
+    // rows of one expert 41 against 43.)  The scales of four-bit operands are read for the last step that the copies
+    // have reached, which is the next one with two.
+    constexpr int kStages = 2;
     typedef Stager<BM, NW, XCOL> SX;
     typedef Stager<BN, NW, YCOL> SY;
     typedef typename Out<ELT, F32>::T T;
@@ -163,8 +175,8 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
     bool more = false;           // nt is a tile
     const uint8_t *cx, *cy;      // bases, advanced by one step at a time
     int64_t cx_step, cy_step;
-    constexpr int kScaleRows = FP4 ? (BM + BN + NW * 64 - 1) / (NW * 64) : 1;  // scale rows of this thread
-    const uint8_t *ps[kScaleRows];                                           // null: no row
+    constexpr int kScaleRows = FP4 ? ((BM + BN) * 4 + NW * 64 - 1) / (NW * 64) : 1;  // rows this thread loads scales of
+    const uint8_t *ps[kScaleRows];                                                 // null: no row
     i32x4 ws[kScaleRows];
     int nsrc[SX::kLoads], nsrc_scale[kScaleRows];  // gathered: the next tile's source rows, -1 for none
     int src[SY::kLoads];                           // grad_b, gathered: the next step's source rows
@@ -190,7 +202,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
                 if constexpr (FP4) {
 #pragma unroll
                     for (int i = 0; i < kScaleRows; ++i) {
-                        const int r = i * NW * 64 + tid;
+                        const int r = (i * NW * 64 + tid) >> 2;
                         nsrc_scale[i] = r < BM && r < nt.rows ? a.rows[nt.row0 + r] : -1;
                     }
                 }
@@ -256,7 +268,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
             const int blocks = a.depth / 32;
 #pragma unroll
             for (int i = 0; i < kScaleRows; ++i) {
-                const int r = i * NW * 64 + tid;
+                const int r = (i * NW * 64 + tid) >> 2;
                 ps[i] = nullptr;
                 if (r < BM) {
                     const int s = !a.rows ? (r < ct.rows ? ct.row0 + r : -1) : nsrc_scale[i];
@@ -309,38 +321,42 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         load_src();
     };
 
-    // four-bit operands: block scales, 16 bytes (two steps) of each row at a time, as words
-    // [step][half]: the blocks half, 2 + half, 4 + half, 6 + half that a lane's four MFMAs of a step need
-    auto load_scales = [&](int pair) {  // zeros past the row's end and for no row
+    // four-bit operands: block scales.  64 bytes of each row (eight steps) are loaded at a time, 16 by each of four
+    // lanes, and go to LDS a pair of steps at a time, by the lane that has it, as words [step][half]: the blocks half,
+    // 2 + half, 4 + half, 6 + half that a lane's four MFMAs of a step need.
+    auto load_scales = [&](int pair) {  // four pairs from `pair` on; zeros past the row's end and for no row
         if constexpr (FP4) {
-            const int blocks = a.depth / 32;
+            const int blocks = a.depth / 32, at = 16 * (pair + (tid & 3));
 #pragma unroll
             for (int i = 0; i < kScaleRows; ++i) {
                 ws[i] = i32x4{};
                 if (!ps[i]) continue;
-                if (16 * pair + 16 <= blocks) {
-                    __builtin_memcpy(&ws[i], ps[i] + 16 * pair, 16);
+                if (at + 16 <= blocks) {
+                    __builtin_memcpy(&ws[i], ps[i] + at, 16);
                 } else {
 #pragma unroll 1
-                    for (int j = blocks - 16 * pair - 1; j >= 0; --j)  // shift in from the last to the first
-                        ws[i] = i32x4{ws[i].x << 8 | ps[i][16 * pair + j],
-                                      (int)__builtin_amdgcn_alignbyte(ws[i].y, ws[i].x, 3),
+                    for (int j = blocks - 1; j >= at; --j)  // shift in from the last to the first
+                        ws[i] = i32x4{ws[i].x << 8 | ps[i][j], (int)__builtin_amdgcn_alignbyte(ws[i].y, ws[i].x, 3),
                                       (int)__builtin_amdgcn_alignbyte(ws[i].z, ws[i].y, 3),
                                       (int)__builtin_amdgcn_alignbyte(ws[i].w, ws[i].z, 3)};
                 }
             }
         }
     };
-    auto store_scales = [&](int buf) {
+    auto store_scales = [&](int buf, int pair) {
         if constexpr (FP4) {
+            if (((tid ^ pair) & 3) != 0) return;
             i32x4 *d = reinterpret_cast<i32x4 *>(sscale + buf * (BM + BN) * 16);
 #pragma unroll
-            for (int i = 0; i < kScaleRows; ++i)
-                if (i * NW * 64 + tid < BM + BN)
-                    d[i * NW * 64 + tid] = i32x4{(int)__builtin_amdgcn_perm(ws[i].y, ws[i].x, 0x06040200),
-                                                 (int)__builtin_amdgcn_perm(ws[i].y, ws[i].x, 0x07050301),
-                                                 (int)__builtin_amdgcn_perm(ws[i].w, ws[i].z, 0x06040200),
-                                                 (int)__builtin_amdgcn_perm(ws[i].w, ws[i].z, 0x07050301)};
+            for (int i = 0; i < kScaleRows; ++i) {
+                const i32x4 w = ws[i];
+                const int r = (i * NW * 64 + tid) >> 2;
+                if (r < BM + BN)
+                    d[r] = i32x4{(int)__builtin_amdgcn_perm(w.y, w.x, 0x06040200),
+                                 (int)__builtin_amdgcn_perm(w.y, w.x, 0x07050301),
+                                 (int)__builtin_amdgcn_perm(w.w, w.z, 0x06040200),
+                                 (int)__builtin_amdgcn_perm(w.w, w.z, 0x07050301)};
+            }
         }
     };
 
@@ -438,15 +454,23 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         for (int k = 0; k < steps; ++k) {
             // the copies of the step after this one are under way: ct is its tile, cstep - 1 its place there
             const bool fresh = FP4 && ((cstep - 1) & 1) == 0;  // it begins a pair
-            if (fresh) load_scales((cstep - 1) >> 1);
+            const int pair = (cstep - 1) >> 1;
+            if (fresh && (pair & 3) == 0) load_scales(pair);
             group(c0, stg, 1, 0, 0, Copy{});
             group(c1, stg, 2, 0, 0, Copy{});
             group(c2, stg, 3, 0, 0, Copy{});
-            if (fresh) store_scales(sbuf ^= 1);
-            wait_vm<0>();
+            if constexpr (FP4) {
+                // keeps the compiler from moving the three groups' MFMAs past the branch, behind all their reads
+#pragma unroll
+                for (int i = 0; i < LIVE; ++i)
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
+            }
+            if (fresh) store_scales(sbuf ^= 1, pair);
+            wait_vm<(kStages - 2) * kCopies>();
             lds_barrier();
             const Copy c = begin_copy(stg);
-            stg ^= 1;
+            stg = stg + 1 == kStages ? 0 : stg + 1;
             group(c3, stg, 0, sbuf, (k + 1) & 1, c);
             end_copy();
         }
@@ -508,11 +532,11 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
     };
     if (FP4) {
         load_scales(0);
-        store_scales(0);
+        store_scales(0, 0);
     }
     copy_step(0);
     wait_vm<0>();
-    copy_step(1);
+    for (int s = 1; s < kStages; ++s) copy_step(s);
     lds_barrier();
     Tile t;
     for (int turn = 0; find(turn, t); ++turn) {
@@ -571,8 +595,9 @@ hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
     // the smallest wastes the least on short groups and fills the chip with
     // few tiles.  48 rows of 4096 x 2048 by 64x128 / 128x128 / 256x256 tiles:
     // 795 / 860 / 980 us; 192 rows of 4096 x 4096: 930 / 690 / 600.
-    // Four-bit operands stop at 128x256, of which all registers hold (192 rows
-    // of 4096 x 4096 by 64x128 / 128x256: 1163 / 883 us; 48 rows 538 / 497).
+    // Four-bit operands stop at 128x256: with 256x256 the scales on their way
+    // do not fit the registers (192 rows of 4096 x 4096 by 64x128 / 128x256 /
+    // 256x256: 1172 / 883 / 1238 us; 48 rows 553 / 506 / 629).
     constexpr int BM = ELT == Elt::Fp4 ? 128 : 256;
     const bool fills = row_tiles(a, BM) * ceil_div(a.N, 256) >= kCus;
     if (fills && (ELT == Elt::Fp4 || !streaming)) return launch_tiles<ELT, false, YCOL, BM, 256, 2, 4, 1>(a, streaming, f32, s);
