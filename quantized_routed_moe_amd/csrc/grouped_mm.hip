@@ -586,7 +586,7 @@ hipError_t launch_tiles(GroupedArgs a, bool streaming, bool f32, hipStream_t s) 
 // 48 rows of 4096 x 2048 795 us against 925, 192 rows of 4096 x 4096 748
 // against 683.  (Whole experts to each XCD: the gradient of eight experts of
 // 710 .. 4702 rows took 794 us, the XCDs being done after 215 .. 1034.)
-constexpr int kStreamRows = 96;
+constexpr int kStreamRows = 96, kFewRows = 16;
 
 template <Elt ELT, bool YCOL>
 hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
@@ -600,7 +600,9 @@ hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
     // 256x256: 1172 / 883 / 1238 us; 48 rows 553 / 506 / 629).
     constexpr int BM = ELT == Elt::Fp4 ? 128 : 256;
     const bool fills = row_tiles(a, BM) * ceil_div(a.N, 256) >= kCus;
-    if (fills && (ELT == Elt::Fp4 || !streaming)) return launch_tiles<ELT, false, YCOL, BM, 256, 2, 4, 1>(a, streaming, f32, s);
+    const bool few = a.P < (int64_t)kFewRows * a.E;  // four-bit, 1 / 8 rows of 4096 x 4096 by 64x128: 219 / 427 us against 226 / 437
+    if (fills && (ELT == Elt::Fp4 ? !few : !streaming))
+        return launch_tiles<ELT, false, YCOL, BM, 256, 2, 4, 1>(a, streaming, f32, s);
     return launch_tiles<ELT, false, YCOL, 64, 128, 1, 4, 2>(a, streaming, f32, s);
 }
 
