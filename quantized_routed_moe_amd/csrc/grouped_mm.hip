@@ -597,10 +597,11 @@ hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
     // 795 / 860 / 980 us; 192 rows of 4096 x 4096: 930 / 690 / 600.
     // Four-bit operands stop at 128x256: with 256x256 the scales on their way
     // do not fit the registers (192 rows of 4096 x 4096 by 64x128 / 128x256 /
-    // 256x256: 1172 / 883 / 1238 us; 48 rows 553 / 506 / 629).
+    // 256x256: 1172 / 883 / 1238 us; 48 rows 553 / 506 / 629), and take the
+    // smallest tile for a few rows (1 / 8: 209 / 404 us against 226 / 437).
     constexpr int BM = ELT == Elt::Fp4 ? 128 : 256;
     const bool fills = row_tiles(a, BM) * ceil_div(a.N, 256) >= kCus;
-    const bool few = a.P < (int64_t)kFewRows * a.E;  // four-bit, 1 / 8 rows of 4096 x 4096 by 64x128: 219 / 427 us against 226 / 437
+    const bool few = a.P < (int64_t)kFewRows * a.E;
     if (fills && (ELT == Elt::Fp4 ? !few : !streaming))
         return launch_tiles<ELT, false, YCOL, BM, 256, 2, 4, 1>(a, streaming, f32, s);
     return launch_tiles<ELT, false, YCOL, 64, 128, 1, 4, 2>(a, streaming, f32, s);
