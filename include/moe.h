@@ -286,9 +286,10 @@ enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_F16 = 3 };
 #define MOE_MAX_PAIRS (1 << 20) /* rows of a grouped call */
 
 /* The groups of a grouped product.  offsets is a device array; its entries
- * are clamped to [0, pairs] where the kernels read them, and rows before
- * offsets[0] or past offsets[n_experts] belong to no group: their outputs
- * are zeros.  rows, if given, is a device array of one entry for each pair:
+ * are clamped to [0, pairs] where the kernels read them, and one that is less
+ * than an entry before it counts as the largest of those (its group is empty).
+ * Rows before offsets[0] or past the largest entry belong to no group: their
+ * outputs are zeros.  rows, if given, is a device array of one entry for each pair:
  * pair p reads row rows[p] of a (src_rows rows; an entry outside [0,
  * src_rows) reads a row of zeros); without it pair p reads row p. */
 typedef struct moe_grouped {

@@ -5,8 +5,10 @@
 // Rows (pairs) are grouped by expert: group e holds rows offsets[e] ..
 // offsets[e+1].  The offsets live on the device, so a grid is sized by a
 // bound the host knows and every workgroup finds its tile itself.  Whatever
-// the offsets hold, they are clamped to [0, P] where they are read, so no
-// kernel leaves its buffers; rows of no group come out as zeros.
+// the offsets hold, they are clamped to [0, P] where they are read and taken
+// no lower than the ones before them, so that no kernel leaves its buffers,
+// no two groups share a row and the host's bound holds; rows of no group come
+// out as zeros.
 #pragma once
 
 #include "common.hpp"
@@ -80,25 +82,69 @@ struct TileList {
     static constexpr int kHeld = 5;
     const int32_t *off;
     int E, P, per, inc, total;
+    int before;  // the largest bound of the lanes below, where some bound is less than one before it; else 0
     int held[kHeld + 1];
 
-    __device__ __forceinline__ int bound(int i) const {  // of group i of this lane's, 0 .. per
+    static __device__ __forceinline__ int tiles(int rows) { return (rows + BM - 1) / BM; }
+    __device__ __forceinline__ int read(int i) const {  // bound of group i of this lane's, 0 .. per, as it stands
         const int g = min((int)(threadIdx.x & 63) * per + i, E + 2);
         const int v = min(max(off[min(max(g - 1, 0), E)], 0), P);
         return g == 0 ? 0 : g > E + 1 ? P : v;
     }
-    __device__ __forceinline__ TileList(const int32_t *o, int e, int p) : off(o), E(e), P(p) {
+    __device__ __forceinline__ int bound(int i) const {
+        int v = before;
+        for (int j = 0; j <= i; ++j) v = max(v, read(j));
+        return v;
+    }
+    // The largest of v over the lanes below this one.
+    static __device__ __forceinline__ int most_below(int v) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int t = __shfl_up(v, o);
+            if (lane >= o) v = max(v, t);
+        }
+        const int t = __shfl_up(v, 1);
+        return lane > 0 ? t : 0;
+    }
+    __device__ __forceinline__ TileList(const int32_t *o, int e, int p) : off(o), E(e), P(p), before(0) {
         per = (E + 2 + 63) / 64;
         int c = 0;
+        bool falls = false;  // offsets that run backwards: then, and only then, the running maximum is formed
         if (per <= kHeld) {
 #pragma unroll
-            for (int i = 0; i <= kHeld; ++i) held[i] = bound(min(i, per));
+            for (int i = 0; i <= kHeld; ++i) held[i] = read(min(i, per));
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) c += (max(held[i + 1] - held[i], 0) + BM - 1) / BM;
+            for (int i = 0; i < kHeld; ++i) falls |= held[i + 1] < held[i];
+            if (__ballot(falls)) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) held[i + 1] = max(held[i + 1], held[i]);
+                before = most_below(held[kHeld]);
+#pragma unroll
+                for (int i = 0; i <= kHeld; ++i) held[i] = max(held[i], before);
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) c += tiles(held[i + 1] - held[i]);
         } else {
 #pragma unroll
             for (int i = 0; i <= kHeld; ++i) held[i] = 0;
-            for (int i = 0; i < per; ++i) c += (max(bound(i + 1) - bound(i), 0) + BM - 1) / BM;
+            int lo = read(0);
+            for (int i = 1; i <= per; ++i) {
+                const int hi = read(i);
+                falls |= hi < lo;
+                c += tiles(max(hi - lo, 0));
+                lo = max(lo, hi);
+            }
+            if (__ballot(falls)) {
+                before = most_below(lo);
+                c = 0;
+                lo = bound(0);
+                for (int i = 1; i <= per; ++i) {
+                    const int hi = max(lo, read(i));
+                    c += tiles(hi - lo);
+                    lo = hi;
+                }
+            }
         }
         inc = wave_incl_scan(c);
         total = __builtin_amdgcn_readlane(inc, 63);
@@ -120,7 +166,7 @@ struct TileList {
         RowTile r{-1, 0, 0};
         bool found = false;
         auto look = [&](int i, int lo, int n) {
-            const int c = (n + BM - 1) / BM;
+            const int c = tiles(n);
             if (!found && skip < c) {
                 found = true;
                 r = RowTile{l * per + i - 1, lo + skip * BM, min(n - skip * BM, BM)};
@@ -131,12 +177,14 @@ struct TileList {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int lo = __builtin_amdgcn_readlane(held[i], l);
-                look(i, lo, max(__builtin_amdgcn_readlane(held[i + 1], l) - lo, 0));
+                look(i, lo, __builtin_amdgcn_readlane(held[i + 1], l) - lo);
             }
         } else {
+            int lo = bound(0);
             for (int i = 0; i < per && !found; ++i) {
-                const int lo = __builtin_amdgcn_readlane(bound(i), l);
-                look(i, lo, max(__builtin_amdgcn_readlane(bound(i + 1), l) - lo, 0));
+                const int hi = max(lo, read(i + 1)), first = __builtin_amdgcn_readlane(lo, l);
+                look(i, first, __builtin_amdgcn_readlane(hi, l) - first);
+                lo = hi;
             }
         }
         return r;

@@ -50,34 +50,33 @@ __global__ __launch_bounds__(kVecWaves * 64) void grouped_vec_kernel(GroupedArgs
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int p = blockIdx.x / a.n_tiles, nb = (blockIdx.x - p * a.n_tiles) * (16 * NT * a.sweep);
 
-    // ---- the group of row p: how many groups end at or before it, where it starts and ends
-    int before = 0;
-    uint32_t start = 0, end = a.P;
-    const int32_t first = a.offsets[0];
-    for (int i = lane; i < a.E; i += 64) {
-        const int o = min(max(a.offsets[i + 1], 0), a.P);
-        if (o <= p) {
-            ++before;
-            start = max(start, (uint32_t)o);
-        } else {
-            end = min(end, (uint32_t)o);
+    // ---- the group of row p: the first offset past p ends it, the largest of those before that one begins it (an
+    // offset less than one before it counts as that one)
+    int start = 0, next = a.E + 1, row1 = a.P;  // next: the offset that ends the group; E + 1: none, past the last group
+    bool found = false;
+    constexpr int kAhead = 5;  // 320 offsets in flight
+    for (int i0 = 0; i0 <= a.E && !found; i0 += 64 * kAhead) {
+        int o[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) o[j] = a.offsets[min(i0 + 64 * j + lane, a.E)];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int v = i0 + 64 * j + lane > a.E ? a.P : min(max(o[j], 0), a.P);
+            const uint64_t past = __ballot(v > p);
+            if (found) continue;
+            const int at = past ? __ffsll((long long)past) - 1 : 64;
+            start = lane < at ? max(start, v) : start;
+            if (past) {
+                found = true;
+                next = min(i0 + 64 * j + at, a.E + 1);
+                row1 = __builtin_amdgcn_readlane(v, at);
+            }
         }
     }
-    before = (int)group_reduce<64>((uint32_t)before, [](uint32_t x, uint32_t y) { return x + y; });
-    start = group_reduce<64>(start, [](uint32_t x, uint32_t y) { return max(x, y); });
-    end = group_reduce<64>(end, [](uint32_t x, uint32_t y) { return min(x, y); });
-    const int e = __builtin_amdgcn_readfirstlane(before);
-    int row0 = __builtin_amdgcn_readfirstlane((int)start), row1 = __builtin_amdgcn_readfirstlane((int)end);
-    bool none = e >= a.E;  // past the last group
-    if (e == 0) {          // rows before the first group are a run of no group of their own
-        const int o0 = min(max(first, 0), a.P);
-        if (p < o0) {
-            none = true;
-            row1 = min(row1, o0);
-        } else {
-            row0 = max(row0, o0);
-        }
-    }
+    const int row0 = __builtin_amdgcn_readfirstlane(
+        (int)group_reduce<64>((uint32_t)start, [](uint32_t x, uint32_t y) { return max(x, y); }));
+    const bool none = next == 0 || next > a.E;  // before the first group or past the last
+    const int e = none ? 0 : next - 1;
     if ((p - row0) % kVecRun != 0) return;
     const int rows = min(row1 - p, kVecRun);
 

@@ -285,6 +285,71 @@ def test_offsets_are_clamped():
     torch.cuda.synchronize()
 
 
+def running_maximum(offsets, pairs):
+    """What offsets mean whatever they hold: each within [0, pairs] and no lower than the ones before it."""
+    out, most = [], 0
+    for o in offsets:
+        most = max(most, min(max(o, 0), pairs))
+        out.append(most)
+    return out
+
+
+def guarded(rows, cols, dtype):
+    """(whole, inner): an output [rows, cols] inside a buffer of sevens, with rows before and past it and columns beside it."""
+    whole = torch.full((rows + 6, cols + 16), 7.0, dtype=dtype, device="cuda")
+    return whole, whole[3 : 3 + rows, :cols]
+
+
+def guards_stand(whole, cols):
+    w = whole.cpu()
+    return bool((w[:3] == 7).all() and (w[-3:] == 7).all() and (w[:, cols:] == 7).all())
+
+
+BACKWARD = [
+    ([0, 30, 10, 10, 50], 50),                                  # a group that ends before it begins
+    ([5, 0, 40, 2, 45], 50),
+    ([50, 0, 50, 0, 50], 50),                                   # every other group the whole of it
+    ([-9, 60, 3, 70, 20], 64),                                  # out of range as well
+    ([0] + [(i * 97) % 301 for i in range(40)], 300),           # more bounds than a lane each of one group
+    ([0, 700, 100, 650, 900, 20, 1100], 1100),                  # long groups
+    ([(i * 389) % 1201 for i in range(401)], 1200),             # more groups than are held in registers
+]
+
+
+@pytest.mark.parametrize("offsets,pairs", BACKWARD)
+@pytest.mark.parametrize("n,k", [(40, 96), (520, 160)])
+def test_offsets_that_run_backwards(offsets, pairs, n, k):
+    """An offset less than one before it counts as the largest of those: groups stay disjoint, every row has one
+    writer, the results are defined and nothing beside the outputs is written."""
+    qr = _qr()
+    E, g = len(offsets) - 1, gen(pairs + n)
+    o, held = dev(offsets), running_maximum(offsets, pairs)
+    a, dc = torch.randn(pairs, k, generator=g).to(BF16), torch.randn(pairs, n, generator=g).to(BF16)
+    b = (torch.randn(E, n, k, generator=g) / k**0.5).to(BF16)
+    want, mag = grouped_ref(a, b, held, None, pairs)
+    whole, c = guarded(pairs, n, BF16)
+    qr.grouped_mm(a.cuda(), b.cuda(), o, out=c)
+    close(c, want, mag, k, "c")
+    assert guards_stand(whole, n)
+    whole, da = guarded(pairs, k, FP32)
+    qr.grouped_mm_grad_a(dc.cuda(), b.cuda(), o, out=da)
+    close(da, *grouped_ref(dc, b.transpose(1, 2), held, None, pairs), n, "da")
+    assert guards_stand(whole, k)
+    whole = torch.full((E + 2, n, k), 7.0, device="cuda")
+    qr.grouped_mm_grad_b(dc.cuda(), a.cuda(), o, out=whole[1:-1])
+    assert (whole[0] == 7).all() and (whole[-1] == 7).all()
+    db = whole[1:-1].cpu()
+    for e in range(E):
+        x, y = dc[held[e] : held[e + 1]].to(FP64), a[held[e] : held[e + 1]].to(FP64)
+        close(db[e], x.t() @ y, x.abs().t() @ y.abs(), max(len(x), 1), f"db {e}")
+    qa, qb = qr.mxfp4_quantize(a.cuda()), qr.mxfp4_quantize(b.cuda())
+    va, vb = values_ref(*(t.cpu() for t in qa)), values_ref(*(t.cpu() for t in qb))
+    whole, c = guarded(pairs, n, FP32)
+    qr.mxfp4_grouped_mm(*qa, *qb, o, out=c)
+    close(c, *grouped_ref(va, vb, held, None, pairs), k, "four-bit c")
+    assert guards_stand(whole, n)
+
+
 def test_no_pairs():
     qr = _qr()
     a, b = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.randn(3, 40, 64, device="cuda").to(BF16)
