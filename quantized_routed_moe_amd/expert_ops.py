@@ -21,6 +21,20 @@ DT = {torch.float32: 1, torch.bfloat16: 2, torch.float16: 3}
 _HALF = (torch.bfloat16, torch.float16)
 
 
+class _Refusal(torch.autograd.Function):
+    """Passes a result on; differentiating through it raises.  `why` says what was asked for in vain."""
+
+    @staticmethod
+    def forward(ctx, why, out, *operands):
+        ctx.why = why
+        ctx.mark_dirty(out)
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(ctx.why)
+
+
 def _dtype(t, name, allowed):
     if t.dtype not in allowed:
         raise ValueError(f"{name}: expected one of {', '.join(map(str, allowed))}, got {t.dtype}")

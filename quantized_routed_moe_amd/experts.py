@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import torch
 
-from .expert_ops import (grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_grouped_mm, mxfp4_quantize, swiglu,
-                         swiglu_grad, swiglu_mxfp4)
+from .expert_ops import (_Refusal, grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_grouped_mm, mxfp4_quantize,
+                         swiglu, swiglu_grad, swiglu_mxfp4)
 
 
 class Routing:
@@ -58,6 +58,17 @@ class _ExpertFFN(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        with torch.no_grad():
+            grads = _ExpertFFN.gradients(ctx, dout)
+        if not torch.is_grad_enabled():
+            return (*grads, None)
+        # create_graph: the kernels leave no graph, so a derivative of these would be wrong, not merely missing
+        why = "expert_ffn cannot be differentiated twice: its gradients come from kernels without a derivative"
+        sources = (dout, *ctx.saved_tensors[:4])
+        return (*(_Refusal.apply(why, g, *sources) for g in grads), None)
+
+    @staticmethod
+    def gradients(ctx, dout):
         x, w, gate_up, down, gu, h, y = ctx.saved_tensors
         r = ctx.routing
         d = r.to_pairs(dout)
@@ -68,12 +79,12 @@ class _ExpertFFN(torch.autograd.Function):
         d_gate_up = grouped_mm_grad_b(dgu, x, r.offsets, rows=r.rows)
         # a token's gradient is the sum of its pairs', in fp32
         dx = r.to_tokens(grouped_mm_grad_a(dgu, gate_up, r.offsets, dtype=torch.float32)).sum(1)
-        return dx.to(x.dtype), dw, d_gate_up, d_down, None
+        return dx.to(x.dtype), dw, d_gate_up, d_down
 
 
 def expert_ffn(x: torch.Tensor, routing: Routing, gate_up: torch.Tensor, down: torch.Tensor) -> torch.Tensor:
     """out [T, H] fp32 of x [T, H] (bf16 or fp16); gate_up [E, 2 F, H] with the gate rows first, down [E, H, F].
-    Differentiable in x, routing.w, gate_up and down."""
+    Differentiable in x, routing.w, gate_up and down; a derivative of those gradients raises RuntimeError."""
     return _ExpertFFN.apply(x, routing.w, gate_up, down, routing)
 
 
