@@ -52,7 +52,9 @@ class _ExpertFFN(torch.autograd.Function):
         gu = grouped_mm(x, gate_up, routing.offsets, rows=routing.rows)
         h = swiglu(gu)
         y = grouped_mm(h, down, routing.offsets)
-        ctx.save_for_backward(x, w, gate_up, down, gu, h, y)
+        need_x, need_w, need_gate_up, need_down, _ = ctx.needs_input_grad
+        ctx.save_for_backward(x, w, gate_up, down, gu if need_x or need_gate_up else None, h if need_down else None,
+                              y if need_w else None)
         ctx.routing = routing
         return (routing.to_tokens(y).float() * w[:, :, None]).sum(1)
 
@@ -65,21 +67,29 @@ class _ExpertFFN(torch.autograd.Function):
         # create_graph: the kernels leave no graph, so a derivative of these would be wrong, not merely missing
         why = "expert_ffn cannot be differentiated twice: its gradients come from kernels without a derivative"
         sources = (dout, *ctx.saved_tensors[:4])
-        return (*(_Refusal.apply(why, g, *sources) for g in grads), None)
+        return (*(g if g is None else _Refusal.apply(why, g, *sources) for g in grads), None)
 
     @staticmethod
     def gradients(ctx, dout):
+        """Of x, w, gate_up and down; None, and nothing computed, for one that is not asked for."""
         x, w, gate_up, down, gu, h, y = ctx.saved_tensors
+        need_x, need_w, need_gate_up, need_down, _ = ctx.needs_input_grad
         r = ctx.routing
-        d = r.to_pairs(dout)
-        dw = (r.to_tokens(y).float() * dout[:, None]).sum(2)
-        dy = (d * w.reshape(-1)[r.perm][:, None]).to(y.dtype)
-        d_down = grouped_mm_grad_b(dy, h, r.offsets)
-        dgu = swiglu_grad(grouped_mm_grad_a(dy, down, r.offsets), gu)
-        d_gate_up = grouped_mm_grad_b(dgu, x, r.offsets, rows=r.rows)
-        # a token's gradient is the sum of its pairs', in fp32
-        dx = r.to_tokens(grouped_mm_grad_a(dgu, gate_up, r.offsets, dtype=torch.float32)).sum(1)
-        return dx.to(x.dtype), dw, d_gate_up, d_down
+        dx = dw = d_gate_up = d_down = None
+        if need_w:
+            dw = (r.to_tokens(y).float() * dout[:, None]).sum(2)
+        if need_x or need_gate_up or need_down:
+            dy = (r.to_pairs(dout) * w.reshape(-1)[r.perm][:, None]).to(down.dtype)
+        if need_down:
+            d_down = grouped_mm_grad_b(dy, h, r.offsets)
+        if need_x or need_gate_up:
+            dgu = swiglu_grad(grouped_mm_grad_a(dy, down, r.offsets), gu)
+        if need_gate_up:
+            d_gate_up = grouped_mm_grad_b(dgu, x, r.offsets, rows=r.rows)
+        if need_x:
+            # a token's gradient is the sum of its pairs', in fp32
+            dx = r.to_tokens(grouped_mm_grad_a(dgu, gate_up, r.offsets, dtype=torch.float32)).sum(1).to(x.dtype)
+        return dx, dw, d_gate_up, d_down
 
 
 def expert_ffn(x: torch.Tensor, routing: Routing, gate_up: torch.Tensor, down: torch.Tensor) -> torch.Tensor:

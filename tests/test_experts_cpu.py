@@ -104,3 +104,28 @@ def test_a_second_derivative_is_refused(calls, first, linear):
     d, = torch.autograd.grad(loss, v[first], create_graph=True)
     with pytest.raises(RuntimeError, match="expert_ffn.*twice"):
         torch.autograd.grad(d.square().sum(), list(v.values()), allow_unused=True)
+
+
+NEEDED = {  # operators of the backward pass that each gradient cannot do without
+    "w": set(),
+    "x": {"swiglu_grad", "grouped_mm_grad_a"},
+    "gate_up": {"swiglu_grad", "grouped_mm_grad_a", "grouped_mm_grad_b"},
+    "down": {"grouped_mm_grad_b"},
+}
+
+
+@pytest.mark.parametrize("wanted", [("x",), ("w",), ("gate_up",), ("down",), ("x", "w"), ("gate_up", "down"),
+                                    ("w", "down"), ("x", "gate_up")])
+def test_only_the_gradients_asked_for_are_computed(calls, wanted):
+    """Frozen banks cost nothing in the backward pass: neither their products nor the memory of their gradients."""
+    v = leaves(*(n for n in ("x", "w", "gate_up", "down") if n not in wanted))
+    loss = own(v).square().sum()
+    del calls[:]
+    loss.backward()
+    assert set(calls) == set().union(*(NEEDED[n] for n in wanted))
+    assert calls.count("grouped_mm_grad_b") == ("gate_up" in wanted) + ("down" in wanted)
+    assert calls.count("grouped_mm_grad_a") == ("x" in wanted) + ("x" in wanted or "gate_up" in wanted)
+    f = {n: t.detach().clone().requires_grad_() for n, t in v.items()}
+    formula(f).square().sum().backward()
+    for n, t in v.items():
+        assert near(t.grad, f[n].grad) if n in wanted else t.grad is None, n

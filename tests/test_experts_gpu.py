@@ -126,3 +126,29 @@ def test_routing_of_a_layer():
     assert off(out, want) <= 2 / 250 + 5 * 2.0**-8
     four = qr.Mxfp4Experts(gate_up.cuda(), down.cuda())(x, routing)
     assert off(four, want) <= 3 * 0.12
+
+
+@pytest.mark.parametrize("wanted", [("x", "w"), ("down",), ("w",)])
+def test_frozen_operands(wanted):
+    """The gradients that are asked for are the bits of the full backward pass; the others are None and their banks'
+    gradients are never allocated."""
+    qr = _qr()
+    T, k, E, H, F = 40, 2, 32, 512, 256
+    ids, w, x, gate_up, down = case(T, k, E, H, F, BF16, 5)
+    dout = torch.randn(T, H, generator=torch.Generator().manual_seed(6)).cuda()
+
+    def grads(asked):
+        v = {n: t.cuda().requires_grad_(n in asked) for n, t in zip(("x", "w", "gate_up", "down"), (x, w, gate_up, down))}
+        out = qr.expert_ffn(v["x"], qr.Routing.from_ids(ids.cuda(), v["w"], E), v["gate_up"], v["down"])
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out.backward(dout)
+        return {n: t.grad for n, t in v.items()}, torch.cuda.max_memory_allocated() - before
+
+    whole, _ = grads(("x", "w", "gate_up", "down"))
+    got, peak = grads(wanted)
+    for n, g in got.items():
+        assert torch.equal(g, whole[n]) if n in wanted else g is None, n
+    if "down" not in wanted:
+        assert peak < down.numel() * 2  # the smaller bank's gradient
