@@ -24,6 +24,17 @@ class Routing:
         self.place = torch.empty_like(self.perm)
         self.place[self.perm] = torch.arange(self.perm.numel(), device=perm.device)
 
+    def _tensors(self) -> tuple:
+        return self.perm, self.offsets, self.rows, self.place
+
+    @classmethod
+    def _of(cls, tensors: tuple, w: torch.Tensor) -> "Routing":
+        """Of what _tensors() gave."""
+        r = cls.__new__(cls)
+        r.perm, r.offsets, r.rows, r.place = tensors
+        r.w, r.k = w, w.shape[1]
+        return r
+
     @classmethod
     def from_layer(cls, debug: dict) -> "Routing":
         """Of what MoELayer.forward_debug returns."""
@@ -54,8 +65,7 @@ class _ExpertFFN(torch.autograd.Function):
         y = grouped_mm(h, down, routing.offsets)
         need_x, need_w, need_gate_up, need_down, _ = ctx.needs_input_grad
         ctx.save_for_backward(x, w, gate_up, down, gu if need_x or need_gate_up else None, h if need_down else None,
-                              y if need_w else None)
-        ctx.routing = routing
+                              y if need_w else None, *routing._tensors())
         return (routing.to_tokens(y).float() * w[:, :, None]).sum(1)
 
     @staticmethod
@@ -72,9 +82,9 @@ class _ExpertFFN(torch.autograd.Function):
     @staticmethod
     def gradients(ctx, dout):
         """Of x, w, gate_up and down; None, and nothing computed, for one that is not asked for."""
-        x, w, gate_up, down, gu, h, y = ctx.saved_tensors
+        x, w, gate_up, down, gu, h, y, *routing = ctx.saved_tensors
         need_x, need_w, need_gate_up, need_down, _ = ctx.needs_input_grad
-        r = ctx.routing
+        r = Routing._of(routing, w)
         dx = dw = d_gate_up = d_down = None
         if need_w:
             dw = (r.to_tokens(y).float() * dout[:, None]).sum(2)

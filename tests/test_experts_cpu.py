@@ -129,3 +129,21 @@ def test_only_the_gradients_asked_for_are_computed(calls, wanted):
     formula(f).square().sum().backward()
     for n, t in v.items():
         assert near(t.grad, f[n].grad) if n in wanted else t.grad is None, n
+
+
+@pytest.mark.parametrize("name", ["perm", "offsets", "rows", "place"])
+def test_routing_rewritten_between_forward_and_backward(calls, name):
+    """Written into, the backward pass raises as torch does for any saved tensor; with another tensor put in its
+    place, the forward call's own is used."""
+    v = leaves()
+    want = torch.autograd.grad(own(v).square().sum(), list(v.values()))
+    r = qr.Routing.from_ids(IDS, v["w"], E)
+    out = qr.expert_ffn(v["x"], r, v["gate_up"], v["down"])
+    setattr(r, name, getattr(r, name).flip(0))
+    for a, b in zip(torch.autograd.grad(out.square().sum(), list(v.values())), want):
+        assert torch.equal(a, b)
+    r = qr.Routing.from_ids(IDS, v["w"], E)
+    out = qr.expert_ffn(v["x"], r, v["gate_up"], v["down"])
+    getattr(r, name).copy_(getattr(r, name).flip(0))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.square().sum().backward()
