@@ -8,12 +8,19 @@ expert e owns rows offsets[e] .. offsets[e+1] - 1 (any number), `offsets` and
 `rows` being int32 tensors on the GPU.  Work is enqueued on `stream` (the
 current stream by default) without synchronising; a result that is not passed
 in as `out` is allocated for that stream.
+
+The calls build no graph: expert_ffn is the differentiable one.  With an
+operand that asks for a gradient the result can be used, but differentiating
+through it raises (at once where it is written to `out` or the operand carries
+a forward-mode tangent); codes and scales are integers, which torch does not
+differentiate.
 """
 from __future__ import annotations
 
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import Grouped, _check, _layout, _lib
 
@@ -33,6 +40,21 @@ class _Refusal(torch.autograd.Function):
     @staticmethod
     def backward(ctx, *grads):
         raise RuntimeError(ctx.why)
+
+
+def _graph(call, out, *operands):
+    """None; where an operand asks for a gradient, why the result's derivative will be refused.  Raises where it could
+    not be: the result is written to the caller's `out`, or an operand carries a forward-mode tangent."""
+    if torch.is_grad_enabled():
+        for t in operands:
+            if t.requires_grad:
+                why = f"{call} builds no graph, but an operand asks for a gradient (detach it, or use expert_ffn)"
+                if out is not None:
+                    raise RuntimeError(why)
+                return why
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in operands):
+        raise RuntimeError(f"{call} has no forward-mode derivative, but an operand carries a tangent")
+    return None
 
 
 def _dtype(t, name, allowed):
@@ -147,10 +169,11 @@ def grouped_mm(a, b, offsets, rows=None, out=None, dtype=None, stream=None):
     index, raw, side = _target(a, "a", stream)
     P = a.shape[0] if rows is None else rows.shape[0]
     g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
-    out, ldc = _output(out, (P, N), dtype or a.dtype, (a.dtype, torch.float32), a, side)
+    graph = _graph("grouped_mm", out, a, b)
+    result, ldc = _output(out, (P, N), dtype or a.dtype, (a.dtype, torch.float32), a, side)
     _check(_lib.moe_grouped_mm(ctypes.byref(g), DT[a.dtype], _pointer(a, "a", index), lda, _pointer(b, "b", index),
-                               _pointer(out, "out", index), DT[out.dtype], ldc, raw), "moe_grouped_mm")
-    return out
+                               _pointer(result, "out", index), DT[result.dtype], ldc, raw), "moe_grouped_mm")
+    return result if graph is None else _Refusal.apply(graph, result, a, b)
 
 
 def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
@@ -164,11 +187,12 @@ def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
     index, raw, side = _target(dc, "dc", stream)
     P = dc.shape[0]
     g = _groups(offsets, None, 0, E, P, N, K, index)
-    out, lda = _output(out, (P, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
+    graph = _graph("grouped_mm_grad_a", out, dc, b)
+    result, lda = _output(out, (P, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
     _check(_lib.moe_grouped_mm_grad_a(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
-                                      _pointer(b, "b", index), _pointer(out, "out", index), DT[out.dtype], lda, raw),
-           "moe_grouped_mm_grad_a")
-    return out
+                                      _pointer(b, "b", index), _pointer(result, "out", index), DT[result.dtype], lda,
+                                      raw), "moe_grouped_mm_grad_a")
+    return result if graph is None else _Refusal.apply(graph, result, dc, b)
 
 
 def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=None):
@@ -186,11 +210,12 @@ def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=No
         raise ValueError(f"offsets: expected [experts + 1], got {tuple(offsets.shape)}")
     E = offsets.shape[0] - 1
     g = _groups(offsets, rows, a.shape[0], E, P, N, K, index)
-    out, _ = _output(out, (E, N, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
+    graph = _graph("grouped_mm_grad_b", out, dc, a)
+    result, _ = _output(out, (E, N, K), dtype or dc.dtype, (dc.dtype, torch.float32), dc, side)
     _check(_lib.moe_grouped_mm_grad_b(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
-                                      _pointer(a, "a", index), lda, _pointer(out, "out", index), DT[out.dtype], raw),
-           "moe_grouped_mm_grad_b")
-    return out
+                                      _pointer(a, "a", index), lda, _pointer(result, "out", index), DT[result.dtype],
+                                      raw), "moe_grouped_mm_grad_b")
+    return result if graph is None else _Refusal.apply(graph, result, dc, a)
 
 
 def _code_outputs(shape, codes, scales, like, stream):
@@ -286,10 +311,11 @@ def swiglu(gu, out=None, stream=None):
     """h = silu(gate) * up of gu [rows, 2 F] = [gate | up] (fp32, bf16 or fp16), [rows, F] of the same type."""
     rows, ffn, ldg = _gate_up(gu)
     index, raw, side = _target(gu, "gu", stream)
-    out, ldh = _output(out, (rows, ffn), gu.dtype, (gu.dtype,), gu, side)
-    _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(out, "out", index), ldh,
+    graph = _graph("swiglu", out, gu)
+    result, ldh = _output(out, (rows, ffn), gu.dtype, (gu.dtype,), gu, side)
+    _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(result, "out", index), ldh,
                            raw), "moe_swiglu")
-    return out
+    return result if graph is None else _Refusal.apply(graph, result, gu)
 
 
 def swiglu_mxfp4(gu, codes=None, scales=None, stream=None):
@@ -309,7 +335,8 @@ def swiglu_grad(dh, gu, out=None, stream=None):
     rows, ffn, ldg = _gate_up(gu)
     ldd = _matrix(dh, "dh", gu.dtype, rows, ffn)
     index, raw, side = _target(gu, "gu", stream)
-    out, ldo = _output(out, (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu, side)
+    graph = _graph("swiglu_grad", out, dh, gu)
+    result, ldo = _output(out, (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu_grad(DT[gu.dtype], _pointer(dh, "dh", index), ldd, _pointer(gu, "gu", index), ldg, rows,
-                                ffn, _pointer(out, "out", index), ldo, raw), "moe_swiglu_grad")
-    return out
+                                ffn, _pointer(result, "out", index), ldo, raw), "moe_swiglu_grad")
+    return result if graph is None else _Refusal.apply(graph, result, dh, gu)

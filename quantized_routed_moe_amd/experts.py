@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import torch
 
-from .expert_ops import (_Refusal, grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_grouped_mm, mxfp4_quantize,
-                         swiglu, swiglu_grad, swiglu_mxfp4)
+from .expert_ops import (_graph, _Refusal, grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_grouped_mm,
+                         mxfp4_quantize, swiglu, swiglu_grad, swiglu_mxfp4)
 
 
 class Routing:
@@ -110,15 +110,18 @@ def expert_ffn(x: torch.Tensor, routing: Routing, gate_up: torch.Tensor, down: t
 
 class Mxfp4Experts:
     """The same FFN on four-bit weights, quantised once from 16- or 32-bit banks; activations are quantised on the
-    way, x once for all its experts and the hidden activation as it is made."""
+    way, x once for all its experts and the hidden activation as it is made.  Differentiable in routing.w only."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor):
         self.gate_up, self.down = mxfp4_quantize(gate_up), mxfp4_quantize(down)
 
     def forward(self, x: torch.Tensor, routing: Routing) -> torch.Tensor:
         """out [T, H] fp32 of x [T, H] (fp32, bf16 or fp16)."""
+        graph = _graph("Mxfp4Experts", None, x)
         gu = mxfp4_grouped_mm(*mxfp4_quantize(x), *self.gate_up, routing.offsets, rows=routing.rows)
         y = mxfp4_grouped_mm(*swiglu_mxfp4(gu), *self.down, routing.offsets)
+        if graph is not None:
+            y = _Refusal.apply(graph, y, x)
         return (routing.to_tokens(y).float() * routing.w[:, :, None]).sum(1)
 
     __call__ = forward

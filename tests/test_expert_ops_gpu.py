@@ -686,3 +686,49 @@ def test_other_streams_graphs_and_repeated_calls():
         again = chain()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(again, want)), f"eager call {i}"
+
+
+def test_operands_that_ask_for_a_gradient():
+    """No call passes for a constant: its result has the same bits, and differentiating through it raises; so does an
+    `out` that torch could not follow, and a forward-mode tangent."""
+    from torch.autograd import forward_ad
+
+    qr = _qr()
+    a, b, offsets, rows, pairs = make_case("ragged", 40, 64, BF16, True, 25)
+    a, b, rows, o = a.cuda(), b.cuda(), rows.cuda(), dev(offsets)
+    dc = torch.randn(pairs, 40, generator=gen(26)).to(BF16).cuda()
+    gu = torch.randn(pairs, 64, generator=gen(27)).cuda()
+    dh = torch.randn(pairs, 32, generator=gen(28)).cuda()
+    calls = [("grouped_mm", lambda x, y, **kw: qr.grouped_mm(x, y, o, rows=rows, **kw), a, b),
+             ("grouped_mm_grad_a", lambda x, y, **kw: qr.grouped_mm_grad_a(x, y, o, **kw), dc, b),
+             ("grouped_mm_grad_b", lambda x, y, **kw: qr.grouped_mm_grad_b(x, y, o, rows=rows, **kw), dc, a),
+             ("swiglu_grad", lambda x, y, **kw: qr.swiglu_grad(x, y, **kw), dh, gu),
+             ("swiglu", lambda x, y, **kw: qr.swiglu(y, **kw), dh, gu)]
+    for name, f, x, y in calls:
+        want = f(x, y)
+        assert not want.requires_grad
+        for which in (0, 1):
+            if name == "swiglu" and which == 0:
+                continue
+            args = [t.detach().clone().requires_grad_(i == which) for i, t in enumerate((x, y))]
+            got = f(*args)
+            assert torch.equal(got, want)
+            with pytest.raises(RuntimeError, match=f"{name} builds no graph"):
+                (got.float().sum() + args[which].float().sum()).backward()
+            with pytest.raises(RuntimeError, match=f"{name} builds no graph"):
+                f(*args, out=torch.empty_like(want))
+            with torch.no_grad():
+                assert not f(*args, out=torch.empty_like(want)).requires_grad
+            with forward_ad.dual_level():
+                args = [forward_ad.make_dual(t, torch.ones_like(t)) if i == which else t for i, t in enumerate((x, y))]
+                with pytest.raises(RuntimeError, match=f"{name} has no forward-mode"):
+                    f(*args)
+                assert torch.equal(f(x, y), want)
+    experts = qr.Mxfp4Experts(b.new_zeros(3, 64, 64).requires_grad_(), b.new_zeros(3, 64, 32))
+    w = torch.rand(5, 2, device="cuda").requires_grad_()
+    r = qr.Routing.from_ids(torch.tensor([[0, 1]] * 5, device="cuda"), w, 3)
+    x = a[:5].detach().clone().requires_grad_()
+    with pytest.raises(RuntimeError, match="Mxfp4Experts builds no graph"):
+        experts(x, r).sum().backward()
+    experts(x.detach(), r).sum().backward()  # the weights' gradient is torch's own
+    assert w.grad.shape == w.shape
