@@ -7,7 +7,9 @@ C ABI of include/moe.h.  Rows are (token, expert) pairs sorted by expert:
 expert e owns rows offsets[e] .. offsets[e+1] - 1 (any number), `offsets` and
 `rows` being int32 tensors on the GPU.  Work is enqueued on `stream` (the
 current stream by default) without synchronising; a result that is not passed
-in as `out` is allocated for that stream.
+in as `out` is allocated for that stream.  On a `stream` other than the one
+that an operand was made on, the caller has that stream wait for it; the
+operands' memory is not given to anyone else before the call has run.
 
 The calls build no graph: expert_ffn is the differentiable one.  With an
 operand that asks for a gradient the result can be used, but differentiating
@@ -125,6 +127,14 @@ def _new(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _hold(stream, *tensors):
+    """Keeps the memory of a call's tensors from being reused, once they are dropped, before `stream` has run it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _output(out, shape, dtype, allowed, like, stream):
     """(out, its row stride): a given output checked, or a new one."""
     if out is None:
@@ -173,6 +183,7 @@ def grouped_mm(a, b, offsets, rows=None, out=None, dtype=None, stream=None):
     result, ldc = _output(out, (P, N), dtype or a.dtype, (a.dtype, torch.float32), a, side)
     _check(_lib.moe_grouped_mm(ctypes.byref(g), DT[a.dtype], _pointer(a, "a", index), lda, _pointer(b, "b", index),
                                _pointer(result, "out", index), DT[result.dtype], ldc, raw), "moe_grouped_mm")
+    _hold(side, a, b, offsets, rows, out)
     return result if graph is None else _Refusal.apply(graph, result, a, b)
 
 
@@ -192,6 +203,7 @@ def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
     _check(_lib.moe_grouped_mm_grad_a(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(b, "b", index), _pointer(result, "out", index), DT[result.dtype], lda,
                                       raw), "moe_grouped_mm_grad_a")
+    _hold(side, dc, b, offsets, out)
     return result if graph is None else _Refusal.apply(graph, result, dc, b)
 
 
@@ -215,6 +227,7 @@ def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=No
     _check(_lib.moe_grouped_mm_grad_b(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(a, "a", index), lda, _pointer(result, "out", index), DT[result.dtype],
                                       raw), "moe_grouped_mm_grad_b")
+    _hold(side, dc, a, offsets, rows, out)
     return result if graph is None else _Refusal.apply(graph, result, dc, a)
 
 
@@ -255,6 +268,7 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     _check(_lib.moe_mxfp4_quantize(DT[x.dtype], _pointer(x, "x", index), ld, rows, cols,
                                    _pointer(codes, "codes", index), _plain(scales, "scales", index), raw),
            "moe_mxfp4_quantize")
+    _hold(side, x, codes, scales)
     return codes, scales
 
 
@@ -275,6 +289,7 @@ def mxfp4_dequantize(codes, scales, out=None, dtype=torch.float32, stream=None):
     _check(_lib.moe_mxfp4_dequantize(_pointer(codes, "codes", index), _plain(scales, "scales", index),
                                      codes.numel() * 2 // cols, cols, DT[out.dtype], _pointer(out, "out", index), ld,
                                      raw), "moe_mxfp4_dequantize")
+    _hold(side, codes, scales, out)
     return out
 
 
@@ -297,6 +312,7 @@ def mxfp4_grouped_mm(a_codes, a_scales, b_codes, b_scales, offsets, rows=None, o
                                      _plain(a_scales, "a_scales", index), _pointer(b_codes, "b_codes", index),
                                      _plain(b_scales, "b_scales", index), _pointer(out, "out", index), DT[out.dtype], ldc,
                                      raw), "moe_mxfp4_grouped_mm")
+    _hold(side, a_codes, a_scales, b_codes, b_scales, offsets, rows, out)
     return out
 
 
@@ -315,6 +331,7 @@ def swiglu(gu, out=None, stream=None):
     result, ldh = _output(out, (rows, ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(result, "out", index), ldh,
                            raw), "moe_swiglu")
+    _hold(side, gu, out)
     return result if graph is None else _Refusal.apply(graph, result, gu)
 
 
@@ -327,6 +344,7 @@ def swiglu_mxfp4(gu, codes=None, scales=None, stream=None):
     codes, scales = _code_outputs((rows, ffn), codes, scales, gu, side)
     _check(_lib.moe_swiglu_mxfp4(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn,
                                  _pointer(codes, "codes", index), _plain(scales, "scales", index), raw), "moe_swiglu_mxfp4")
+    _hold(side, gu, codes, scales)
     return codes, scales
 
 
@@ -339,4 +357,5 @@ def swiglu_grad(dh, gu, out=None, stream=None):
     result, ldo = _output(out, (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu_grad(DT[gu.dtype], _pointer(dh, "dh", index), ldd, _pointer(gu, "gu", index), ldg, rows,
                                 ffn, _pointer(result, "out", index), ldo, raw), "moe_swiglu_grad")
+    _hold(side, dh, gu, out)
     return result if graph is None else _Refusal.apply(graph, result, dh, gu)

@@ -732,3 +732,63 @@ def test_operands_that_ask_for_a_gradient():
         experts(x, r).sum().backward()
     experts(x.detach(), r).sum().backward()  # the weights' gradient is torch's own
     assert w.grad.shape == w.shape
+
+
+def test_operands_dropped_while_a_side_stream_has_work():
+    """Operands, and outputs passed in, that are dropped right after a call on another stream: their memory is not
+    handed out again before the call has run."""
+    qr = _qr()
+    pairs, n, k = 300, 264, 4096
+    g = torch.Generator(device="cuda").manual_seed(29)
+    o = [0, 120, 120, pairs]
+    big = torch.randn(4096, 4096, device="cuda", generator=g)
+
+    def fresh(*shape, dtype=BF16):
+        return torch.randn(*shape, device="cuda", generator=g).to(dtype)
+
+    def codes(x):
+        return list(qr.mxfp4_quantize(x))
+
+    def rows():
+        return torch.arange(pairs, device="cuda", dtype=torch.int32).flip(0)
+
+    new = torch.empty
+    calls = [
+        (lambda s, a, b, o, r, out: qr.grouped_mm(a, b, o, rows=r, out=out, stream=s),
+         lambda: [fresh(pairs, k), fresh(3, n, k), dev(o), rows(), new(pairs, n, device="cuda", dtype=BF16)]),
+        (lambda s, d, b, o, out: qr.grouped_mm_grad_a(d, b, o, out=out, stream=s),
+         lambda: [fresh(pairs, n), fresh(3, n, k), dev(o), new(pairs, k, device="cuda", dtype=BF16)]),
+        (lambda s, d, a, o, r, out: qr.grouped_mm_grad_b(d, a, o, rows=r, out=out, stream=s),
+         lambda: [fresh(pairs, n), fresh(pairs, k), dev(o), rows(), new(3, n, k, device="cuda", dtype=BF16)]),
+        (lambda s, x, c, e: qr.mxfp4_quantize(x, c, e, stream=s),
+         lambda: [fresh(pairs, k), *codes(fresh(pairs, k))]),
+        (lambda s, c, e, out: qr.mxfp4_dequantize(c, e, out=out, stream=s),
+         lambda: [*codes(fresh(pairs, k)), new(pairs, k, device="cuda")]),
+        (lambda s, ac, ae, bc, be, o, r, out: qr.mxfp4_grouped_mm(ac, ae, bc, be, o, rows=r, out=out, stream=s),
+         lambda: [*codes(fresh(pairs, k)), *codes(fresh(3, n, k)), dev(o), rows(),
+                  new(pairs, n, device="cuda", dtype=BF16)]),
+        (lambda s, gu, out: qr.swiglu(gu, out=out, stream=s),
+         lambda: [fresh(pairs, 2 * k), new(pairs, k, device="cuda", dtype=BF16)]),
+        (lambda s, gu, c, e: qr.swiglu_mxfp4(gu, c, e, stream=s),
+         lambda: [fresh(pairs, 2 * k), *codes(fresh(pairs, k))]),
+        (lambda s, d, gu, out: qr.swiglu_grad(d, gu, out=out, stream=s),
+         lambda: [fresh(pairs, k), fresh(pairs, 2 * k), new(pairs, 2 * k, device="cuda", dtype=BF16)]),
+    ]
+    side = torch.cuda.Stream()
+    for i, (call, operands) in enumerate(calls):
+        held = operands()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                torch.mm(big, big)
+            busy = torch.cuda.Event()
+            busy.record()
+        result = call(side, *held)
+        was = {(t.data_ptr(), t.shape, t.dtype) for t in held}
+        like = [(t.shape, t.dtype) for t in held]
+        del held, result
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in like]
+        assert not busy.query(), "the side stream was not kept busy"
+        assert not was & {(t.data_ptr(), t.shape, t.dtype) for t in again}, f"call {i}"
+        del again
+        torch.cuda.synchronize()
