@@ -28,11 +28,13 @@ struct Mat {
     uintptr_t end() const { return rows > 0 ? begin() + (uintptr_t)(((rows - 1) * stride + cols) * bytes) : begin(); }
 };
 
-// Present, 16-byte aligned rows that do not overlap each other.
+// Present, 16-byte aligned rows that do not overlap each other and end within the address space (what is computed from
+// the row count afterwards does not wrap).
 int check_mat(const Mat &m) {
     if (m.rows > 0 && (!m.p || !aligned16(m.p))) return MOE_ERR_INVALID_ARG;
-    if (m.stride < m.cols || m.stride * m.bytes % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (m.stride < m.cols || m.stride > INT64_MAX / m.bytes || m.stride * m.bytes % 16 != 0) return MOE_ERR_INVALID_ARG;
     if (m.stride > kMaxStride) return MOE_ERR_UNSUPPORTED;
+    if (m.rows > INT64_MAX / (m.stride * m.bytes) || m.end() < m.begin()) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 bool overlap(const Mat &a, const Mat &b) {
@@ -58,7 +60,7 @@ int64_t a_rows(const moe_grouped *g) { return g->rows ? g->src_rows : g->pairs; 
 
 // The kernels address a gathered operand with 31-bit offsets.
 bool gather_too_long(const moe_grouped *g, int64_t stride_bytes) {
-    return g->rows && g->src_rows * stride_bytes >= (int64_t)0x7fffffff;
+    return g->rows && g->src_rows >= ((int64_t)0x7fffffff + stride_bytes - 1) / stride_bytes;
 }
 
 GroupedArgs base_args(const moe_grouped *g) {

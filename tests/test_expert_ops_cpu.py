@@ -182,3 +182,20 @@ def test_binding_checks_tensors():
     refused("dh: expected shape", qr.swiglu_grad, torch.zeros(4, 16), torch.zeros(4, 16))
     refused("dh: expected torch.float32", qr.swiglu_grad, torch.zeros(4, 8, dtype=bf), torch.zeros(4, 16))
     refused("blocks of 32", qr.swiglu_mxfp4, torch.zeros(4, 16))
+
+
+@pytest.mark.parametrize("rows", [1 << 40, 1 << 43, 1 << 44, 1 << 52, 1 << 56, 1 << 61, (1 << 62) + 1, (1 << 63) - 1])
+def test_row_counts_past_the_address_space(rows):
+    """Sizes whose bytes do not fit 64 bits, or wrap the operand's address, are refused like other impossible ones:
+    nothing computed from them wraps into a range that looks right."""
+    s = 1 << 21  # the longest stride
+    for f in (lambda: mm(rows=ROWS, src_rows=rows, lda=s), lambda: grad_b(rows=ROWS, src_rows=rows, lda=s),
+              lambda: mm(rows=ROWS, src_rows=rows), lambda: grad_b(rows=ROWS, src_rows=rows),
+              lambda: mm4(rows=ROWS, src_rows=rows), lambda: mm4(rows=ROWS, src_rows=rows, in_features=65536)):
+        assert f() in (INVALID, UNSUPPORTED)
+    if rows >= 1 << 43:  # 2^21 fp32 elements a row: 2^23 bytes
+        assert L.moe_mxfp4_quantize(FP32, A, s, rows, s, B, C, None) == INVALID
+        assert L.moe_mxfp4_dequantize(A, B, rows, s, FP32, C, s, None) == INVALID
+        assert L.moe_swiglu(FP32, A, s, rows, s // 2, B, s // 2, None) == INVALID
+        assert L.moe_swiglu_mxfp4(FP32, A, s, rows, s // 2, B, C, None) == INVALID
+        assert L.moe_swiglu_grad(FP32, A, s // 2, B, s, rows, s // 2, C, s, None) == INVALID
