@@ -37,8 +37,17 @@ int check_mat(const Mat &m) {
     if (m.rows > INT64_MAX / (m.stride * m.bytes) || m.end() < m.begin()) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
+// Whether a byte belongs to both: not where their spans are apart, nor where rows of the same stride lie side by side
+// (columns of one wide matrix).
 bool overlap(const Mat &a, const Mat &b) {
-    return a.begin() < b.end() && b.begin() < a.end() && a.begin() != a.end() && b.begin() != b.end();
+    if (a.begin() >= b.end() || b.begin() >= a.end() || a.begin() == a.end() || b.begin() == b.end()) return false;
+    const uintptr_t step = (uintptr_t)(a.stride * a.bytes);
+    if (step != (uintptr_t)(b.stride * b.bytes)) return true;
+    const uintptr_t wa = (uintptr_t)(a.cols * a.bytes), wb = (uintptr_t)(b.cols * b.bytes);
+    // where b's rows begin in those of a
+    const uintptr_t at = b.begin() >= a.begin() ? (b.begin() - a.begin()) % step
+                                                : (step - (a.begin() - b.begin()) % step) % step;
+    return at < wa || at + wb > step;
 }
 
 // The part of the checks the grouped calls share.

@@ -792,3 +792,34 @@ def test_operands_dropped_while_a_side_stream_has_work():
         assert not was & {(t.data_ptr(), t.shape, t.dtype) for t in again}, f"call {i}"
         del again
         torch.cuda.synchronize()
+
+
+def test_columns_of_one_matrix():
+    """Operands and outputs that are columns of one wide matrix share no element and are accepted; columns that do
+    share one, or rows of another stride over the same memory, are refused."""
+    qr = _qr()
+    rows, f = 70, 64
+    wide = torch.randn(rows, 6 * f, generator=gen(30)).to(BF16).cuda()
+    gu, dh = wide[:, f : 3 * f], wide[:, 3 * f : 4 * f]
+    want_h, want_g = qr.swiglu(gu.contiguous()), qr.swiglu_grad(dh.contiguous(), gu.contiguous())
+    b, o = (torch.randn(2, f, 2 * f, generator=gen(31)) / 11).to(BF16).cuda(), dev([0, 30, rows])
+    want_c = qr.grouped_mm(gu.contiguous(), b, o)
+    want_a = qr.grouped_mm_grad_a(dh.contiguous(), b, o)
+    before = wide.clone()
+    assert torch.equal(qr.swiglu(gu, out=wide[:, :f]), want_h)              # before the operand's columns
+    assert torch.equal(qr.swiglu(gu, out=wide[:, 3 * f : 4 * f]), want_h)   # right after them
+    wide[:, 3 * f : 4 * f] = before[:, 3 * f : 4 * f]
+    assert torch.equal(qr.swiglu_grad(dh, gu, out=wide[:, 4 * f :]), want_g)
+    assert torch.equal(qr.grouped_mm(gu, b, o, out=wide[:, 5 * f :]), want_c)
+    assert torch.equal(qr.grouped_mm_grad_a(dh, b, o, out=wide[:, 4 * f :]), want_a)
+    assert torch.equal(wide[:, f : 4 * f], before[:, f : 4 * f])
+    for bad in (wide[:, 8 : f + 8], wide[:, f : 2 * f], wide[:, 3 * f - 8 : 4 * f - 8], wide.view(-1, 3 * f)[:rows, :f]):
+        with pytest.raises(qr.MoEError):
+            qr.swiglu(gu, out=bad)
+    assert torch.equal(wide[:, f : 4 * f], before[:, f : 4 * f])
+    # one row further down and at the edge of the next row's columns
+    tall = torch.zeros(rows + 1, 4 * f, dtype=BF16, device="cuda")
+    tall[:rows, 2 * f :] = gu
+    assert torch.equal(qr.swiglu(tall[:rows, 2 * f :], out=tall[1:, :f]), want_h)
+    with pytest.raises(qr.MoEError):
+        qr.swiglu(tall[:rows, 2 * f :], out=tall[1:, f + 8 : 2 * f + 8])
