@@ -334,7 +334,8 @@ int moe_mxfp4_grouped_mm(const moe_grouped *g, const uint8_t *a_codes, const uin
 
 /* h = silu(gate) * up for rows of gu = [gate | up] (2 ffn elements; ffn a
  * multiple of 8, for the four-bit output of 32), and its gradient dgu =
- * [dgate | dup] from dh.  fp32, bf16 or fp16 in and out, computed in fp32. */
+ * [dgate | dup] from dh.  fp32, bf16 or fp16 in and out, computed in fp32,
+ * the sigmoid and its complement to a few units of 2^-24 for every gate. */
 int moe_swiglu(int32_t dtype, const void *gu, int64_t gu_stride, int64_t rows, int64_t ffn, void *h, int64_t h_stride,
                void *stream);
 int moe_swiglu_mxfp4(int32_t dtype, const void *gu, int64_t gu_stride, int64_t rows, int64_t ffn, uint8_t *codes,

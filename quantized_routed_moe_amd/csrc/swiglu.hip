@@ -10,9 +10,30 @@
 
 namespace qrmoe {
 
-// e^-g overflows to infinity for g < -88: s is then 0, and g s(g) = -0, the
-// limit.  g = -inf itself is NaN (inf * 0), as the formula's product is.
-__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// s(g) and 1 - s(g), each with a relative error of a few units of 2^-24
+// whatever g is: with e = e^-|g| in [0, 1] they are 1 / (1 + e) and e / (1 + e).
+//
+// e = 2^n 2^f: n is the integer nearest to -|g| log2(e), f what is left, which
+// fused multiply-adds form without the rounding of the product (its error
+// would grow as |g| 2^-24) and with the part of log2(e) that fp32 lacks.  The
+// power of n is put on last, so subnormal results come out too.  The
+// reciprocal gets one Newton step.  49152 x 2048 bf16, gradient: 175 us, as
+// with the bare exponential.
+//
+// g = -inf makes g s(g) NaN (-inf * 0), as the formula's product is.
+struct Sigmoid {
+    float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid_f(float g) {
+    constexpr double kLog2e = 1.4426950408889634;
+    constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+    const float x = fmaxf(-fabsf(g), -256.0f);  // e^-256 is 0; keeps the infinities out of what follows
+    const float n = rintf(x * kHi), f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
+    const float e = ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+    const float q = 1.0f + e, r0 = __builtin_amdgcn_rcpf(q);
+    const float r = __builtin_fmaf(__builtin_fmaf(-q, r0, 1.0f), r0, r0), er = e * r;
+    return g < 0 ? Sigmoid{er, r} : Sigmoid{r, er};
+}
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const void *gu, int64_t gu_ld, int64_t rows, int64_t ffn,
@@ -25,7 +46,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const void *gu, int64_
         load8<DT>(gu, r * gu_ld + c, g);
         load8<DT>(gu, r * gu_ld + ffn + c, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid_f(g[j]) * u[j];
+        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid_f(g[j]).s * u[j];
         store8<DT>(h, r * h_ld + c, o);
     }
 }
@@ -41,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_mxfp4_kernel(const void *gu, 
         load8<DT>(gu, r * gu_ld + c, g);
         load8<DT>(gu, r * gu_ld + ffn + c, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid_f(g[j]) * u[j];
+        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid_f(g[j]).s * u[j];
         uint32_t s;
         const uint32_t q = mxfp4_quad(o, s);
         *reinterpret_cast<uint32_t *>(codes + 4 * i) = q;
@@ -63,9 +84,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const void *dh, i
         load8<DT>(gu, r * gu_ld + ffn + c, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float s = sigmoid_f(g[j]);
-            dg[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-            du[j] = d[j] * g[j] * s;
+            const Sigmoid s = sigmoid_f(g[j]);
+            dg[j] = d[j] * u[j] * s.s * (1.0f + g[j] * s.rest);
+            du[j] = d[j] * g[j] * s.s;
         }
         store8<DT>(dgu, r * dgu_ld + c, dg);
         store8<DT>(dgu, r * dgu_ld + ffn + c, du);

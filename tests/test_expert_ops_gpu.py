@@ -587,6 +587,30 @@ def test_swiglu_and_gradient(dtype, rows, ffn):
     assert ((dgu[:, :ffn] - dg).abs() <= swiglu_tol(dg, g, dtype, terms)).all()
 
 
+@pytest.mark.parametrize("deviation", [0.1, 1.5, 16.0, 40.0])
+def test_swiglu_in_32_bits(deviation):
+    """fp32 results keep their relative precision for gates of every size.  In units of 2^-24: e^-|g| is off by 3 (a
+    unit of the last place of the exponential, a rounding), 1 + e and its reciprocal by 1 each, e / (1 + e) by 6 in
+    all; h = g s u takes two products more: 8.  du = dh g s likewise; dg's factors dh u s by 8, 1 + g (1 - s) by 8 of
+    its terms, their product by 1: 17 of the terms' magnitudes.  2^-120 covers what is below the normal range."""
+    qr = _qr()
+    g = gen(int(10 * deviation))
+    gate = torch.randn(500, 256, generator=g) * deviation
+    gate[0] = torch.linspace(-80, 80, 256)
+    gate[1] = torch.linspace(-1, 1, 256)
+    gu = torch.cat([gate, torch.randn(500, 256, generator=g)], 1)
+    dh = torch.randn(500, 256, generator=g)
+    h, dgu = qr.swiglu(gu.cuda()).cpu(), qr.swiglu_grad(dh.cuda(), gu.cuda()).cpu().to(FP64)
+    gate, up, s = swiglu_ref(gu)
+    rest, d, unit = torch.sigmoid(-gate), dh.to(FP64), 2.0**-24 * 1.001
+    want = gate * s * up
+    assert ((h.to(FP64) - want).abs() <= 8 * unit * want.abs() + 2.0**-120).all()
+    want = d * gate * s
+    assert ((dgu[:, 256:] - want).abs() <= 8 * unit * want.abs() + 2.0**-120).all()
+    want, terms = d * up * s * (1 + gate * rest), (d * up).abs() * s * (1 + gate.abs() * rest)
+    assert ((dgu[:, :256] - want).abs() <= 17 * unit * terms + 2.0**-120).all()
+
+
 def test_swiglu_gradient_against_differences():
     """Central differences of the 64-bit formula with step 2^-12: the third derivative of silu is below 1, so they
     are within h^2 / 6 of the gradient (times dh and the other factor)."""
