@@ -213,7 +213,7 @@ __device__ __forceinline__ void dma16_async(i32x4 rsrc, uint32_t lds, uint32_t v
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_ptr)p);
