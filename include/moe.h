@@ -281,7 +281,9 @@ void moe_ctx_destroy(moe_ctx *ctx);
  *    16 bytes and at most 2^21 elements.  Banks b are dense.  Outputs must
  *    not overlap inputs.
  *  - Sums are held in fp32 and rounded once to the output type, which is the
- *    operands' type or fp32. */
+ *    operands' type or fp32.  Subnormal operands keep their value; in a sum
+ *    the matrix unit aligns an fp16 one as if it were 2^-14, so the rounding
+ *    of the sum is relative to that. */
 enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_F16 = 3 };
 #define MOE_MAX_PAIRS (1 << 20) /* rows of a grouped call */
 

@@ -847,3 +847,140 @@ def test_columns_of_one_matrix():
     assert torch.equal(qr.swiglu(tall[:rows, 2 * f :], out=tall[1:, :f]), want_h)
     with pytest.raises(qr.MoEError):
         qr.swiglu(tall[:rows, 2 * f :], out=tall[1:, f + 8 : 2 * f + 8])
+
+
+# ------------------------------------- every kernel of the products, by the rule that chooses it
+def typed(sizes, n, k, dtype, seed):
+    """many_tiles in another type."""
+    a, b, dc, rows, offsets = many_tiles(sizes, n, k, seed)
+    return a.to(dtype), b.to(dtype), dc.to(dtype), rows, offsets
+
+
+# 31 tiles of 256 rows by 9 of 256 columns, at least 96 rows a group on average: the largest tile; remainders of 1, 65,
+# 129 and 193 rows (one to four live row blocks of a wave) and of a whole tile
+LARGE = [769, 577, 385, 705, 0, 2048, 1, 952]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, FP32), (FP16, FP16), (FP16, FP32)])
+def test_largest_tiles(dtype, out):
+    """Forward and both gradients by 256x256 tiles, each operand type into each output type."""
+    qr = _qr()
+    k, n = 200, 2056
+    a, b, _, rows, offsets = typed(LARGE, n, k, dtype, 40)
+    o, at = dev(offsets), rows.long()
+    c = qr.grouped_mm(a, b, o, rows=rows, dtype=out)
+    close_each(c, lambda e, s: (a[at[s]].double(), b[e].double().t()), LARGE, offsets, lambda e: k, False)
+    _, b, dc, _, _ = typed(LARGE, k, n, dtype, 41)  # columns of da: 2056
+    da = qr.grouped_mm_grad_a(dc, b, o, dtype=out)
+    close_each(da, lambda e, s: (dc[s].double(), b[e].double()), LARGE, offsets, lambda e: k, False)
+    sizes, n, k = [64, 0, 1, 63, 65, 193, 700, 128, 300], 1032, 1288  # 9 experts of 5 x 6 tiles
+    a, _, dc, rows, offsets = typed(sizes, n, k, dtype, 42)
+    at = rows.long()
+    for gather in (True, False):
+        db = qr.grouped_mm_grad_b(dc, a if gather else a[at], dev(offsets), rows=rows if gather else None, dtype=out)
+        close_each(db, lambda e, s: (dc[s].double().t(), a[at[s]].double()), sizes, offsets, lambda e: sizes[e], True)
+
+
+# (group sizes, columns): few rows, streamed, a workgroup taking one column tile or several (the last of them short);
+# tiles of 64x128, where there are few tiles and where there are few rows a group; tiles of 128x256
+FORMS = {
+    "streamed": ([1, 0, 3], 136),
+    "streamed_sweeps": ([16, 0, 31, 1, 17, 40, 0, 0, 60, 5, 9, 16, 20, 30, 11, 0], 1400),
+    "few_tiles": ([200, 0, 45], 264),
+    "few_rows_a_group": ([(i * 5) % 19 for i in range(60)], 1032),
+    "largest_tile": ([130, 900, 0, 257, 1, 700, 64, 1300], 1800),
+}
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("k", [1024, 2048, 2080, 2304, 4096, 4128])
+def test_mxfp4_long_rows(form, k):
+    """Rows of more than one load of scales (2048 elements), whole loads and remainders, through each kernel.  The
+    scale of every block is its own, so that one taken from another block shows."""
+    qr = _qr()
+    sizes, n = FORMS[form]
+    offsets = offsets_of(sizes)
+    pairs, src, E = offsets[-1], 97, len(sizes)
+    g = torch.Generator(device="cuda").manual_seed(k + n)
+
+    def rand(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+    ac, as_, bc, bs = rand(0, 256, src, k // 2), rand(118, 132, src, k // 32), rand(0, 256, E, n, k // 2), rand(118, 132, E, n, k // 32)
+    rows = torch.randint(0, src, (pairs,), device="cuda", generator=g, dtype=torch.int32)
+    va, vb = qr.mxfp4_dequantize(ac, as_).double(), qr.mxfp4_dequantize(bc, bs)
+    at = rows.long()
+    for gather, out in ((True, BF16), (False, FP32)):
+        c = qr.mxfp4_grouped_mm(*((ac, as_) if gather else (ac[at], as_[at])), bc, bs, dev(offsets),
+                                rows=rows if gather else None, dtype=out)
+        close_each(c, lambda e, s: (va[at[s]], vb[e].double().t()), sizes, offsets, lambda e: k, False)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, FP32), (FP16, FP16)])
+@pytest.mark.parametrize("k", [520, 2056])
+def test_streamed_sweeps(dtype, out, k):
+    """16-bit rows of few rows a group: workgroups that take several column tiles, the last of them short."""
+    qr = _qr()
+    sizes, n = FORMS["streamed_sweeps"]
+    a, b, _, rows, offsets = typed(sizes, n, k, dtype, k)
+    at = rows.long()
+    c = qr.grouped_mm(a, b, dev(offsets), rows=rows, dtype=out)
+    close_each(c, lambda e, s: (a[at[s]].double(), b[e].double().t()), sizes, offsets, lambda e: k, False)
+
+
+# ------------------------------------------------------------ subnormals
+@pytest.mark.parametrize("dtype,low,other", [(FP16, -24, 0), (FP16, -24, -14), (BF16, -133, 20)])
+@pytest.mark.parametrize("pairs", [3, 300])
+def test_subnormal_operands_keep_their_value(dtype, low, other, pairs):
+    """One term a sum, one factor of it subnormal: the product is exact in fp32, in each direction and kernel."""
+    qr = _qr()
+    n = k = 136
+    g = gen(pairs)
+
+    def small(*shape):
+        return (torch.randint(1, 8, shape, generator=g) * 2.0**low).to(dtype)
+
+    def plain(*shape):
+        return ((1 + torch.randint(0, 64, shape, generator=g) / 64) * 2.0**other).to(dtype)
+
+    a, b, dc = torch.zeros(pairs, k, dtype=dtype), plain(1, n, k), torch.zeros(pairs, n, dtype=dtype)
+    p = torch.arange(pairs)
+    a[p, (p * 7) % k], dc[p, (p * 5) % n] = small(pairs), small(pairs)
+    o = dev([0, pairs])
+    want = a.double() @ b[0].double().t()
+    assert want.abs().max() < 2.0 ** (low + other + 4) and (want != 0).all()
+    assert torch.equal(qr.grouped_mm(a.cuda(), b.cuda(), o, dtype=FP32).cpu().double(), want)
+    assert torch.equal(qr.grouped_mm_grad_a(dc.cuda(), b.cuda(), o, dtype=FP32).cpu().double(), dc.double() @ b[0].double())
+    dc, x = dc[:1], plain(1, k)  # one pair: one term
+    assert torch.equal(qr.grouped_mm_grad_b(dc.cuda(), x.cuda(), dev([0, 1]), dtype=FP32)[0].cpu().double(),
+                       dc.double().t() @ x.double())
+
+
+@pytest.mark.parametrize("pairs", [3, 300])
+def test_sums_of_fp16_subnormals(pairs):
+    """In a sum the matrix unit aligns an fp16 subnormal as if its exponent were that of the smallest normal number,
+    2^-14: the bound of the sum's rounding is that of terms whose factors are at least that large."""
+    qr = _qr()
+    n, k = 264, 520
+    a = (torch.randn(pairs, k, generator=gen(50)) * 2.0**-22).to(FP16)
+    b = torch.randn(1, n, k, generator=gen(51)).to(FP16)
+    c = qr.grouped_mm(a.cuda(), b.cuda(), dev([0, pairs]), dtype=FP32)
+    x, y = a.double(), b[0].double()
+    close(c, x @ y.t(), x.abs().clamp_min(2.0**-14) @ y.abs().clamp_min(2.0**-14).t(), k, "c")
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+def test_swiglu_to_four_bits_against_64_bits(dtype):
+    """Codes and scales are those of the 64-bit activation, or of one that is off by the 8 units of 2^-24 that the
+    fp32 activation may be off by."""
+    qr = _qr()
+    gu = (torch.randn(300, 512, generator=gen(52)) * 3).to(dtype)
+    codes, scales = (t.cpu() for t in qr.swiglu_mxfp4(gu.cuda()))
+    g, u, s = swiglu_ref(gu)
+    near = [quantize_ref(g * s * u * (1 + d)) for d in (-8 * 2.0**-24 * 1.001, 0, 8 * 2.0**-24 * 1.001)]
+    assert ((scales == near[0][1]) | (scales == near[2][1])).all()
+    same = (near[0][1] == near[2][1]).repeat_interleave(16, 1)  # blocks of one possible scale
+    assert same.float().mean() > 0.99
+    for nibble in (lambda c: c & 15, lambda c: c >> 4):
+        ok = torch.stack([nibble(codes) == nibble(c) for c, _, _ in near]).any(0)
+        assert (ok | ~same).all()

@@ -152,3 +152,17 @@ def test_frozen_operands(wanted):
         assert torch.equal(g, whole[n]) if n in wanted else g is None, n
     if "down" not in wanted:
         assert peak < down.numel() * 2  # the smaller bank's gradient
+
+
+def test_no_tokens():
+    """A batch without tokens: empty results, zero gradients of the banks."""
+    qr = _qr()
+    ids, w, x, gate_up, down = (t[:0] if i < 3 else t for i, t in enumerate(case(3, 2, 4, 64, 32, BF16, 7)))
+    xs, ws, gs, ds = [t.cuda().requires_grad_() for t in (x, w, gate_up, down)]
+    r = qr.Routing.from_ids(ids.cuda(), ws, 4)
+    out = qr.expert_ffn(xs, r, gs, ds)
+    assert out.shape == (0, 64) and out.dtype == torch.float32
+    out.backward(torch.zeros(0, 64, device="cuda"))
+    assert xs.grad.shape == (0, 64) and ws.grad.shape == (0, 2)
+    assert gs.grad.shape == gs.shape and not gs.grad.any() and ds.grad.shape == ds.shape and not ds.grad.any()
+    assert qr.Mxfp4Experts(gate_up.cuda(), down.cuda())(x.cuda(), r).shape == (0, 64)
