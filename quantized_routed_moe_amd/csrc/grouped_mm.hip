@@ -17,10 +17,17 @@
 // the power limit leaves (8192^3 bf16: 1290 TFLOP/s, the library 1311 with the
 // units 87% busy at 1.58 GHz), and how fast 64 KB a step come from the L2s
 // (1.7 us a step of a 256x256 tile; 1.2 us with nothing to fetch).  Short
-// groups: reading the weights (48 rows an expert, 4096 x 2048 of 256: 5.2 TB/s).
-// grad_b of short groups: writing the gradients and, with three steps a tile,
-// the copies' latency (64 experts of 192 rows, 4096 x 4096: 865 us; without
-// fetching 592, without storing 786).
+// groups: reading the weights (48 rows an expert, 4096 x 2048 of 256: 5.1 TB/s).
+// grad_b of short groups: with three steps a tile, the copies' latency and the
+// serial end of a tile (64 experts of 192 rows, 4096 x 4096, rows gathered: 865
+// to 923 us by card; 772 where they are not; where it took 865, a copy of the
+// kernel took 592 without fetching and 786 without storing).
+//
+// LDS: the operand reads meet no bank conflicts (none are counted in a kernel
+// that writes fp32).  What is counted are two lanes a bank in the writes of
+// 16-bit results (17 to 19% of the LDS cycles where a tile is three or four
+// steps, 2% at 64) and in the reads of four-bit operands' scales (23%).
+// Layouts without them made no difference in time.
 #include <algorithm>
 #include <type_traits>
 
@@ -323,7 +330,8 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
 
     // four-bit operands: block scales.  64 bytes of each row (eight steps) are loaded at a time, 16 by each of four
     // lanes, and go to LDS a pair of steps at a time, by the lane that has it, as words [step][half]: the blocks half,
-    // 2 + half, 4 + half, 6 + half that a lane's four MFMAs of a step need.
+    // 2 + half, 4 + half, 6 + half that a lane's four MFMAs of a step need.  (A read
+    // takes words 16 bytes apart of 32 rows: two lanes a bank.)
     auto load_scales = [&](int pair) {  // four pairs from `pair` on; zeros past the row's end and for no row
         if constexpr (FP4) {
             const int blocks = a.depth / 32, at = 16 * (pair + (tid & 3));
@@ -478,8 +486,9 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void group
         // ---- out, through LDS in blocks of 32 rows, so that a wave stores
         // whole stretches of them.  Register 4 q + i of a 32x32 tile holds
         // column 8 q + 4 half + i of row l32.  Piece c (16 bytes) of row r lies
-        // in slot c ^ (r & (kPieces - 1)): the 32 rows of a write and the
-        // pieces of a read fall on different banks.
+        // in slot c ^ (r & (kPieces - 1)): the pieces of a read and the 32
+        // rows of an fp32 write fall on different banks; a write of 16-bit
+        // results is half a piece, which puts rows 16 apart on the same ones.
         constexpr int kPer = 16 / (int)sizeof(T), kPieces = kOutCols / kPer;  // elements of a piece, pieces of a row
         constexpr int kNh = NI / kHalves;
         const int tid = afresh(threadIdx.x), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
@@ -582,9 +591,11 @@ hipError_t launch_tiles(GroupedArgs a, bool streaming, bool f32, hipStream_t s) 
 // what a call waits for: tiles then follow the weights through memory, one row
 // tile at a time, an eighth of the list to each XCD.  Above, the XCDs share
 // the list in runs of one tile a CU, eight row tiles by a few columns, which
-// share operands behind one L2 whatever the groups' sizes.  Measured, bf16:
-// 48 rows of 4096 x 2048 795 us against 925, 192 rows of 4096 x 4096 748
-// against 683.  (Whole experts to each XCD: the gradient of eight experts of
+// share operands behind one L2 whatever the groups' sizes.  Measured, bf16,
+// the first way / the second: 48 rows of 4096 x 2048 of 256 experts by 64x128
+// tiles 882 / 943 us, by 256x256 862 / 956; 192 rows of 4096 x 4096 of 64 by
+// 64x128 1018 / 843, by 256x256 594 / 599; eight experts of 2048 rows by
+// 256x256 538 / 503.  (Whole experts to each XCD: the gradient of eight experts of
 // 710 .. 4702 rows took 794 us, the XCDs being done after 215 .. 1034.)
 constexpr int kStreamRows = 96, kFewRows = 16;
 
@@ -593,12 +604,17 @@ hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
     const bool streaming = a.P < (int64_t)kStreamRows * a.E;
     // The largest tile moves the least between L2 and LDS for its arithmetic,
     // the smallest wastes the least on short groups and fills the chip with
-    // few tiles.  48 rows of 4096 x 2048 by 64x128 / 128x128 / 256x256 tiles:
-    // 795 / 860 / 980 us; 192 rows of 4096 x 4096: 930 / 690 / 600.
+    // few tiles.  By 64x128 / 128x128 / 256x256 tiles, bf16, 256 experts of
+    // 4096 x 2048: 16 rows 765 / 765 / 826 us, 32 rows 816 / 790 / 844, 48 rows
+    // 885 / 823 / 864, 90 rows 1128 / 941 / 941; 64 experts of 4096 x 4096: 192
+    // rows 843 / 681 / 596.  Between 40 rows and kStreamRows the order depends on
+    // how the last round of tiles fills the chip: 24 experts of 2816 x 2048, 48
+    // rows 86 / 93 / 108, 90 rows 83 / 91 / 109.  The smallest is taken there.
     // Four-bit operands stop at 128x256: with 256x256 the scales on their way
     // do not fit the registers (192 rows of 4096 x 4096 by 64x128 / 128x256 /
-    // 256x256: 1172 / 883 / 1238 us; 48 rows 553 / 506 / 629), and take the
-    // smallest tile for a few rows (1 / 8: 209 / 404 us against 226 / 437).
+    // 256x256: 1144 / 874 / 1251 us; 48 rows 531 / 500 / 623), and take the
+    // smallest tile for a few rows (8 / 32 tokens top-6 of 256 experts: 81 / 210
+    // us against 88 / 236).
     constexpr int BM = ELT == Elt::Fp4 ? 128 : 256;
     const bool fills = row_tiles(a, BM) * ceil_div(a.N, 256) >= kCus;
     const bool few = a.P < (int64_t)kFewRows * a.E;
@@ -612,10 +628,10 @@ hipError_t launch_ragged(const GroupedArgs &a, bool f32, hipStream_t s) {
 hipError_t launch_grouped_mm(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
     // Few tiles leave CUs idle; the streaming kernel spreads a few rows' weights
     // over all of them, but reads them again for every 16 rows.  Tiles of 64x128
-    // against it, 4096 x 4096 of 256 experts top-6, bf16: one token 62 / 41 us,
-    // four 154 / 144, eight 253 / 266, 32 719 / 762; four-bit: one token 23 /
-    // 17, two 25 / 29, 32 224 / 250.  One expert, bf16: 16 rows 40 / 18, 64 rows
-    // 40 / 58.
+    // against it, 4096 x 4096 of 256 experts top-6, bf16: one token 64 / 41 us,
+    // four 149 / 145, eight 249 / 259, 32 730 / 789; four-bit: one token 21 /
+    // 16, two 29 / 28, 32 210 / 254.  One expert, bf16: 16 rows 39 / 19, 64 rows
+    // 39 / 54.
     const int64_t tiles = row_tiles(a, 64) * ceil_div(a.N, 128);
     if (tiles <= kCus * (elt == Elt::Fp4 ? 1 : 3) && a.P <= 16 * (int64_t)a.E) return launch_grouped_vec(a, elt, f32, s);
     if (elt == Elt::Bf16) return launch_ragged<Elt::Bf16, false>(a, f32, s);
@@ -629,7 +645,7 @@ hipError_t launch_grouped_grad_a(const GroupedArgs &a, Elt elt, bool f32, hipStr
 }
 
 hipError_t launch_grouped_grad_b(const GroupedArgs &a, Elt elt, bool f32, hipStream_t s) {
-    // 64 experts of 192 rows, 4096 x 4096, by 128x128 / 256x256 tiles: 1147 / 862 us.
+    // 64 experts of 192 rows, 4096 x 4096, rows gathered, by 128x128 / 256x256 tiles: 1223 / 922 us.
     const bool fills = (int64_t)a.E * ceil_div(a.M, 256) * ceil_div(a.N, 256) >= kCus;
     auto go = [&](auto e) {
         constexpr Elt E = decltype(e)::value;
