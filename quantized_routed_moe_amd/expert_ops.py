@@ -48,6 +48,8 @@ def _graph(call, out, *operands):
     """None; where an operand asks for a gradient, why the result's derivative will be refused.  Raises where it could
     not be: the result is written to the caller's `out`, or an operand carries a forward-mode tangent."""
     if torch.is_grad_enabled():
+        if out is not None and out.requires_grad:
+            raise RuntimeError(f"{call} cannot write to an out that asks for a gradient")
         for t in operands:
             if t.requires_grad:
                 why = f"{call} builds no graph, but an operand asks for a gradient (detach it, or use expert_ffn)"
@@ -135,6 +137,14 @@ def _hold(stream, *tensors):
                 t.record_stream(stream)
 
 
+def _written(*outputs):
+    """Tells autograd that the caller's tensors have been written to, as torch's own calls do: a graph that saved one
+    refuses to use it."""
+    for t in outputs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _output(out, shape, dtype, allowed, like, stream):
     """(out, its row stride): a given output checked, or a new one."""
     if out is None:
@@ -183,6 +193,8 @@ def grouped_mm(a, b, offsets, rows=None, out=None, dtype=None, stream=None):
     result, ldc = _output(out, (P, N), dtype or a.dtype, (a.dtype, torch.float32), a, side)
     _check(_lib.moe_grouped_mm(ctypes.byref(g), DT[a.dtype], _pointer(a, "a", index), lda, _pointer(b, "b", index),
                                _pointer(result, "out", index), DT[result.dtype], ldc, raw), "moe_grouped_mm")
+    if out is not None:
+        _written(out)
     _hold(side, a, b, offsets, rows, out)
     return result if graph is None else _Refusal.apply(graph, result, a, b)
 
@@ -203,6 +215,8 @@ def grouped_mm_grad_a(dc, b, offsets, out=None, dtype=None, stream=None):
     _check(_lib.moe_grouped_mm_grad_a(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(b, "b", index), _pointer(result, "out", index), DT[result.dtype], lda,
                                       raw), "moe_grouped_mm_grad_a")
+    if out is not None:
+        _written(out)
     _hold(side, dc, b, offsets, out)
     return result if graph is None else _Refusal.apply(graph, result, dc, b)
 
@@ -227,6 +241,8 @@ def grouped_mm_grad_b(dc, a, offsets, rows=None, out=None, dtype=None, stream=No
     _check(_lib.moe_grouped_mm_grad_b(ctypes.byref(g), DT[dc.dtype], _pointer(dc, "dc", index), ldd,
                                       _pointer(a, "a", index), lda, _pointer(result, "out", index), DT[result.dtype],
                                       raw), "moe_grouped_mm_grad_b")
+    if out is not None:
+        _written(out)
     _hold(side, dc, a, offsets, rows, out)
     return result if graph is None else _Refusal.apply(graph, result, dc, a)
 
@@ -264,10 +280,12 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     if cols % 32:
         raise ValueError(f"x: rows of {cols} elements are not made of blocks of 32")
     index, raw, side = _target(x, "x", stream)
+    given = codes, scales
     codes, scales = _code_outputs(x.shape, codes, scales, x, side)
     _check(_lib.moe_mxfp4_quantize(DT[x.dtype], _pointer(x, "x", index), ld, rows, cols,
                                    _pointer(codes, "codes", index), _plain(scales, "scales", index), raw),
            "moe_mxfp4_quantize")
+    _written(*given)
     _hold(side, x, codes, scales)
     return codes, scales
 
@@ -285,12 +303,15 @@ def mxfp4_dequantize(codes, scales, out=None, dtype=torch.float32, stream=None):
     cols = _format(codes, scales, "codes", "scales")
     shape = (*codes.shape[:-1], cols)
     index, raw, side = _target(codes, "codes", stream)
-    out, ld = _output(out, shape, dtype, tuple(DT), codes, side)
+    _graph("mxfp4_dequantize", out)
+    result, ld = _output(out, shape, dtype, tuple(DT), codes, side)
     _check(_lib.moe_mxfp4_dequantize(_pointer(codes, "codes", index), _plain(scales, "scales", index),
-                                     codes.numel() * 2 // cols, cols, DT[out.dtype], _pointer(out, "out", index), ld,
-                                     raw), "moe_mxfp4_dequantize")
+                                     codes.numel() * 2 // cols, cols, DT[result.dtype], _pointer(result, "out", index),
+                                     ld, raw), "moe_mxfp4_dequantize")
+    if out is not None:
+        _written(out)
     _hold(side, codes, scales, out)
-    return out
+    return result
 
 
 def mxfp4_grouped_mm(a_codes, a_scales, b_codes, b_scales, offsets, rows=None, out=None, dtype=torch.bfloat16,
@@ -307,13 +328,16 @@ def mxfp4_grouped_mm(a_codes, a_scales, b_codes, b_scales, offsets, rows=None, o
     R = a_codes.shape[0]
     P = R if rows is None else rows.shape[0]
     g = _groups(offsets, rows, R, E, P, N, K, index)
-    out, ldc = _output(out, (P, N), dtype, (torch.bfloat16, torch.float32), a_codes, side)
+    _graph("mxfp4_grouped_mm", out)
+    result, ldc = _output(out, (P, N), dtype, (torch.bfloat16, torch.float32), a_codes, side)
     _check(_lib.moe_mxfp4_grouped_mm(ctypes.byref(g), _pointer(a_codes, "a_codes", index),
                                      _plain(a_scales, "a_scales", index), _pointer(b_codes, "b_codes", index),
-                                     _plain(b_scales, "b_scales", index), _pointer(out, "out", index), DT[out.dtype], ldc,
-                                     raw), "moe_mxfp4_grouped_mm")
+                                     _plain(b_scales, "b_scales", index), _pointer(result, "out", index),
+                                     DT[result.dtype], ldc, raw), "moe_mxfp4_grouped_mm")
+    if out is not None:
+        _written(out)
     _hold(side, a_codes, a_scales, b_codes, b_scales, offsets, rows, out)
-    return out
+    return result
 
 
 def _gate_up(gu):
@@ -331,6 +355,8 @@ def swiglu(gu, out=None, stream=None):
     result, ldh = _output(out, (rows, ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn, _pointer(result, "out", index), ldh,
                            raw), "moe_swiglu")
+    if out is not None:
+        _written(out)
     _hold(side, gu, out)
     return result if graph is None else _Refusal.apply(graph, result, gu)
 
@@ -341,9 +367,11 @@ def swiglu_mxfp4(gu, codes=None, scales=None, stream=None):
     if ffn % 32:
         raise ValueError(f"gu: rows of {ffn} outputs are not made of blocks of 32")
     index, raw, side = _target(gu, "gu", stream)
+    given = codes, scales
     codes, scales = _code_outputs((rows, ffn), codes, scales, gu, side)
     _check(_lib.moe_swiglu_mxfp4(DT[gu.dtype], _pointer(gu, "gu", index), ldg, rows, ffn,
                                  _pointer(codes, "codes", index), _plain(scales, "scales", index), raw), "moe_swiglu_mxfp4")
+    _written(*given)
     _hold(side, gu, codes, scales)
     return codes, scales
 
@@ -357,5 +385,7 @@ def swiglu_grad(dh, gu, out=None, stream=None):
     result, ldo = _output(out, (rows, 2 * ffn), gu.dtype, (gu.dtype,), gu, side)
     _check(_lib.moe_swiglu_grad(DT[gu.dtype], _pointer(dh, "dh", index), ldd, _pointer(gu, "gu", index), ldg, rows,
                                 ffn, _pointer(result, "out", index), ldo, raw), "moe_swiglu_grad")
+    if out is not None:
+        _written(out)
     _hold(side, dh, gu, out)
     return result if graph is None else _Refusal.apply(graph, result, dh, gu)

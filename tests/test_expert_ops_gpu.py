@@ -984,3 +984,40 @@ def test_swiglu_to_four_bits_against_64_bits(dtype):
     for nibble in (lambda c: c & 15, lambda c: c >> 4):
         ok = torch.stack([nibble(codes) == nibble(c) for c, _, _ in near]).any(0)
         assert (ok | ~same).all()
+
+
+def test_autograd_sees_what_is_written():
+    """An output that a graph has saved is refused by that graph once a call has written to it, as torch's own calls
+    have it; an output that asks for a gradient itself is refused by the call."""
+    qr = _qr()
+    a, b, offsets, _, pairs = make_case("ragged", 64, 64, BF16, False, 60)
+    a, b, o = a.cuda(), b.cuda(), dev(offsets)
+    gu = torch.randn(pairs, 64, generator=gen(61)).to(BF16).cuda()
+    dh = gu[:, :32].contiguous()
+    codes, scales = qr.mxfp4_quantize(a)
+    bc, bs = qr.mxfp4_quantize(b)
+    calls = [lambda out: qr.grouped_mm(a, b, o, out=out), lambda out: qr.grouped_mm_grad_a(a, b, o, out=out),
+             lambda out: qr.grouped_mm_grad_b(a, a, o, out=out), lambda out: qr.mxfp4_dequantize(codes, scales, out=out),
+             lambda out: qr.mxfp4_grouped_mm(codes, scales, bc, bs, o, out=out), lambda out: qr.swiglu(gu, out=out),
+             lambda out: qr.swiglu_grad(dh, gu, out=out)]
+    shapes = [(pairs, 64), (pairs, 64), (len(offsets) - 1, 64, 64), (pairs, 64), (pairs, 64), (pairs, 32), (pairs, 64)]
+    for i, (call, shape) in enumerate(zip(calls, shapes)):
+        out = torch.zeros(shape, dtype=BF16, device="cuda")
+        w = torch.ones(shape, dtype=BF16, device="cuda", requires_grad=True)
+        y = (out * w).sum()
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        with pytest.raises(RuntimeError, match="cannot write to an out"):
+            call(w)
+        assert (w == 1).all(), i
+        with torch.inference_mode():
+            assert torch.equal(call(torch.empty(shape, dtype=BF16, device="cuda")), out)
+    for call, c, s in ((lambda c, s: qr.mxfp4_quantize(a, c, s), codes, scales),
+                       (lambda c, s: qr.swiglu_mxfp4(torch.cat([a, a], 1), c, s), codes, scales)):
+        for t in (c, s):
+            w = torch.ones(t.shape, device="cuda", requires_grad=True)
+            y = (w * t).sum()
+            call(c, s)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
