@@ -345,6 +345,83 @@ int moe_swiglu_mxfp4(int32_t dtype, const void *gu, int64_t gu_stride, int64_t r
 int moe_swiglu_grad(int32_t dtype, const void *dh, int64_t dh_stride, const void *gu, int64_t gu_stride, int64_t rows,
                     int64_t ffn, void *dgu, int64_t dgu_stride, void *stream);
 
+/* ------------------------------------------- operators around the experts
+ * What trains a layer beside its experts' products: the router on given
+ * logits with the order of its pairs and its gradient, and the sum of a
+ * token's pairs with its gradients.  The conventions of the expert operators
+ * hold: nothing is allocated, nothing synchronises, every call can be
+ * captured, the same call gives the same bits.  Workspaces are the caller's,
+ * 256-byte aligned, written before they are read; calls that share one must
+ * not overlap. */
+
+/* The router.  Scores s are sigmoid(l) or softmax(l) of a token's logits;
+ * an expert's key is s + bias, the bias taking part in the choice only.  An
+ * expert whose logit or bias is -infinity is not there.  With groups > 1 the
+ * experts are groups of n_experts / groups consecutive ones; a group's score
+ * is the sum of its group_best largest keys (of those there), and the
+ * keep_groups best groups stay.  The top_k largest keys are chosen, in
+ * falling order; equal keys and groups: the lower index first.  Keys are
+ * compared as real numbers to 64 bits (without a bias as their logits, which
+ * have the same order).  NaN ranks behind every number.  Weights are s, or s
+ * / sum of the chosen s with renormalize (0 where that sum is 0), times
+ * scale, to fp32 rounding.  Where fewer than top_k experts are there, the
+ * ranks left have expert -1 and weight 0. */
+enum { MOE_SCORE_SIGMOID = 1, MOE_SCORE_SOFTMAX = 2 };
+typedef struct moe_router {
+    int32_t n_experts;   /* 1..1024 */
+    int32_t top_k;       /* 1..8, at most what the kept groups hold */
+    int32_t score;       /* MOE_SCORE_* */
+    int32_t groups;      /* 1..16, divides n_experts */
+    int32_t keep_groups; /* 1..groups */
+    int32_t group_best;  /* 1 or 2 */
+    int32_t renormalize; /* 0 or 1 */
+    float scale;
+    const float *bias;   /* [n_experts] on the device, or NULL */
+} moe_router;
+
+/* The pairs (token, rank), pair t * top_k + j, sorted by expert, those of one
+ * expert in their own order, pairs of no expert behind all others. */
+typedef struct moe_pair_order {
+    int64_t *perm;    /* [pairs] the pair at each place */
+    int64_t *place;   /* [pairs] each pair's place */
+    int32_t *rows;    /* [pairs] the token at each place */
+    int32_t *offsets; /* [n_experts + 1] where each expert's pairs begin */
+    void *workspace;  /* moe_pair_order_bytes(tokens, n_experts) */
+    size_t workspace_bytes;
+} moe_pair_order;
+size_t moe_pair_order_bytes(int64_t tokens, int32_t n_experts);
+
+/* ids[tokens][top_k] and w[tokens][top_k] from logits[tokens][n_experts]
+ * (fp32, bf16 or fp16, rows at any stride of at least n_experts elements);
+ * order: NULL, or the pairs' order too.  At most MOE_MAX_PAIRS pairs. */
+int moe_route(const moe_router *router, int32_t dtype, const void *logits, int64_t stride, int64_t tokens, int32_t *ids,
+              float *w, const moe_pair_order *order, void *stream);
+/* dlogits[tokens][n_experts] (the logits' type) from dw[tokens][top_k]: the
+ * gradient through the weights, the choice ids being given.  Entries of ids
+ * outside [0, n_experts) have none; one named twice has both's.  Of router,
+ * groups and bias are not looked at. */
+int moe_route_grad(const moe_router *router, int32_t dtype, const void *logits, int64_t stride, int64_t tokens,
+                   const int32_t *ids, const float *dw, void *dlogits, int64_t d_stride, void *stream);
+/* The order of any choice ids[tokens][top_k] (top_k >= 1), int32 or int64 by
+ * id_bytes; entries outside [0, n_experts) are of no expert. */
+int moe_sort_pairs(const void *ids, int32_t id_bytes, int64_t tokens, int64_t top_k, int32_t n_experts,
+                   const moe_pair_order *order, void *stream);
+
+/* out[t] = sum over j of w[t][j] y[place[t][j]] for y[pairs][cols] (fp32,
+ * bf16 or fp16; cols a multiple of 8), summed in fp32 in the order of j; out
+ * in y's type or fp32, from fp32 in any.  w NULL: ones.  A place outside [0,
+ * pairs) adds nothing. */
+int moe_combine(int32_t dtype, const void *y, int64_t y_stride, int64_t pairs, const int64_t *place, const float *w,
+                int64_t tokens, int64_t top_k, int64_t cols, void *out, int32_t out_dtype, int64_t out_stride,
+                void *stream);
+/* dy[place[t][j]] = w[t][j] dout[t] (dy: dtype; dout: dtype or fp32) and
+ * dw[t][j] = sum over columns of y[place[t][j]] dout[t].  Either output may
+ * be NULL; y is needed for dw only.  Rows of dy that no place names are left
+ * as they were; a row named twice gets one of the two, element by element. */
+int moe_combine_grad(int32_t dtype, const void *dout, int32_t dout_dtype, int64_t dout_stride, const void *y,
+                     int64_t y_stride, int64_t pairs, const int64_t *place, const float *w, int64_t tokens,
+                     int64_t top_k, int64_t cols, void *dy, int64_t dy_stride, float *dw, void *stream);
+
 /* Per-stage timing with HIP events.  While a profiler is attached to the
  * calling thread, every kernel a forward call launches records its own start
  * and end into two events (hipExtLaunchKernelGGL; dispatch latency between

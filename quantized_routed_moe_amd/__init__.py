@@ -68,6 +68,17 @@ class Grouped(ctypes.Structure):
                 ("src_rows", ctypes.c_int64)]
 
 
+class Router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_experts", "top_k", "score", "groups", "keep_groups", "group_best", "renormalize")] + [
+                    ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class PairOrder(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("perm", "place", "rows", "offsets", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t)]
+
+
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "moe_abi_version": ([], ctypes.c_int),
@@ -99,6 +110,13 @@ _SIGS = {
     "moe_swiglu": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
     "moe_swiglu_mxfp4": ([_I32, _P, _I64, _I64, _I64, _P, _P, _P], ctypes.c_int),
     "moe_swiglu_grad": ([_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
+    "moe_pair_order_bytes": ([_I64, _I32], _SZ),
+    "moe_route": ([ctypes.POINTER(Router), _I32, _P, _I64, _I64, _P, _P, ctypes.POINTER(PairOrder), _P], ctypes.c_int),
+    "moe_route_grad": ([ctypes.POINTER(Router), _I32, _P, _I64, _I64, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "moe_sort_pairs": ([_P, _I32, _I64, _I64, _I32, ctypes.POINTER(PairOrder), _P], ctypes.c_int),
+    "moe_combine": ([_I32, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P], ctypes.c_int),
+    "moe_combine_grad": ([_I32, _P, _I32, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P],
+                         ctypes.c_int),
     "moe_stage_name": ([_I32], ctypes.c_char_p),
     "moe_prof_create": ([ctypes.POINTER(_P), _I32], ctypes.c_int),
     "moe_prof_destroy": ([_P], None),
@@ -302,6 +320,7 @@ class Profiler:
 from .layer import MoELayer  # noqa: E402
 from .expert_ops import (grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_dequantize,  # noqa: E402
                          mxfp4_grouped_mm, mxfp4_quantize, swiglu, swiglu_grad, swiglu_mxfp4)
+from .train_ops import combine, combine_grad, route, route_grad, sort_pairs  # noqa: E402
 from .experts import Mxfp4Experts, Routing, expert_ffn  # noqa: E402
 
 __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Profiler", "make_shape", "workspace_bytes",
@@ -309,4 +328,5 @@ __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Prof
            "abi_version", "FMT_Q8", "FMT_Q2", "FLAG_BAD_TOKEN", "FLAG_BAD_TABLE_ENTRY", "FLAG_REPEATED_EXPERT", "ROUTE_LEARNED", "ROUTE_HASH", "ROUTE_HASH_SCORED", "EXPORTED",
            "LIB_PATH", "Grouped", "grouped_mm", "grouped_mm_grad_a", "grouped_mm_grad_b", "mxfp4_quantize",
            "mxfp4_dequantize", "mxfp4_grouped_mm", "swiglu", "swiglu_mxfp4", "swiglu_grad",
+           "Router", "PairOrder", "route", "route_grad", "sort_pairs", "combine", "combine_grad",
            "Routing", "expert_ffn", "Mxfp4Experts"]

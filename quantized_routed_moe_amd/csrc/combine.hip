@@ -1,0 +1,166 @@
+// The sum of a token's pairs and its gradients.
+//
+//   out[t] = sum_j w[t][j] y[place[t][j]]           (w absent: ones)
+//   dy[place[t][j]] = w[t][j] dout[t],   dw[t][j] = <y[place[t][j]], dout[t]>
+//
+// Memory-bound: every row is touched once, eight elements a lane, the rows of
+// a token's pairs in flight together.  Sums are in fp32, over j in order.  A
+// place outside [0, P) stands for no pair: it adds nothing and gets nothing.
+#include "mxfp4.hpp"
+#include "ops.hpp"
+
+namespace qrmoe {
+
+namespace {
+
+constexpr int kTogether = 8;  // pairs of a token whose rows are loaded together
+
+// Threads take eight columns each: whole workgroups of one token where rows are long, several tokens where not.
+template <int DT, int OUT, int K>  // K pairs a token; 0: any number
+__global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
+    const int per = (int)(a.H / 8), tid = threadIdx.x;
+    int64_t t;
+    int c;
+    if (per >= kThreads) {
+        const int blocks = (per + kThreads - 1) / kThreads;
+        t = blockIdx.x / blocks;
+        c = (blockIdx.x % blocks) * kThreads + tid;
+        if (c >= per) return;
+    } else {
+        const int tokens = kThreads / per;
+        t = (int64_t)blockIdx.x * tokens + tid / per;
+        c = tid % per;
+        if (tid >= tokens * per || t >= a.T) return;
+    }
+    const int64_t *place = a.place + t * a.k;
+    const float *w = a.w ? a.w + t * a.k : nullptr;
+    float sum[8] = {};
+    auto some = [&](int j0, auto n_c) {
+        constexpr int N = decltype(n_c)::value;
+        float y[N][8], f[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t p = place[j0 + j];
+            const bool there = (uint64_t)p < (uint64_t)a.P;
+            f[j] = w ? w[j0 + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[j][i] = 0;
+            if (there) load8<DT>(a.y, p * a.y_ld + 8 * c, y[j]);
+            else f[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(f[j], y[j][i], sum[i]);
+    };
+    if constexpr (K > 0) {
+        some(0, std::integral_constant<int, K>{});
+    } else {
+        int j = 0;
+        for (; j + 4 <= a.k; j += 4) some(j, std::integral_constant<int, 4>{});
+        for (; j < a.k; ++j) some(j, std::integral_constant<int, 1>{});
+    }
+    store8<OUT>(a.out, t * a.out_ld + 8 * c, sum);
+}
+
+// One workgroup a token.
+template <int DT, int DOUT>
+__global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineArgs a) {
+    __shared__ float part[kThreads / 64][kTogether];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
+    const int per = (int)(a.H / 8);
+    const int64_t t = blockIdx.x;
+    for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+        const int n = min(a.k - j0, kTogether);
+        int64_t p[kTogether];
+        float f[kTogether], dot[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            p[j] = j < n ? a.place[t * a.k + j0 + j] : -1;
+            if ((uint64_t)p[j] >= (uint64_t)a.P) p[j] = -1;
+            f[j] = j >= n ? 0.0f : a.w ? a.w[t * a.k + j0 + j] : 1.0f;
+            dot[j] = 0;
+        }
+        for (int c = tid; c < per; c += threads) {
+            float d[8], y[kTogether][8];
+            load8<DOUT>(a.dout, t * a.out_ld + 8 * c, d);
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j)
+                    if (p[j] >= 0) load8<DT>(a.y, p[j] * a.y_ld + 8 * c, y[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                if (p[j] < 0) continue;
+                if (a.dw) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(y[j][i], d[i], dot[j]);
+                }
+                if (a.dy) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = f[j] * d[i];
+                    store8<DT>(a.dy, p[j] * a.dy_ld + 8 * c, v);
+                }
+            }
+        }
+        if (!a.dw) continue;
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            const float s = group_sum<64>(dot[j]);
+            if (lane == 0) part[wave][j] = s;
+        }
+        __syncthreads();
+        if (tid < n) {
+            float s = 0;
+            for (int v = 0; v < threads / 64; ++v) s += part[v][tid];
+            a.dw[t * a.k + j0 + tid] = s;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStream_t s) {
+    const int per = (int)(a.H / 8);
+    const int64_t blocks = per >= kThreads ? a.T * ((per + kThreads - 1) / kThreads)
+                                           : (a.T + kThreads / per - 1) / (kThreads / per);
+    auto go = [&](auto dt_c, auto out_c) {
+        constexpr int DT = decltype(dt_c)::value, OUT = decltype(out_c)::value;
+        auto k = combine_kernel<DT, OUT, 0>;
+        switch (a.k) {
+            case 1: k = combine_kernel<DT, OUT, 1>; break;
+            case 2: k = combine_kernel<DT, OUT, 2>; break;
+            case 3: k = combine_kernel<DT, OUT, 3>; break;
+            case 4: k = combine_kernel<DT, OUT, 4>; break;
+            case 5: k = combine_kernel<DT, OUT, 5>; break;
+            case 6: k = combine_kernel<DT, OUT, 6>; break;
+            case 7: k = combine_kernel<DT, OUT, 7>; break;
+            case 8: k = combine_kernel<DT, OUT, 8>; break;
+        }
+        klaunch(k, dim3((unsigned)blocks), dim3(kThreads), s, a);
+        return hipGetLastError();
+    };
+    constexpr std::integral_constant<int, kDtF32> f32{};
+    constexpr std::integral_constant<int, kDtBf16> bf16{};
+    constexpr std::integral_constant<int, kDtF16> f16{};
+    if (dt == kDtF32) return out_dt == kDtF32 ? go(f32, f32) : out_dt == kDtBf16 ? go(f32, bf16) : go(f32, f16);
+    if (dt == kDtBf16) return out_dt == kDtF32 ? go(bf16, f32) : go(bf16, bf16);
+    return out_dt == kDtF32 ? go(f16, f32) : go(f16, f16);
+}
+
+hipError_t launch_combine_grad(int dt, int dout_dt, const CombineArgs &a, hipStream_t s) {
+    const int64_t per = a.H / 8;
+    const dim3 grid((unsigned)a.T), block(per <= 64 ? 64 : per <= 128 ? 128 : kThreads);
+    auto go = [&](auto k) {
+        klaunch(k, grid, block, s, a);
+        return hipGetLastError();
+    };
+    if (dt == kDtF32) return go(combine_grad_kernel<kDtF32, kDtF32>);
+    if (dt == kDtBf16)
+        return dout_dt == kDtF32 ? go(combine_grad_kernel<kDtBf16, kDtF32>) : go(combine_grad_kernel<kDtBf16, kDtBf16>);
+    return dout_dt == kDtF32 ? go(combine_grad_kernel<kDtF16, kDtF32>) : go(combine_grad_kernel<kDtF16, kDtF16>);
+}
+
+}  // namespace qrmoe

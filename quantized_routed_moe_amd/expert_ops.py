@@ -44,7 +44,7 @@ class _Refusal(torch.autograd.Function):
         raise RuntimeError(ctx.why)
 
 
-def _graph(call, out, *operands):
+def _graph(call, out, *operands, instead="use expert_ffn"):
     """None; where an operand asks for a gradient, why the result's derivative will be refused.  Raises where it could
     not be: the result is written to the caller's `out`, or an operand carries a forward-mode tangent."""
     if torch.is_grad_enabled():
@@ -52,7 +52,7 @@ def _graph(call, out, *operands):
             raise RuntimeError(f"{call} cannot write to an out that asks for a gradient")
         for t in operands:
             if t.requires_grad:
-                why = f"{call} builds no graph, but an operand asks for a gradient (detach it, or use expert_ffn)"
+                why = f"{call} builds no graph, but an operand asks for a gradient (detach it, or {instead})"
                 if out is not None:
                     raise RuntimeError(why)
                 return why

@@ -1,0 +1,574 @@
+"""The operators around the experts' products on the GPU, against plain 64-bit computations: the router with the order
+of its pairs and its gradient, and the sum of a token's pairs with its gradients.
+
+Tolerances, relative unless said otherwise.  A router's weights come from 64 bits and are rounded once: 2^-24.  Only a
+softmax that is not renormalised has an fp32 sum below it: e^x is within 2 units of 2^-24 and, its argument being
+rounded, |x| more, which under the softmax averages at most ln 1024 < 7; the sum has at most 16 additions in a lane and
+6 across lanes: 2 + 7 + 22 + 1 < 2^5 units, 2^-19.  Its gradient subtracts two such products (and e^x itself with |x| up
+to 30): 2^-18 of their magnitudes, and the output's rounding.  Weighted sums are in fp32: a unit for each term and one
+for the product, of the sum of magnitudes, and the output's rounding.
+"""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+BF16, FP16, FP32, FP64 = torch.bfloat16, torch.float16, torch.float32, torch.float64
+UNIT = {BF16: 2.0**-8, FP16: 2.0**-11, FP32: 2.0**-24}
+TINY = {BF16: 2.0**-130, FP16: 2.0**-25, FP32: 2.0**-149}
+ALL = [FP32, BF16, FP16]
+
+
+def _qr():
+    import quantized_routed_moe_amd as qr
+    return qr
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------------- router
+def scores_of(x, score):
+    x = x.to(FP64)
+    if score == "sigmoid":
+        return torch.sigmoid(x)
+    top = x.amax(1, keepdim=True)
+    e = torch.exp(x - torch.where(torch.isinf(top), 0.0, top))
+    z = e.sum(1, keepdim=True)
+    return e / torch.where(z > 0, z, 1.0)
+
+
+def reference(x, k, score="sigmoid", bias=None, groups=1, keep_groups=None, group_best=2, renormalize=True, scale=1.0):
+    """(ids, w) in 64 bits, on the host."""
+    T, E = x.shape
+    s = scores_of(x, score)
+    gone = x == -math.inf
+    if bias is not None:
+        gone = gone | (bias == -math.inf)
+        key = s + bias.to(FP64)
+    else:
+        key = x.to(FP64) + 0.0
+    key = torch.where(gone, -math.inf, key)
+    if groups > 1:
+        g = (key if bias is not None else torch.where(gone, -math.inf, s)).view(T, groups, E // groups)
+        best = g.sort(2, descending=True).values[:, :, :group_best]
+        total = torch.where(best[:, :, 0] > -math.inf, torch.where(best > -math.inf, best, 0.0).sum(2), -math.inf)
+        keep = total.sort(dim=1, descending=True, stable=True).indices[:, : keep_groups or groups]
+        mask = torch.zeros(T, groups, dtype=torch.bool).scatter_(1, keep, True)
+        key = torch.where(mask.repeat_interleave(E // groups, 1), key, -math.inf)
+    value, ids = key.sort(dim=1, descending=True, stable=True)
+    value, ids = value[:, :k], ids[:, :k]
+    there = value > -math.inf
+    w = torch.where(there, s.gather(1, ids), 0.0)
+    if renormalize:
+        total = w.sum(1, keepdim=True)
+        w = w / torch.where(total == 0, 1.0, total)
+    return torch.where(there, ids, -1).to(torch.int32), w * scale
+
+
+def order_of(ids, E):
+    flat = ids.reshape(-1).long()
+    flat = torch.where((flat < 0) | (flat >= E), E, flat)
+    perm = flat.sort(stable=True).indices
+    place = torch.empty_like(perm)
+    place[perm] = torch.arange(perm.numel())
+    offsets = torch.zeros(E + 1, dtype=torch.int32)
+    offsets[1:] = torch.bincount(flat, minlength=E + 1)[:E].cumsum(0)
+    return perm, offsets, (perm // max(ids.shape[1], 1)).to(torch.int32), place
+
+
+def check_order(got, ids, E):
+    for name, a, b in zip(("perm", "offsets", "rows", "place"), got, order_of(ids, E)):
+        assert a.dtype == b.dtype and torch.equal(a.cpu(), b), name
+
+
+def check_route(x, k, n=None, **kw):
+    """route and Routing.from_logits of host logits against the reference; returns the ids."""
+    qr = _qr()
+    bias = kw.get("bias")
+    want, w = reference(x, k, **kw)
+    xs = x.cuda()
+    on = dict(kw, bias=None if bias is None else bias.cuda())
+    ids, weights = qr.route(xs, k, **on)
+    assert ids.dtype == torch.int32 and torch.equal(ids.cpu(), want), f"{int((ids.cpu() != want).any(1).sum())} rows differ"
+    dense = kw.get("score") == "softmax" and not kw.get("renormalize", True)
+    unit = 2.0**-19 if dense else 2.0**-24 * (1 + 2.0**-20)
+    err = (weights.cpu().to(FP64) - w).abs()
+    assert weights.dtype == FP32 and bool((err <= unit * w.abs() + 2.0**-149).all()), float((err / w.abs()).nan_to_num().max())
+    r = qr.Routing.from_logits(xs, k, **on)
+    assert torch.equal(r.ids, ids) and torch.equal(r.w, weights) and r.k == k
+    check_order((r.perm, r.offsets, r.rows, r.place), want, x.shape[1])
+    return want
+
+
+def logits(T, E, dtype, seed):
+    g = gen(seed)
+    return (1.5 * torch.randn(T, E, generator=g) + 0.7 * torch.randn(E, generator=g)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("T,E,k", [(1, 256, 6), (1, 1, 1), (5, 8, 8), (67, 60, 4), (130, 64, 8), (65, 100, 3), (64, 128, 1),
+                                   (33, 257, 8), (70, 512, 6), (19, 1000, 8), (40, 1024, 5)])
+def test_route(dtype, T, E, k):
+    bias = 0.3 * torch.randn(E, generator=gen(E))
+    for seed, (score, b, renorm, scale) in enumerate([("sigmoid", bias, True, 1.0), ("sigmoid", None, False, 2.5),
+                                                      ("softmax", None, True, 1.0), ("softmax", None, False, 1.0),
+                                                      ("softmax", bias / E, False, 0.5)]):
+        check_route(logits(T, E, dtype, seed), k, score=score, bias=b, renormalize=renorm, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("T,E,k,groups,keep", [(77, 256, 6, 8, 4), (65, 256, 8, 8, 1), (9, 16, 3, 16, 5), (66, 60, 2, 4, 2),
+                                               (20, 512, 8, 16, 16), (30, 1024, 8, 8, 3), (12, 6, 4, 2, 2), (31, 96, 5, 3, 2)])
+def test_route_groups(dtype, T, E, k, groups, keep):
+    bias = 0.2 * torch.randn(E, generator=gen(E))
+    for seed, (score, b, best) in enumerate([("sigmoid", bias, 2), ("sigmoid", None, 2), ("softmax", None, 1),
+                                             ("softmax", bias / E, 2)]):
+        check_route(logits(T, E, dtype, seed), k, score=score, bias=b, groups=groups, keep_groups=keep, group_best=best)
+
+
+def test_route_many_tokens():
+    """More than one pass of a workgroup, and more than one workgroup's chunk of the order."""
+    bias = 0.1 * torch.randn(64, generator=gen(0))
+    check_route(logits(20011, 64, BF16, 3), 6, bias=bias)
+    check_route(logits(33001, 10, FP32, 4), 2, score="softmax", renormalize=False)
+    check_route(logits(3001, 320, FP16, 5), 8, bias=0.1 * torch.randn(320, generator=gen(1)), groups=8, keep_groups=3)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_ties(dtype, score):
+    """Few distinct logits: most choices are among equals, with and without a bias that keeps them so."""
+    x = torch.randint(-3, 3, (200, 96), generator=gen(7)).to(dtype) / 2
+    x[0], x[1], x[2, 5] = 0.0, -0.0, -0.0
+    even = torch.full((96,), 0.25)
+    steps = torch.randint(0, 3, (96,), generator=gen(8)).float() / 4
+    for b in (None, torch.zeros(96), even, steps):
+        check_route(x, 8, score=score, bias=b)
+        check_route(x, 4, score=score, bias=b, groups=8, keep_groups=2)
+        check_route(x, 4, score=score, bias=b, groups=4, keep_groups=3, group_best=1)
+
+
+def test_route_keys_next_to_each_other():
+    """Keys that fp32 cannot tell apart: logits a place apart, and a bias that makes up for a logit's difference."""
+    g = gen(9)
+    base = torch.randn(300, 1, generator=g)
+    x = base.repeat(1, 64)
+    for _ in range(2):
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.5, torch.nextafter(x, torch.tensor(9.0)), x)
+    for b in (None, torch.zeros(64), 3 * torch.ones(64)):
+        for score in ("sigmoid", "softmax"):
+            check_route(x, 6, score=score, bias=b)
+            check_route(x, 6, score=score, bias=b, groups=8, keep_groups=2)
+    # keys all within a few units of 0.75: what is left of the score's rounding decides
+    x = torch.randn(1, 64, generator=g).repeat(50, 1)
+    bias = (0.75 - torch.sigmoid(x[0].double())).float()
+    x = x + 1e-7 * torch.randn(50, 64, generator=g)
+    check_route(x, 8, bias=bias)
+    check_route(x, 8, bias=bias, groups=4, keep_groups=2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups", [(48, 1), (256, 1), (48, 8), (256, 8)])
+def test_route_masked(score, E, groups):
+    """Experts that are not there, rows with fewer than top_k of them, rows with none."""
+    x = logits(60, E, FP32, 2)
+    g = gen(3)
+    x[torch.rand(x.shape, generator=g) < 0.5] = -math.inf
+    x[:3] = -math.inf
+    x[3, : E - 2] = -math.inf
+    x[4, 1:] = -math.inf
+    bias = torch.randn(E, generator=g)
+    bias[::7] = -math.inf
+    for b in (None, bias):
+        ids = check_route(x, 6, score=score, bias=b, groups=groups, keep_groups=max(1, groups // 2))
+        assert (ids[:3] == -1).all() and (ids[3] == -1).any()
+        check_route(x, 6, score=score, bias=b, groups=groups, renormalize=False)
+    lowest = torch.finfo(FP32).min
+    x[x == -math.inf] = lowest  # a mask of the type's lowest value leaves the expert there, with score 0
+    check_route(x, 6, score=score, groups=groups, keep_groups=max(1, groups // 2))
+
+
+def test_route_far_logits():
+    x = torch.tensor([[1e4, -1e4, 3.0, 88.0, -88.0, 0.0, 700.0, -700.0]]).repeat(3, 1)
+    x[1] = -1e30
+    x[2, 0] = 3e38
+    for score in ("sigmoid", "softmax"):
+        check_route(x, 5, score=score)
+        check_route(x, 5, score=score, bias=torch.tensor([0.0, 9.0, -3.0, 0, 1e30, -1e30, 0, 0]))
+    # scores below fp32's and below 64 bits' range: weights of 0
+    x = torch.full((1, 8), -2000.0)
+    ids, w = _qr().route(x.cuda(), 3)
+    assert ids.tolist() == [[0, 1, 2]] and w.tolist() == [[0.0, 0.0, 0.0]]
+
+
+def test_route_not_a_number():
+    """NaN ranks behind every number; ids stay distinct and in range."""
+    qr = _qr()
+    x = logits(40, 64, FP32, 11)
+    bad = torch.rand(40, 64, generator=gen(1)) < 0.3
+    x[bad] = math.nan
+    ids, w = qr.route(x.cuda(), 6)
+    assert not bad.gather(1, ids.cpu().long()).any() and not w.isnan().any()
+    x[0], x[1, 3:] = math.nan, math.nan
+    for kw in (dict(), dict(score="softmax"), dict(bias=torch.zeros(64).cuda()), dict(groups=8, keep_groups=2),
+               dict(score="softmax", bias=torch.zeros(64).cuda(), groups=4, keep_groups=4)):
+        ids = qr.route(x.cuda(), 6, **kw)[0].cpu()
+        assert ((ids >= 0) & (ids < 64)).all() and all(len(set(r)) == 6 for r in ids.tolist())
+    bias = torch.zeros(64)
+    bias[5] = math.inf
+    y = logits(3, 64, FP32, 12)
+    assert (qr.route(y.cuda(), 2, bias=bias.cuda())[0][:, 0] == 5).all()
+
+
+def test_route_strided_rows():
+    qr = _qr()
+    wide = logits(50, 201, BF16, 6).cuda()
+    part = wide[:, 3:103]
+    a, b = qr.route(part, 5), qr.route(part.contiguous(), 5)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dw = torch.randn(50, 5, generator=gen(1)).cuda()
+    out = torch.full((50, 230), 7.0, dtype=BF16, device="cuda")
+    qr.route_grad(dw, part, a[0], out=out[:, 30:130])
+    assert torch.equal(out[:, 30:130], qr.route_grad(dw, part.contiguous(), a[0]))
+    assert (out[:, :30] == 7).all() and (out[:, 130:] == 7).all()
+    one = wide[:1, 1:98]
+    assert torch.equal(qr.route(one, 2)[0], qr.route(one.clone(), 2)[0])
+
+
+# ----------------------------------------------------------------- gradient
+def grad_reference(dw, x, ids, score, renormalize, scale):
+    """(dlogits, the magnitudes it is a difference of) in 64 bits, by autograd of the formula on the chosen."""
+    p = scores_of(x, score)
+    there = (ids >= 0) & (ids < x.shape[1])
+    at, slip = ids.long() * there, torch.zeros_like(dw, dtype=FP64)
+    s, G = p.gather(1, at) * there, dw.to(FP64) * scale * there
+    if renormalize:
+        S = s.sum(1, keepdim=True)
+        S = torch.where(S == 0, 1.0, S)
+        c = (G * s).sum(1, keepdim=True) / S
+        # the difference is formed in 64 bits: off by a few units of 2^-53 of its operands, as the kernel's is
+        slip = 2.0**-27 * (G.abs() + (G.abs() * s).sum(1, keepdim=True) / S) / S * there
+        G = (G - c) / S * there
+    # an expert named several times has the sum of its terms, each rounded before: what that is relative to is the sum
+    # of their magnitudes, which may be far above that of the sum
+    d, m = torch.zeros_like(p), torch.zeros_like(p)
+    for j in range(ids.shape[1]):
+        d.scatter_add_(1, at[:, j : j + 1], G[:, j : j + 1])
+        m.scatter_add_(1, at[:, j : j + 1], G[:, j : j + 1].abs() + slip[:, j : j + 1])
+    if score == "sigmoid":
+        rest = scores_of(-x.to(FP64), score)  # 1 - p, which 64 bits lose where p is near 1
+        return d * p * rest, m * p * rest
+    if renormalize:
+        return d * p, m * p
+    c = (G * s).sum(1, keepdim=True)
+    return d * p - p * c, m * p + (p * c).abs()
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 256, 6), (1, 1, 1), (67, 60, 4), (33, 257, 8), (9, 1024, 2), (515, 100, 3)])
+def test_route_grad(dtype, score, renorm, T, E, k):
+    qr = _qr()
+    x = logits(T, E, dtype, T)
+    if T > 8:
+        x[2], x[3, 1:], x[5] = -math.inf, -math.inf, 40.0
+    ids, _ = reference(x, k, score=score)
+    if T > 8 and E > 8:
+        ids[6, 0], ids[7] = E, 3  # of no expert; the same expert every time
+    dw = torch.randn(T, k, generator=gen(1))
+    want, mag = grad_reference(dw, x, ids, score, renorm, 1.5)
+    got = qr.route_grad(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalize=renorm, scale=1.5)
+    assert got.dtype == dtype
+    dense = score == "softmax" and not renorm
+    tol = UNIT[dtype] * (1 + 2.0**-10) * want.abs() + (2.0**-18 if dense else 2.0**-21) * mag + TINY[dtype]
+    err = (got.cpu().to(FP64) - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
+
+
+def test_route_grad_against_differences():
+    """The weights' change along a direction, from 64 bits, is what the gradient says."""
+    qr = _qr()
+    for score in ("sigmoid", "softmax"):
+        for renorm in (True, False):
+            x = logits(12, 40, FP32, 5)
+            dw = torch.randn(12, 5, generator=gen(2))
+            ids, _ = reference(x, 5, score=score)
+            d = qr.route_grad(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalize=renorm).cpu().to(FP64)
+            step = torch.randn(12, 40, generator=gen(3), dtype=FP64)
+            h = 2.0**-12
+
+            def loss(v):
+                s = scores_of(v, score).gather(1, ids.long())
+                return ((s / s.sum(1, keepdim=True) if renorm else s) * dw.to(FP64)).sum()
+
+            num = (loss(x.to(FP64) + h * step) - loss(x.to(FP64) - h * step)) / (2 * h)
+            # the third derivative's part, h^2 / 6 of it, and the fp32 rounding of each entry
+            assert abs(float((d * step).sum() - num)) <= 1e-6 * float((d * step).abs().sum()) + h * h * 100
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_routing_from_logits_is_differentiable(score, renorm):
+    qr = _qr()
+    x = logits(30, 24, FP32, 8)
+    leaf = x.cuda().requires_grad_()
+    r = qr.Routing.from_logits(leaf, 3, score=score, renormalize=renorm, scale=2.0)
+    dw = torch.randn(30, 3, generator=gen(4))
+    got, = torch.autograd.grad(r.w, leaf, dw.cuda())
+    want, mag = grad_reference(dw, x, r.ids.cpu(), score, renorm, 2.0)
+    assert bool(((got.cpu().to(FP64) - want).abs() <= 2.0**-18 * mag + 2.0**-24 * want.abs() + 2.0**-149).all())
+    r = qr.Routing.from_logits(leaf, 3, score=score)
+    d, = torch.autograd.grad(r.w.square().sum(), leaf, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated twice"):
+        torch.autograd.grad(d.sum(), leaf)
+
+
+# --------------------------------------------------------------- pair order
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T,k,E", [(0, 6, 8), (1, 1, 1), (1, 6, 256), (64, 6, 256), (65, 6, 256), (3, 40, 7), (1000, 6, 1024),
+                                   (4099, 3, 1000), (16385, 2, 2), (20000, 8, 128), (50001, 6, 300), (1 << 20, 1, 5)])
+def test_sort_pairs(dtype, T, k, E):
+    ids = torch.randint(-1, E + 1, (T, k), generator=gen(T), dtype=dtype)  # some of no expert
+    check_order(_qr().sort_pairs(ids.cuda(), E), ids, E)
+
+
+def test_sort_pairs_uneven():
+    qr = _qr()
+    same = torch.full((5000, 4), 3)
+    check_order(qr.sort_pairs(same.cuda(), 9), same, 9)
+    none = torch.full((500, 4), -1)
+    check_order(qr.sort_pairs(none.cuda(), 9), none, 9)
+    far = torch.tensor([[1 << 40, -(1 << 40)], [(1 << 32) + 1, 1]])
+    check_order(qr.sort_pairs(far.cuda(), 4), far, 4)
+    r = qr.Routing.from_ids(same.cuda(), torch.rand(5000, 4).cuda(), 9)
+    check_order(r._tensors(), same, 9)
+    byte = torch.randint(0, 9, (50, 2), generator=gen(1), dtype=torch.uint8)
+    check_order(qr.Routing.from_ids(byte.cuda(), torch.rand(50, 2).cuda(), 9)._tensors(), byte, 9)
+
+
+def test_from_ids_past_the_kernels_limits():
+    """More experts than the kernels take: torch's own operations, the same order."""
+    ids = torch.randint(0, 2000, (300, 3), generator=gen(2))
+    check_order(_qr().Routing.from_ids(ids.cuda(), torch.rand(300, 3).cuda(), 2000)._tensors(), ids, 2000)
+
+
+# ------------------------------------------------------------------ combine
+def pairs(T, k, n, dtype, seed, extra=0):
+    g = gen(seed)
+    y = torch.randn(T * k + extra, n, generator=g).to(dtype)
+    place = torch.randperm(T * k + extra, generator=g)[: T * k].view(T, k)
+    return y, place, torch.rand(T, k, generator=g) - 0.3
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, FP32), (BF16, BF16), (FP16, FP32), (FP16, FP16), (FP32, FP32), (FP32, BF16),
+                                       (FP32, FP16)])
+@pytest.mark.parametrize("T,k,n", [(1, 6, 4096), (1, 1, 8), (7, 3, 104), (33, 8, 2056), (5, 11, 72), (300, 2, 24), (40, 5, 520),
+                                   (3, 4, 65536), (130, 7, 256)])
+def test_combine(dtype, out, T, k, n):
+    y, place, w = pairs(T, k, n, dtype, n)
+    place[0, 0] = -1  # of no pair
+    for weights in (w, None):
+        f = torch.ones(T, k) if weights is None else weights
+        there = (place >= 0)[:, :, None]
+        terms = y.to(FP64)[place.clamp_min(0)] * f.to(FP64)[:, :, None] * there
+        got = _qr().combine(y.cuda(), place.cuda(), None if weights is None else weights.cuda(), dtype=out)
+        assert got.dtype == out and got.shape == (T, n)
+        want = terms.sum(1)
+        tol = UNIT[out] * (1 + 2.0**-10) * want.abs() + (k + 1) * 2.0**-24 * terms.abs().sum(1) + TINY[out]
+        assert bool(((got.cpu().to(FP64) - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype,dd", [(BF16, FP32), (BF16, BF16), (FP16, FP32), (FP16, FP16), (FP32, FP32)])
+@pytest.mark.parametrize("T,k,n", [(1, 6, 4096), (1, 1, 8), (7, 3, 104), (33, 8, 2056), (5, 11, 72), (300, 2, 24), (40, 5, 1032),
+                                   (2, 17, 1024)])
+def test_combine_grad(dtype, dd, T, k, n):
+    y, place, w = pairs(T, k, n, dtype, n)
+    d = torch.randn(T, n, generator=gen(1)).to(dd)
+    for weights in (w, None):
+        f = (torch.ones(T, k) if weights is None else weights).to(FP64)
+        dy, dw = _qr().combine_grad(d.cuda(), y.cuda(), place.cuda(), None if weights is None else weights.cuda())
+        assert dy.dtype == dtype and dw.dtype == FP32
+        want = torch.empty(T * k, n, dtype=FP64)
+        want[place] = f[:, :, None] * d.to(FP64)[:, None]
+        tol = (UNIT[dtype] + 2.0**-24) * (1 + 2.0**-10) * want.abs() + TINY[dtype]
+        assert bool(((dy.cpu().to(FP64) - want).abs() <= tol).all())
+        terms = y.to(FP64)[place] * d.to(FP64)[:, None]
+        err = (dw.cpu().to(FP64) - terms.sum(2)).abs()
+        assert bool((err <= n * 2.0**-24 * terms.abs().sum(2) + 2.0**-149).all())
+
+
+def test_combine_grad_rows_no_pair_names():
+    """Rows behind the pairs, and a pair without a place: left as they were, weight gradient 0."""
+    qr = _qr()
+    y, place, w = pairs(9, 3, 64, BF16, 1, extra=5)
+    place[4, 1], place[5, 2] = 9 * 3 + 5, -7
+    d = torch.randn(9, 64, generator=gen(2))
+    dy = torch.full((32, 64), 3.0, dtype=BF16, device="cuda")
+    _, dw = qr.combine_grad(d.cuda(), y.cuda(), place.cuda(), w.cuda(), dy=dy)
+    named = torch.zeros(32, dtype=torch.bool)
+    named[place[(place >= 0) & (place < 32)]] = True
+    assert (dy.cpu()[~named] == 3).all() and not (dy.cpu()[named] == 3).all(1).any()
+    assert dw[4, 1] == 0 and dw[5, 2] == 0
+    with pytest.raises(ValueError, match="place"):
+        qr.combine_grad(d.cuda(), y.cuda(), place.cuda(), w.cuda())
+
+
+def test_combine_strided_and_special_values():
+    qr = _qr()
+    wide = torch.randn(12, 200, generator=gen(3)).to(BF16).cuda()
+    y, place = wide[:, 16:80], torch.randperm(12, generator=gen(4)).view(6, 2).cuda()
+    w = torch.rand(6, 2, generator=gen(5)).cuda()
+    out = torch.full((6, 128), 9.0, device="cuda")
+    qr.combine(y, place, w, out=out[:, 32:96])
+    assert torch.equal(out[:, 32:96], qr.combine(y.contiguous(), place, w))
+    assert (out[:, :32] == 9).all() and (out[:, 96:] == 9).all()
+    x = y.contiguous()
+    x[place[2, 0], 7], x[place[3, 1], 0] = math.nan, math.inf
+    got = qr.combine(x, place, w)
+    assert got[2, 7].isnan() and got[3, 0] == math.inf
+    assert int((~got.isfinite()).sum()) == 2
+
+
+def test_routing_combine():
+    """Kernels and torch's operations say the same; with a graph both gradients are there."""
+    qr = _qr()
+    ids = torch.stack([torch.randperm(9, generator=gen(i))[:3] for i in range(20)]).cuda()
+    w = torch.rand(20, 3, generator=gen(1)).cuda()
+    y = torch.randn(60, 48, generator=gen(2)).to(BF16).cuda()
+    r = qr.Routing.from_ids(ids, w, 9)
+    want = (r.to_tokens(y).double() * w.double()[:, :, None]).sum(1)
+    assert (r.combine(y).double() - want).abs().max() <= 2.0**-21 * want.abs().max()
+    leaf, wl = y.float().requires_grad_(), w.clone().requires_grad_()
+    rg = qr.Routing.from_ids(ids, wl, 9)
+    rg.combine(leaf).sum().backward()
+    assert leaf.grad is not None and wl.grad is not None
+    odd = torch.randn(60, 5, generator=gen(3)).cuda()  # a width the kernel does not take
+    assert r.combine(odd).shape == (20, 5)
+
+
+# ------------------------------------------------- streams, graphs, together
+def test_other_stream_and_repeat():
+    qr = _qr()
+    x = logits(700, 128, BF16, 1).cuda()
+    y, place, w = (t.cuda() for t in pairs(700, 4, 256, BF16, 2))
+    d = torch.randn(700, 256, generator=gen(3)).cuda()
+    bias = 0.1 * torch.randn(128, generator=gen(4)).cuda()
+    base = (*qr.route(x, 4, bias=bias), qr.combine(y, place, w), *qr.combine_grad(d, y, place, w))
+    grad = qr.route_grad(base[1], x, base[0])
+    order = qr.sort_pairs(base[0], 128)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        got = (*qr.route(x, 4, bias=bias, stream=s), qr.combine(y, place, w, stream=s),
+               *qr.combine_grad(d, y, place, w, stream=s))
+        got += (qr.route_grad(base[1], x, base[0], stream=s), *qr.sort_pairs(base[0], 128, stream=s))
+        s.synchronize()
+        for a, b in zip(got, (*base, grad, *order)):
+            assert torch.equal(a, b)
+
+
+def test_captured_and_replayed():
+    """The router, the products' order and the sum in one graph, on new inputs each replay."""
+    qr = _qr()
+    g = gen(5)
+    x = torch.randn(500, 64, generator=g).cuda()
+    bank_in = torch.randn(500 * 4, 64, generator=g).to(BF16).cuda()
+    dout = torch.randn(500, 64, generator=g).cuda()
+
+    def step():
+        r = qr.Routing.from_logits(x, 4)
+        out = qr.combine(bank_in, r.place.view(500, 4), r.w)
+        dy, dw = qr.combine_grad(dout, bank_in, r.place.view(500, 4), r.w)
+        return r.ids, r.w, r.perm, r.offsets, r.rows, out, dy, dw, qr.route_grad(dw, x, r.ids)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        x.copy_(torch.randn(500, 64, generator=g))
+        bank_in.copy_(torch.randn(500 * 4, 64, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), i
+
+
+def test_two_streams_at_once():
+    """Two calls at once have workspaces of their own."""
+    qr = _qr()
+    xs = [logits(30000, 64, FP32, i).cuda() for i in range(2)]
+    want = [qr.Routing.from_logits(x, 6) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(qr.Routing.from_logits(x, 6))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.ids, b.ids) and torch.equal(a.perm, b.perm) and torch.equal(a.offsets, b.offsets)
+
+
+def test_nothing_to_do():
+    qr = _qr()
+    ids, w = qr.route(torch.empty(0, 16).cuda(), 3)
+    assert ids.shape == (0, 3) and w.shape == (0, 3)
+    r = qr.Routing.from_logits(torch.empty(0, 16).cuda(), 3)
+    assert r.offsets.tolist() == [0] * 17 and r.perm.numel() == 0
+    assert qr.route_grad(w, torch.empty(0, 16).cuda(), ids).shape == (0, 16)
+    place = torch.empty(0, 3, dtype=torch.int64).cuda()
+    assert qr.combine(torch.empty(0, 8).cuda(), place, w).shape == (0, 8)
+    dy, dw = qr.combine_grad(torch.empty(0, 8).cuda(), torch.empty(0, 8).cuda(), place, w)
+    assert dy.shape == (0, 8) and dw.shape == (0, 3)
+    none = torch.full((4, 3), -1).cuda()
+    assert (qr.combine(torch.empty(0, 8).cuda(), none, torch.rand(4, 3).cuda()) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_layer_from_logits_to_gradients(dtype):
+    """Router, experts and sum together, differentiated to the router's logits, against 64-bit autograd.  At most
+    eight 16-bit roundings in a row, as in the experts alone, the router's part being in fp32."""
+    qr = _qr()
+    T, E, k, H, F = 40, 12, 3, 64, 48
+    g = gen(6)
+    router = torch.randn(E, H, generator=g) / H**0.5
+    x = torch.randn(T, H, generator=g).to(dtype)
+    gate_up = (torch.randn(E, 2 * F, H, generator=g) / H**0.5).to(dtype)
+    down = (torch.randn(E, H, F, generator=g) / F**0.5).to(dtype)
+    dout = torch.randn(T, H, generator=g)
+    leaves = [t.to(FP64).requires_grad_() for t in (router, x, gate_up, down)]
+    lo = leaves[1].detach() @ leaves[0].t()
+    lo32 = lo.float()
+    ids, _ = reference(lo32.detach(), k, groups=4, keep_groups=2)
+    s = torch.sigmoid(lo).gather(1, ids.long())
+    w = 1.5 * s / s.sum(1, keepdim=True)
+    y = []
+    for t in range(T):
+        acc = 0
+        for j in range(k):
+            gu = leaves[2][ids[t, j]] @ leaves[1][t]
+            acc = acc + w[t, j] * (leaves[3][ids[t, j]] @ (torch.nn.functional.silu(gu[:F]) * gu[F:]))
+        y.append(acc)
+    want = torch.stack(y)
+    grads = torch.autograd.grad(want, leaves, dout.to(FP64))
+    rr, xx, gg, dd = [t.cuda().requires_grad_() for t in (router, x, gate_up, down)]
+    logit = lo32.detach().cuda() + (xx.detach().float() @ rr.t() - (xx.detach().float() @ rr.t()).detach())
+    r = qr.Routing.from_logits(logit, k, groups=4, keep_groups=2, scale=1.5)
+    assert torch.equal(r.ids.cpu(), ids)
+    out = qr.expert_ffn(xx, r, gg, dd)
+    out.backward(dout.cuda())
+    tol = 8 * UNIT[dtype]
+    for got, ref in zip((out, rr.grad, xx.grad, gg.grad, dd.grad), (want.detach(), *grads)):
+        assert float((got.detach().cpu().to(FP64) - ref).norm() / ref.norm()) <= tol
