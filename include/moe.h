@@ -422,6 +422,21 @@ int moe_combine_grad(int32_t dtype, const void *dout, int32_t dout_dtype, int64_
                      int64_t y_stride, int64_t pairs, const int64_t *place, const float *w, int64_t tokens,
                      int64_t top_k, int64_t cols, void *dy, int64_t dy_stride, float *dw, void *stream);
 
+/* The orthogonalised update of a batch of dense matrices g[batch][rows][cols]
+ * (fp32, bf16 or fp16): X = g / (|g| + eps) with the Frobenius norm, then
+ * `steps` times X <- c0 X + (c1 A + c2 A A) X with A = X X^T (for rows > cols
+ * the same on the transpose), to out of g's type; out may be g.  coefficients
+ * is a host array [steps][3], read during the call; it is refused where a
+ * singular value of at most 1 could pass 64.  Everything between the products
+ * has 22 bits, products are summed in fp32.  A matrix of zeros gives zeros,
+ * one with a NaN or an infinity NaN throughout.  rows and cols: at most
+ * 65536, the smaller at most 16384; steps at most 32.  The workspace holds as
+ * many matrices as fit 4 GiB at a time. */
+size_t moe_orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols);
+int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                      const float *coefficients, float eps, void *out, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /* Per-stage timing with HIP events.  While a profiler is attached to the
  * calling thread, every kernel a forward call launches records its own start
  * and end into two events (hipExtLaunchKernelGGL; dispatch latency between

@@ -117,6 +117,9 @@ _SIGS = {
     "moe_combine": ([_I32, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P], ctypes.c_int),
     "moe_combine_grad": ([_I32, _P, _I32, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P],
                          ctypes.c_int),
+    "moe_orthogonalize_bytes": ([_I64, _I64, _I64], _SZ),
+    "moe_orthogonalize": ([_I32, _P, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_float), ctypes.c_float, _P, _P, _SZ,
+                           _P], ctypes.c_int),
     "moe_stage_name": ([_I32], ctypes.c_char_p),
     "moe_prof_create": ([ctypes.POINTER(_P), _I32], ctypes.c_int),
     "moe_prof_destroy": ([_P], None),
@@ -320,7 +323,7 @@ class Profiler:
 from .layer import MoELayer  # noqa: E402
 from .expert_ops import (grouped_mm, grouped_mm_grad_a, grouped_mm_grad_b, mxfp4_dequantize,  # noqa: E402
                          mxfp4_grouped_mm, mxfp4_quantize, swiglu, swiglu_grad, swiglu_mxfp4)
-from .train_ops import combine, combine_grad, route, route_grad, sort_pairs  # noqa: E402
+from .train_ops import combine, combine_grad, orthogonalize, route, route_grad, sort_pairs  # noqa: E402
 from .experts import Mxfp4Experts, Routing, expert_ffn  # noqa: E402
 
 __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Profiler", "make_shape", "workspace_bytes",
@@ -329,4 +332,5 @@ __all__ = ["MoELayer", "MoEError", "Context", "Shape", "Weights", "Debug", "Prof
            "LIB_PATH", "Grouped", "grouped_mm", "grouped_mm_grad_a", "grouped_mm_grad_b", "mxfp4_quantize",
            "mxfp4_dequantize", "mxfp4_grouped_mm", "swiglu", "swiglu_mxfp4", "swiglu_grad",
            "Router", "PairOrder", "route", "route_grad", "sort_pairs", "combine", "combine_grad",
+           "orthogonalize",
            "Routing", "expert_ffn", "Mxfp4Experts"]

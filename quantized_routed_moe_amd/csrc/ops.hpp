@@ -43,6 +43,28 @@ struct CombineArgs {
     int32_t k;
 };
 
+// One step's coefficients and the powers of two by which its split matrices are scaled.
+struct OrthogonalStep {
+    float c0, c1, c2;
+    int32_t x, a, p;  // of X, A and P
+};
+constexpr int kMaxOrthogonalSteps = 32, kMaxOrthogonal = 16384;  // steps; the shorter side
+struct OrthogonalArgs {
+    const void *g;
+    void *out;
+    uint8_t *work;
+    int32_t batch, rows, cols, steps;
+    float eps;
+    OrthogonalStep step[kMaxOrthogonalSteps + 1];  // the last: X only
+};
+// X is m x n, m <= n; strides in bytes.
+struct OrthogonalSizes {
+    int32_t m, n, parts;
+    int64_t x_ld, a_ld, x_mat, a_mat;
+    // two X, A and P, the sums of squares and the factor of the norm
+    int64_t bytes() const { return 2 * x_mat + 2 * a_mat + 8 * (int64_t)parts + 4; }
+};
+
 // Tokens of a chunk of the pairs' order, and the chunks of T tokens.
 int32_t order_chunk(int64_t tokens);
 hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s);
@@ -50,6 +72,8 @@ hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s);
 hipError_t launch_sort_pairs(const void *ids, bool wide, int64_t tokens, int32_t k, int32_t E, const PairOrder &o,
                              hipStream_t s);
 hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStream_t s);
+OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols);
+hipError_t launch_orthogonal(int dt, const OrthogonalArgs &a, hipStream_t s);
 hipError_t launch_combine_grad(int dt, int dout_dt, const CombineArgs &a, hipStream_t s);
 
 }  // namespace qrmoe

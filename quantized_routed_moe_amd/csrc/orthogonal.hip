@@ -1,0 +1,637 @@
+// The orthogonalised update: a matrix with the row and column space of g and
+// singular values near 1, by Newton-Schulz products.
+//
+//   X = g / (|g| + eps), transposed where g is tall;  steps times
+//     A = X X^T,   P = a I + b A + c A A,   X <- P X
+//
+// Small singular values grow by `a` a step, and so does whatever a rounding
+// put beside them: 16 bits would show in the result (a step of 2^-12 can come
+// out 500 times as large).  Everything between the products is therefore kept
+// as two fp16 numbers, hi + lo, 22 bits, scaled by a power of two so that both
+// stay clear of fp16's ends, and a product is three: hi hi + hi lo + lo hi,
+// summed in fp32 by the matrix units.  What is left out, lo lo, is 2^-22.
+//
+// Layout of a split matrix: rows of 128-byte chunks, 32 hi and the same 32 lo
+// elements each, rows padded with zeros to whole chunks.  One K step of an
+// operand is a chunk of every row of the tile (or 32 rows of its columns), so
+// hi and lo arrive together and each is multiplied from registers by both
+// parts of the other operand: 48 matrix instructions a wave for the copies
+// that 32 of a plain 16-bit product need.
+//
+// A and P are symmetric: the tiles on and below the diagonal are computed, a
+// tile below is stored a second time, transposed on the way by LDS reads.
+// The norm is taken out as a power of two when X is made, which is exact; what
+// is left of it, a factor in (1, 2], goes into the first step's products.
+#include <type_traits>
+
+#include "mxfp4.hpp"
+#include "ops.hpp"
+
+namespace qrmoe {
+
+namespace {
+
+constexpr int kCus = 256, kXcds = 8;
+constexpr int kChunk = 128;  // bytes of 32 split elements
+enum : int { kGram = 0, kPoly = 1, kApply = 2 };
+
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unroll(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, I + 1>(f);
+    }
+}
+
+typedef __attribute__((address_space(3))) i16x4 *lds_i16x4;
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// v as two fp16 numbers.  Each conversion rounds to nearest even: v is off by 2^-22 of itself, or 2^-25 where that is
+// more (the values are scaled to at most 2^15).
+__device__ __forceinline__ void split(float v, _Float16 &hi, _Float16 &lo) {
+    hi = (_Float16)v;
+    lo = (_Float16)(v - (float)hi);
+}
+
+struct GemmArgs {
+    const uint8_t *x, *y, *add;  // add: kPoly, A
+    uint8_t *out;
+    int64_t x_ld, y_ld, out_ld;     // row strides, bytes (add: as out)
+    int64_t x_mat, y_mat, out_mat;  // a matrix of the batch, bytes (add: as out)
+    int32_t rows, cols;             // of the output; cols padded to whole chunks
+    int32_t y_rows;                 // kApply: contraction rows that y has
+    int32_t steps;                  // chunks of the contraction
+    int32_t batch, m_tiles, n_tiles;
+    float scale;                    // of the sum: kGram, kApply
+    float c0, c1, c2;               // kPoly: identity, A, A A
+    const float *rest;              // what is left of each matrix's norm, or null
+};
+
+// Place in the list of tiles of turn b: runs of `run` consecutive tiles go to one XCD.
+__device__ __forceinline__ int xcd_tile(int b, int run) {
+    const int i = b / kXcds;
+    return (i / run * kXcds + b % kXcds) * run + i % run;
+}
+
+struct Tile {
+    int b, m, n;  // matrix, tile row, tile column
+};
+
+// XL, YL: whether the operand has a lo part.
+template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU>
+__global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split_gemm_kernel(GemmArgs a) {
+    constexpr bool YCOL = MODE == kApply, TRI = !YCOL;
+    constexpr int NW = WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
+    constexpr int XB = BM * kChunk, YB = BN * kChunk, STAGE = XB + YB;
+    constexpr int XC = BM / 8 / NW, YC = BN / 8 / NW;  // 1 KB copies of each wave and step
+    constexpr int OUT_ROW = BN * 4;
+    static_assert(!TRI || BM == BN, "tiles of a symmetric product are square");
+    __shared__ __align__(1024) uint8_t smem[2 * STAGE + 32 * OUT_ROW];
+    uint8_t *const sout = smem + 2 * STAGE;
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+
+    // ---- the list of tiles: lower triangle row by row, or eight row tiles advancing through the columns together
+    const int each = TRI ? a.m_tiles * (a.m_tiles + 1) / 2 : a.m_tiles * a.n_tiles;
+    const int total = each * a.batch, run = kCus / kXcds * PER_CU;
+    auto find = [&](int turn, Tile &t) -> bool {
+        const int at = xcd_tile(blockIdx.x + turn * gridDim.x, run);
+        if (at >= total) {
+            t = Tile{0, 0, 0};
+            return false;
+        }
+        t.b = at / each;
+        const int r = at - t.b * each;
+        if constexpr (TRI) {
+            int m = (int)((__builtin_sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
+            while ((m + 1) * (m + 2) / 2 <= r) ++m;
+            while (m * (m + 1) / 2 > r) --m;
+            t.m = m;
+            t.n = r - m * (m + 1) / 2;
+        } else {
+            const int g = r / (8 * a.n_tiles), gm = min(8, a.m_tiles - 8 * g), q = r - g * 8 * a.n_tiles;
+            t.m = 8 * g + q % gm;
+            t.n = q / gm;
+        }
+        t.b = __builtin_amdgcn_readfirstlane(t.b);
+        t.m = __builtin_amdgcn_readfirstlane(t.m);
+        t.n = __builtin_amdgcn_readfirstlane(t.n);
+        return true;
+    };
+
+    // ---- the stream of copies.  Row operand: piece c (16 bytes) of row r in slot c ^ ((r >> 1) & 7); column operand:
+    // [32][4 BN bytes], piece c of row d in slot c ^ ((d & 3) << 2).
+    constexpr int kPer = BN * 4 / 16;  // pieces of a row of a column operand
+    uint32_t xoff[XC], yoff[YC];
+    const uint8_t *cx = nullptr, *cy = nullptr;
+    int cturn = -1, cleft = 0, crows = 0;  // tile being sent for, its steps left, contraction rows left (kApply)
+    auto x_row = [&](int i) { return (wave * XC + i) * 8 + (lane >> 3); };
+    auto y_row = [&](int i) { return YCOL ? (wave * YC + i) * (64 / kPer) + lane / kPer : (wave * YC + i) * 8 + (lane >> 3); };
+    auto next_tile = [&] {
+        Tile t;
+        const bool more = find(++cturn, t);
+        cleft = more ? a.steps : 0x7fffffff;  // past the end: copies of nothing
+        crows = a.y_rows;
+        cx = a.x + t.b * a.x_mat + (int64_t)t.m * BM * a.x_ld;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            const int r = x_row(i);
+            xoff[i] = more && t.m * BM + r < a.rows ? (uint32_t)(r * a.x_ld + 16 * ((lane & 7) ^ ((r >> 1) & 7))) : kOob;
+        }
+        cy = a.y + t.b * a.y_mat + (YCOL ? (int64_t)t.n * BN * 4 : (int64_t)t.n * BN * a.y_ld);
+#pragma unroll
+        for (int i = 0; i < YC; ++i) {
+            const int r = y_row(i);
+            if constexpr (YCOL) {
+                const int p = (lane % kPer) ^ ((r & 3) << 2);
+                yoff[i] = more && t.n * BN + 4 * p < a.cols ? (uint32_t)(r * a.y_ld + 16 * p) : kOob;
+            } else {
+                yoff[i] = more && t.n * BN + r < a.rows ? (uint32_t)(r * a.y_ld + 16 * ((lane & 7) ^ ((r >> 1) & 7))) : kOob;
+            }
+        }
+    };
+    const uint32_t lds0 = lds_addr(smem);
+    struct Copy {
+        i32x4 rx, ry;
+        uint32_t lx, ly;
+    };
+    auto begin_copy = [&](int stg) {
+        const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + stg * STAGE);
+        return Copy{dma_rsrc(cx), dma_rsrc(cy), base + wave * (XC * 1024), base + XB + wave * (YC * 1024)};
+    };
+    auto send = [&](const Copy &c, auto idx) {
+        constexpr int I = decltype(idx)::value;
+        if constexpr (I < XC) dma16_async(c.rx, c.lx + I * 1024, xoff[I]);
+        else dma16_async(c.ry, c.ly + (I - XC) * 1024, !YCOL || y_row(I - XC) < crows ? yoff[I - XC] : kOob);
+    };
+    auto end_copy = [&] {
+        if (--cleft == 0) {
+            next_tile();
+        } else {
+            cx += kChunk;
+            cy += YCOL ? 32 * a.y_ld : kChunk;
+            crows -= 32;
+        }
+    };
+
+    // ---- operand reads: 32 rows (columns) at w0, elements 16 s + 8 half .. +7 of the step, hi (L 0) or lo (1)
+    const int swz = (l32 >> 1) & 7;
+    auto read_row = [&](const uint8_t *t, int w0, int s, int L) -> i32x4 {
+        return *reinterpret_cast<const i32x4 *>(t + (w0 + l32) * kChunk + 16 * ((4 * L + 2 * s + half) ^ swz));
+    };
+    const int tr_d = 8 * half + ((lane & 15) >> 2), tr_c = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    auto read_col = [&](const uint8_t *t, int w0, int s, int L) -> i32x4 {
+        const int d = 16 * s + tr_d, at = (w0 >> 5) * kChunk + 64 * L + 2 * tr_c;
+        const uint8_t *p = t + d * OUT_ROW + (((at >> 4) ^ ((d & 3) << 2)) << 4) + (at & 15);
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4)p);
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4)(p + 4 * OUT_ROW));
+        struct { i16x4 a, b; } both{lo, hi};
+        return __builtin_bit_cast(i32x4, both);
+    };
+
+    // ---- a tile's product.  A step is two halves s of 16 elements, each three groups of MFMAs: hi hi, hi lo, lo hi.
+    // A group's operands are read during the group before.  A step's stage is free before its last group: there the
+    // waves meet, the next step has arrived, and one more is sent for.
+    constexpr int kCopies = XC + YC;
+    const int wrow = wm * MI * 32, wcol = wn * NI * 32;
+    int stg = 0;
+    f32x16 acc[MI][NI];
+    auto product = [&] {
+        i32x4 xh[MI], xl[XL ? MI : 1], yh[2][NI], yl[YL ? NI : 1];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
+        auto read_x = [&](i32x4 &v, int st, int i, int s, int L) { v = read_row(smem + st * STAGE, wrow + i * 32, s, L); };
+        auto read_y = [&](i32x4 &v, int st, int j, int s, int L) {
+            const uint8_t *t = smem + st * STAGE + XB;
+            v = YCOL ? read_col(t, wcol + j * 32, s, L) : read_row(t, wcol + j * 32, s, L);
+        };
+        auto mul = [&](const i32x4 &y, const i32x4 &x, f32x16 &c) { c = mfma32<Elt::F16, 0>(y, x, c, 0, 0); };
+        constexpr int kMf = MI * NI;
+        // what runs beside the MFMAs of a group: `reads` reads and `sends` copies, spread evenly
+        auto group = [&](auto &&mm, auto reads_c, auto &&rd, auto sends_c, const Copy &c) {
+            constexpr int R = decltype(reads_c)::value, S = decltype(sends_c)::value;
+            unroll<kMf>([&](auto m_c) {
+                constexpr int m = decltype(m_c)::value;
+                mm(std::integral_constant<int, m / NI>{}, std::integral_constant<int, m % NI>{});
+                unroll<(m + 1) * R / kMf - m * R / kMf>([&](auto r_c) {
+                    rd(std::integral_constant<int, m * R / kMf + decltype(r_c)::value>{});
+                });
+                unroll<(m + 1) * S / kMf - m * S / kMf>([&](auto s_c) {
+                    send(c, std::integral_constant<int, m * S / kMf + decltype(s_c)::value>{});
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        constexpr std::integral_constant<int, 0> none{};
+        auto nothing = [](auto) {};
+#pragma unroll
+        for (int j = 0; j < NI; ++j) read_y(yh[0][j], stg, j, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) read_x(xh[i], stg, i, 0, 0);
+#pragma unroll 1
+        for (int k = 0; k < a.steps; ++k) {
+            // half 0
+            group([&](auto i, auto j) { mul(yh[0][j], xh[i], acc[i][j]); },
+                  std::integral_constant<int, (YL ? NI : 0) + (XL ? MI : 0)>{},
+                  [&](auto r) {
+                      constexpr int R = decltype(r)::value;
+                      if constexpr (YL && R < NI) read_y(yl[R], stg, R, 0, 1);
+                      else read_x(xl[R - (YL ? NI : 0)], stg, R - (YL ? NI : 0), 0, 1);
+                  },
+                  none, Copy{});
+            if constexpr (YL)
+                group([&](auto i, auto j) { mul(yl[j], xh[i], acc[i][j]); }, none, nothing, none, Copy{});
+            if constexpr (XL) {
+                group([&](auto i, auto j) { mul(yh[0][j], xl[i], acc[i][j]); }, std::integral_constant<int, NI + MI>{},
+                      [&](auto r) {
+                          constexpr int R = decltype(r)::value;
+                          if constexpr (R < NI) read_y(yh[1][R], stg, R, 1, 0);
+                          else read_x(xh[R - NI], stg, R - NI, 1, 0);
+                      },
+                      none, Copy{});
+            } else {
+#pragma unroll
+                for (int j = 0; j < NI; ++j) read_y(yh[1][j], stg, j, 1, 0);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) read_x(xh[i], stg, i, 1, 0);
+            }
+            // half 1; the last group runs on the other side of the barrier
+            auto hand_over = [&] {
+                wait_vm<0>();
+                lds_barrier();
+            };
+            auto ahead = [&](auto r) {  // the next step's first operands
+                constexpr int R = decltype(r)::value;
+                if constexpr (R < NI) read_y(yh[0][R], stg, R, 0, 0);
+                else read_x(xh[R - NI], stg, R - NI, 0, 0);
+            };
+            constexpr std::integral_constant<int, NI + MI> all{};
+            constexpr std::integral_constant<int, kCopies> copies{};
+            if constexpr (XL) {
+                group([&](auto i, auto j) { mul(yh[1][j], xh[i], acc[i][j]); },
+                      std::integral_constant<int, (YL ? NI : 0) + MI>{},
+                      [&](auto r) {
+                          constexpr int R = decltype(r)::value;
+                          if constexpr (YL && R < NI) read_y(yl[R], stg, R, 1, 1);
+                          else read_x(xl[R - (YL ? NI : 0)], stg, R - (YL ? NI : 0), 1, 1);
+                      },
+                      none, Copy{});
+                if constexpr (YL)
+                    group([&](auto i, auto j) { mul(yl[j], xh[i], acc[i][j]); }, none, nothing, none, Copy{});
+                hand_over();
+                const Copy c = begin_copy(stg);
+                stg ^= 1;
+                group([&](auto i, auto j) { mul(yh[1][j], xl[i], acc[i][j]); }, all, ahead, copies, c);
+            } else {
+                // only hi hi: the operands are in registers, but xh is read for the next step while it is used
+                i32x4 now[MI];
+#pragma unroll
+                for (int i = 0; i < MI; ++i) now[i] = xh[i];
+                hand_over();
+                const Copy c = begin_copy(stg);
+                stg ^= 1;
+                group([&](auto i, auto j) { mul(yh[1][j], now[i], acc[i][j]); }, all, ahead, copies, c);
+            }
+            end_copy();
+        }
+    };
+
+    // ---- out, through LDS in blocks of 32 rows of fp32 sums; register 4 q + u of a 32x32 tile holds column
+    // 8 q + 4 half + u of row l32.  16-byte slot c of row r is at c ^ (r & 63).  Eight columns (two slots) become
+    // eight hi and eight lo elements of the same place, from which the transposed copy is read.
+    auto slot_of = [&](int r, int c) { return sout + r * OUT_ROW + ((c ^ (r & (OUT_ROW / 16 - 1))) << 4); };
+    auto finish = [&](const Tile &t) {
+        const float rest = a.rest ? a.rest[t.b] : 1.0f;
+        const float scale = a.scale * (MODE == kGram ? rest * rest : rest);
+        uint8_t *out = a.out + t.b * a.out_mat;
+        const uint8_t *add = a.add + t.b * a.out_mat;
+        const int m0 = t.m * BM, n0 = t.n * BN;
+        const bool mirror = TRI && t.m != t.n;
+        unroll<WM * MI>([&](auto part_c) {
+            constexpr int part = decltype(part_c)::value, w0 = part / MI, i = part % MI;
+            const int r0 = m0 + w0 * MI * 32 + i * 32;  // the block's first row
+            if (r0 >= a.rows) return;
+            if (wm == w0) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                        *reinterpret_cast<f32x4 *>(slot_of(l32, ((wn * NI + j) * 32 + 8 * q + 4 * half) >> 2)) = v;
+                    }
+            }
+            lds_barrier();
+            constexpr int kUnits = 32 * BN / 8;
+#pragma unroll
+            for (int s = 0; s < kUnits / (NW * 64); ++s) {
+                const int p = s * NW * 64 + tid, r = p / (BN / 8), u = p % (BN / 8);  // row of the block, eight columns
+                uint8_t *s0 = slot_of(r, 2 * u), *s1 = slot_of(r, 2 * u + 1);
+                const f32x4 v0 = *reinterpret_cast<f32x4 *>(s0), v1 = *reinterpret_cast<f32x4 *>(s1);
+                float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                const int row = r0 + r, col = n0 + 8 * u;
+                const bool in = row < a.rows && col < a.cols;
+                const int64_t at = row * a.out_ld + (col >> 5) * kChunk + (col & 31) * 2;
+                if constexpr (MODE == kPoly) {
+                    f16x8 h{}, l{};
+                    if (in) {
+                        h = *reinterpret_cast<const f16x8 *>(add + at);
+                        l = *reinterpret_cast<const f16x8 *>(add + at + 64);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = __builtin_fmaf(a.c2, v[e], a.c1 * ((float)h[e] + (float)l[e])) + (row == col + e ? a.c0 : 0.0f);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= scale;
+                }
+                f16x8 h, l;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    _Float16 x, y;
+                    split(v[e], x, y);
+                    h[e] = x;
+                    l[e] = y;
+                }
+                if (in) {
+                    *reinterpret_cast<f16x8 *>(out + at) = h;
+                    *reinterpret_cast<f16x8 *>(out + at + 64) = l;
+                }
+                if (mirror) {
+                    *reinterpret_cast<f16x8 *>(s0) = h;
+                    *reinterpret_cast<f16x8 *>(s1) = l;
+                }
+            }
+            lds_barrier();
+            if (mirror) {
+                // rows of the transposed tile are columns here: 32 of them at a time, the chunk of the block's 32 rows;
+                // a lane gets elements 8 half .. +7 (16 s further) of column w + l32, hi or lo
+                for (int w = wave * 32; w < BN; w += NW * 32) {
+                    const int row = n0 + w + l32;
+#pragma unroll
+                    for (int L = 0; L < 2; ++L)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int d = 16 * s + tr_d, c = w + tr_c;
+                            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (lds_i16x4)(slot_of(d, 2 * (c >> 3) + L) + (c & 7) * 2));
+                            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (lds_i16x4)(slot_of(d + 4, 2 * (c >> 3) + L) + (c & 7) * 2));
+                            struct { i16x4 a, b; } both{lo, hi};
+                            if (row < a.rows)
+                                *reinterpret_cast<i32x4 *>(out + row * a.out_ld + (r0 >> 5) * kChunk + 64 * L + 32 * s +
+                                                           16 * half) = __builtin_bit_cast(i32x4, both);
+                        }
+                }
+                lds_barrier();
+            }
+        });
+    };
+
+    next_tile();
+    auto copy_step = [&](int s) {
+        const Copy c = begin_copy(s);
+        unroll<kCopies>([&](auto i) { send(c, i); });
+        end_copy();
+    };
+    copy_step(0);
+    wait_vm<0>();
+    copy_step(1);
+    lds_barrier();
+    Tile t;
+    for (int turn = 0; find(turn, t); ++turn) {
+        product();
+        finish(t);
+    }
+    wait_vm<0>();
+}
+
+// -------------------------------------------------------------- in and out
+// The norm of each matrix: 64-bit sums of squares, `parts` of them a matrix.
+template <int DT>
+__device__ __forceinline__ float element(const void *p, int64_t at) {
+    if constexpr (DT == kDtF32) return ((const float *)p)[at];
+    else if constexpr (DT == kDtBf16) return (float)((const __bf16 *)p)[at];
+    else return (float)((const _Float16 *)p)[at];
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void norm_kernel(const void *g, int64_t n, int parts, double *sums) {
+    __shared__ double part[kThreads / 64];
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.x / parts, p = blockIdx.x % parts;
+    const int64_t per = ((n + parts - 1) / parts + 7) / 8 * 8, lo = p * per, hi = min(n, lo + per);
+    const int64_t base = b * n;
+    const bool wide = (uintptr_t)g % 16 == 0 && n % 8 == 0;
+    double s = 0;
+    if (wide) {
+        for (int64_t i = lo + 8 * tid; i < hi; i += 8 * kThreads) {
+            float v[8];
+            load8<DT>(g, base + i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += (double)v[j] * v[j];
+        }
+    } else {
+        for (int64_t i = lo + tid; i < hi; i += kThreads) {
+            const double v = element<DT>(g, base + i);
+            s += v * v;
+        }
+    }
+    s = wave_sum_f64(s);
+    if ((tid & 63) == 0) part[tid >> 6] = s;
+    __syncthreads();
+    if (tid == 0) sums[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+}
+
+// X split and scaled to 2^scale times g / 2^e, 2^e the power of two above the norm; rest: 2^e / norm.  A workgroup
+// takes 64 rows by 64 columns of X; where g is tall they are read transposed, through LDS.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void split_kernel(const void *g, int rows, int cols, bool tall, int parts,
+                                                         const double *sums, float eps, int scale, uint8_t *x,
+                                                         int64_t x_ld, int64_t x_mat, float *rest) {
+    __shared__ float tile[64][65];
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.z;
+    double s = 0;
+    for (int i = 0; i < parts; ++i) s += sums[b * parts + i];
+    const double norm = sqrt(s) + eps;
+    int e = 0;
+    frexp(norm, &e);  // norm = f 2^e, f in [1/2, 1)
+    const bool usual = norm > 0 && norm < INFINITY;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
+        rest[b] = usual ? (float)(ldexp(1.0, e) / norm) : norm == 0 ? 1.0f : NAN;
+    if (!usual) e = 0;
+    const int m = tall ? cols : rows, n = tall ? rows : cols;  // of X
+    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+    const int64_t base = b * rows * cols;
+    const int c = tid & 63;
+    for (int r = tid >> 6; r < 64; r += kThreads / 64) {
+        // consecutive threads read consecutive elements of g
+        const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + c;
+        const float v = gr < rows && gc < cols ? ldexpf(element<DT>(g, base + (int64_t)gr * cols + gc), scale - e) : 0.0f;
+        if (tall) tile[c][r] = v;
+        else tile[r][c] = v;
+    }
+    __syncthreads();
+    for (int p = tid; p < 64 * 8; p += kThreads) {
+        const int r = p >> 3, u = p & 7;
+        const int row = m0 + r, col = n0 + 8 * u;
+        if (row >= m || col >= (n + 31) / 32 * 32) continue;
+        f16x8 h, l;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            _Float16 a, d;
+            split(tile[r][8 * u + i], a, d);
+            h[i] = a;
+            l[i] = d;
+        }
+        uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
+        *reinterpret_cast<f16x8 *>(o) = h;
+        *reinterpret_cast<f16x8 *>(o + 64) = l;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void put(void *p, int64_t at, float v) {
+    if constexpr (DT == kDtF32) ((float *)p)[at] = v;
+    else if constexpr (DT == kDtBf16) ((__bf16 *)p)[at] = (__bf16)v;
+    else ((_Float16 *)p)[at] = (_Float16)v;
+}
+
+// The way back.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void join_kernel(const uint8_t *x, int64_t x_ld, int64_t x_mat, int scale,
+                                                        int rows, int cols, bool tall, void *out) {
+    __shared__ float tile[64][65];
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.z;
+    const int m = tall ? cols : rows, n = tall ? rows : cols;
+    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+    const float back = ldexpf(1.0f, -scale);
+    for (int p = tid; p < 64 * 8; p += kThreads) {
+        const int r = p >> 3, u = p & 7;
+        const int row = m0 + r, col = n0 + 8 * u;
+        if (row >= m || col >= (n + 31) / 32 * 32) continue;
+        const uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
+        const f16x8 h = *reinterpret_cast<const f16x8 *>(o), l = *reinterpret_cast<const f16x8 *>(o + 64);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tile[r][8 * u + i] = ((float)h[i] + (float)l[i]) * back;
+    }
+    __syncthreads();
+    const int64_t base = b * rows * cols;
+    const int c = tid & 63;
+    for (int r = tid >> 6; r < 64; r += kThreads / 64) {
+        const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + c;
+        if (gr < rows && gc < cols) put<DT>(out, base + (int64_t)gr * cols + gc, tall ? tile[c][r] : tile[r][c]);
+    }
+}
+
+inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU>
+hipError_t launch_tiles(GemmArgs a, int out_cols, hipStream_t s) {
+    a.m_tiles = ceil_div(a.rows, BM);
+    a.n_tiles = ceil_div(out_cols, BN);
+    klaunch(split_gemm_kernel<MODE, XL, YL, BM, BN, WM, WN, PER_CU>, dim3(kCus * PER_CU), dim3(WM * WN * 64), s, a);
+    return hipGetLastError();
+}
+
+template <int MODE, bool XL, bool YL>
+hipError_t launch_product(const GemmArgs &a, hipStream_t s) {
+    const int64_t m = ceil_div(a.rows, 256), n = ceil_div(a.cols, 256);
+    const int64_t tiles = a.batch * (MODE == kApply ? m * n : m * (m + 1) / 2);
+    if (tiles >= kCus) return launch_tiles<MODE, XL, YL, 256, 256, 2, 4, 1>(a, a.cols, s);
+    return launch_tiles<MODE, XL, YL, 128, 128, 2, 2, 2>(a, a.cols, s);
+}
+
+}  // namespace
+
+// Buffers of the matrices of one pass, `each` bytes apart where they belong to one matrix.
+OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols) {
+    OrthogonalSizes z;
+    z.m = (int32_t)(rows < cols ? rows : cols);
+    z.n = (int32_t)(rows < cols ? cols : rows);
+    z.x_ld = (int64_t)ceil_div(z.n, 32) * kChunk;
+    z.a_ld = (int64_t)ceil_div(z.m, 32) * kChunk;
+    z.x_mat = z.m * z.x_ld;
+    z.a_mat = z.m * z.a_ld;
+    const int64_t want = rows * cols / 32768;  // elements a workgroup sums
+    z.parts = (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want);
+    return z;
+}
+
+hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
+    const OrthogonalSizes z = orthogonal_sizes(o.rows, o.cols);
+    const bool tall = o.rows > o.cols;
+    uint8_t *x[2] = {o.work, o.work + o.batch * z.x_mat}, *A = x[1] + o.batch * z.x_mat, *P = A + o.batch * z.a_mat;
+    double *sums = (double *)(P + o.batch * z.a_mat);
+    float *rest = (float *)(sums + o.batch * z.parts);
+    const dim3 block(kThreads), blocks64(ceil_div(z.n, 64), ceil_div(z.m, 64), o.batch);
+    auto in = [&](auto d) {
+        constexpr int DT = decltype(d)::value;
+        klaunch(norm_kernel<DT>, dim3(o.batch * z.parts), block, s, o.g, (int64_t)o.rows * o.cols, (int)z.parts, sums);
+        klaunch(split_kernel<DT>, blocks64, block, s, o.g, (int)o.rows, (int)o.cols, tall, (int)z.parts,
+                (const double *)sums, o.eps, (int)o.step[0].x, x[0], z.x_ld, z.x_mat, rest);
+        return hipGetLastError();
+    };
+    hipError_t err = dt == kDtF32 ? in(std::integral_constant<int, kDtF32>{})
+                                  : dt == kDtBf16 ? in(std::integral_constant<int, kDtBf16>{})
+                                                  : in(std::integral_constant<int, kDtF16>{});
+    for (int k = 0; k < o.steps && err == hipSuccess; ++k) {
+        const OrthogonalStep &t = o.step[k];
+        const uint8_t *now = x[k & 1];
+        GemmArgs a{};
+        a.batch = o.batch;
+        a.rest = k == 0 ? rest : nullptr;
+        // 16-bit input has no lo part: it is as it was but for a power of two
+        const bool lo = k > 0 || dt == kDtF32;
+        // A
+        a.x = a.y = now;
+        a.x_ld = a.y_ld = z.x_ld;
+        a.x_mat = a.y_mat = z.x_mat;
+        a.out = A;
+        a.out_ld = z.a_ld;
+        a.out_mat = z.a_mat;
+        a.rows = z.m;
+        a.cols = ceil_div(z.m, 32) * 32;
+        a.steps = ceil_div(z.n, 32);
+        a.scale = ldexpf(1.0f, t.a - 2 * t.x);
+        err = lo ? launch_product<kGram, true, true>(a, s) : launch_product<kGram, false, false>(a, s);
+        if (err != hipSuccess) break;
+        // P
+        a.x = a.y = a.add = A;
+        a.x_ld = a.y_ld = z.a_ld;
+        a.x_mat = a.y_mat = z.a_mat;
+        a.out = P;
+        a.steps = ceil_div(z.m, 32);
+        a.rest = nullptr;
+        a.c0 = ldexpf(t.c0, t.p);
+        a.c1 = ldexpf(t.c1, t.p - t.a);
+        a.c2 = ldexpf(t.c2, t.p - 2 * t.a);
+        err = launch_product<kPoly, true, true>(a, s);
+        if (err != hipSuccess) break;
+        // X
+        a.x = P;
+        a.y = now;
+        a.y_ld = z.x_ld;
+        a.y_mat = z.x_mat;
+        a.out = x[(k + 1) & 1];
+        a.out_ld = z.x_ld;
+        a.out_mat = z.x_mat;
+        a.cols = ceil_div(z.n, 32) * 32;
+        a.y_rows = z.m;
+        a.rest = k == 0 ? rest : nullptr;
+        a.scale = ldexpf(1.0f, o.step[k + 1].x - t.x - t.p);
+        err = lo ? launch_product<kApply, true, true>(a, s) : launch_product<kApply, true, false>(a, s);
+    }
+    if (err != hipSuccess) return err;
+    auto k = dt == kDtF32 ? join_kernel<kDtF32> : dt == kDtBf16 ? join_kernel<kDtBf16> : join_kernel<kDtF16>;
+    klaunch(k, blocks64, block, s, (const uint8_t *)x[o.steps & 1], z.x_ld, z.x_mat, (int)o.step[o.steps].x, (int)o.rows,
+            (int)o.cols, tall, o.out);
+    return hipGetLastError();
+}
+
+}  // namespace qrmoe

@@ -3,6 +3,9 @@
 // Nothing is allocated and nothing synchronises.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "checks.hpp"
 #include "ops.hpp"
 
@@ -102,9 +105,99 @@ int check_cols(int64_t cols) {
     return cols % 8 != 0 || cols > kMaxFeatures ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// Matrices that one pass of the orthogonalised update takes: as many as fit 4 GiB of workspace (several rounds of
+// tiles for 256 CUs at any size), one at least.
+constexpr int64_t kOrthogonalBytes = (int64_t)4 << 30;
+int64_t orthogonal_pass(const OrthogonalSizes &z, int64_t batch) {
+    return std::max<int64_t>(1, std::min({batch, kOrthogonalBytes / z.bytes(), (int64_t)65535}));
+}
+
+// The largest |c0 s + c1 s^3 + c2 s^5| (odd) or |c0 + c1 l + c2 l^2| over s in [0, u], l = s^2: at the ends or where
+// the derivative is 0.
+double largest(const float *c, double u, bool odd) {
+    auto at = [&](double l) { return std::fabs(c[0] + c[1] * l + c[2] * l * l) * (odd ? std::sqrt(l) : 1.0); };
+    // odd: c0 + 3 c1 l + 5 c2 l^2 = 0; even: c1 + 2 c2 l = 0
+    double most = std::max(at(0), at(u * u));
+    auto look = [&](double l) {
+        if (l > 0 && l < u * u) most = std::max(most, at(l));
+    };
+    if (!odd) {
+        if (c[2] != 0) look(-c[1] / (2.0 * c[2]));
+    } else {
+        const double A = 5.0 * c[2], B = 3.0 * c[1], C = c[0], D = B * B - 4 * A * C;
+        if (A == 0) {
+            if (B != 0) look(-C / B);
+        } else if (D >= 0) {
+            look((-B + std::sqrt(D)) / (2 * A));
+            look((-B - std::sqrt(D)) / (2 * A));
+        }
+    }
+    return most;
+}
+// The power of two that takes values of at most `most` to 2^14 .. 2^15, half of what fp16 holds.
+int32_t scale_of(double most) { return most > 0 ? std::min(15, (int)std::floor(std::log2(32768.0 / most))) : 15; }
+
+// Scales of every step from the largest singular values that can come up; past 64 the steps do not converge.
+int plan_orthogonal(const float *c, int32_t steps, OrthogonalArgs &o) {
+    double u = 1;
+    for (int32_t k = 0; k < steps; ++k) {
+        OrthogonalStep &t = o.step[k];
+        const float *q = c + 3 * k;
+        if (!std::isfinite(q[0]) || !std::isfinite(q[1]) || !std::isfinite(q[2])) return MOE_ERR_INVALID_ARG;
+        t = OrthogonalStep{q[0], q[1], q[2], scale_of(u), scale_of(u * u), scale_of(largest(q, u, false))};
+        u = largest(q, u, true) * 1.001;  // fp32's rounding is far below that
+        if (!(u <= 64)) return MOE_ERR_INVALID_ARG;
+    }
+    o.step[steps] = OrthogonalStep{0, 0, 0, scale_of(u), 0, 0};
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    if (batch < 1 || rows < 1 || cols < 1 || std::max(rows, cols) > kMaxFeatures || std::min(rows, cols) > kMaxOrthogonal)
+        return 0;
+    const OrthogonalSizes z = orthogonal_sizes(rows, cols);
+    return (size_t)(orthogonal_pass(z, batch) * z.bytes());
+}
+
+int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                      const float *coefficients, float eps, void *out, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    if (!known_dtype(dtype) || batch < 0 || rows < 1 || cols < 1 || steps < 1 || !coefficients) return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    if (std::max(rows, cols) > kMaxFeatures || std::min(rows, cols) > kMaxOrthogonal || steps > kMaxOrthogonalSteps)
+        return MOE_ERR_UNSUPPORTED;
+    const int bytes = dt_bytes(dtype);
+    if (batch > INT64_MAX / (rows * cols * bytes)) return MOE_ERR_INVALID_ARG;
+    const Mat mg = array(g, batch * rows * cols, bytes), mo = array(out, batch * rows * cols, bytes);
+    MOE_TRY(check_array(mg));
+    MOE_TRY(check_array(mo));
+    OrthogonalArgs o{};
+    MOE_TRY(plan_orthogonal(coefficients, steps, o));
+    if (g != out && overlap(mo, mg)) return MOE_ERR_INVALID_ARG;
+    if (batch == 0) return MOE_OK;
+    const size_t need = moe_orthogonalize_bytes(batch, rows, cols);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    const Mat mw = array(workspace, (int64_t)need, 1);
+    MOE_TRY(check_array(mw));
+    if (overlap(mw, mg) || overlap(mw, mo)) return MOE_ERR_INVALID_ARG;
+    const int64_t pass = orthogonal_pass(orthogonal_sizes(rows, cols), batch);
+    o.work = (uint8_t *)workspace;
+    o.rows = (int32_t)rows;
+    o.cols = (int32_t)cols;
+    o.steps = steps;
+    o.eps = eps;
+    for (int64_t b = 0; b < batch; b += pass) {
+        o.g = (const uint8_t *)g + b * rows * cols * bytes;
+        o.out = (uint8_t *)out + b * rows * cols * bytes;
+        o.batch = (int32_t)std::min(pass, batch - b);
+        MOE_TRY(status_of(launch_orthogonal(dtype, o, (hipStream_t)stream)));
+    }
+    return MOE_OK;
+}
 
 size_t moe_pair_order_bytes(int64_t tokens, int32_t n_experts) {
     if (tokens < 0 || tokens > MOE_MAX_PAIRS || n_experts < 1 || n_experts > 1024) return 0;

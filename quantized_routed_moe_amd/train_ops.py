@@ -1,5 +1,6 @@
 """Operators around the experts' products: the router with the order of its
-pairs and its gradient, and the sum of a token's pairs with its gradients.
+pairs and its gradient, the sum of a token's pairs with its gradients, and the
+orthogonalised update of a bank.
 
 Argument checks and marshalling only, with the conventions of expert_ops: HIP
 kernels behind the C ABI of include/moe.h, enqueued on `stream` (the current
@@ -216,3 +217,42 @@ def combine_grad(dout, y, place, w=None, dy=None, dw=None, stream=None):
     if graph is None:
         return dy, dw
     return tuple(_Refusal.apply(graph, t, *operands) for t in (dy, dw))
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)  # small singular values grow 3.4445 a step; all end in about 0.7 .. 1.2
+
+
+def orthogonalize(g, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, stream=None):
+    """The update that an orthogonalising optimiser makes of a gradient or its momentum g [.., rows, cols] (fp32, bf16
+    or fp16, dense; a bank is a batch of matrices), each matrix by itself, in g's type.
+
+    X = g / (|g| + eps) with the Frobenius norm, then `steps` times X <- a X + (b A + c A A) X with A = X X^T: the
+    singular vectors of g, the singular values near 1.  `coefficients` is (a, b, c), or one such triple for each step.
+    A matrix of zeros (an expert without tokens) gives zeros, one with a NaN or an infinity NaN throughout.  Values
+    between the products have 22 bits.  `out` may be g itself."""
+    _dtype(g, "g", _FLOATS)
+    _layout(g, "g")
+    if g.dim() < 2 or g.shape[-1] < 1 or g.shape[-2] < 1:
+        raise ValueError(f"g: expected [.., rows, cols], got {tuple(g.shape)}")
+    rows, cols = g.shape[-2:]
+    batch = g.numel() // (rows * cols)
+    each = [tuple(coefficients)] * steps if not hasattr(coefficients[0], "__len__") else [tuple(c) for c in coefficients]
+    if len(each) != steps or any(len(c) != 3 for c in each):
+        raise ValueError(f"coefficients: expected (a, b, c) or {steps} of them, got {coefficients!r}")
+    index, raw, side = _target(g, "g", stream)
+    graph = _graph("orthogonalize", out, g, instead="call it without gradients")
+    if out is None:
+        result = _new(g, tuple(g.shape), g.dtype, side)
+    else:
+        _layout(out, "out", g.dtype, tuple(g.shape))
+        result = out
+    n = _lib.moe_orthogonalize_bytes(batch, rows, cols)
+    work = _new(g, (n,), torch.uint8, side) if n else None
+    flat = (ctypes.c_float * (3 * steps))(*(x for c in each for x in c))
+    _check(_lib.moe_orthogonalize(DT[g.dtype], g.data_ptr(), batch, rows, cols, steps, flat, eps,
+                                  _plain(result, "out", index), work.data_ptr() if n else None, n, raw),
+           "moe_orthogonalize")
+    if out is not None:
+        _written(out)
+    _hold(side, g, work, out)
+    return result if graph is None else _Refusal.apply(graph, result, g)

@@ -572,3 +572,45 @@ def test_a_layer_from_logits_to_gradients(dtype):
     tol = 8 * UNIT[dtype]
     for got, ref in zip((out, rr.grad, xx.grad, gg.grad, dd.grad), (want.detach(), *grads)):
         assert float((got.detach().cpu().to(FP64) - ref).norm() / ref.norm()) <= tol
+
+
+# ------------------------------------------------------ orthogonalised update
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(g, steps=5, coefficients=QUINTIC, eps=1e-7):
+    """64 bits, on the host."""
+    each = [coefficients] * steps if not isinstance(coefficients[0], tuple) else coefficients
+    x = g.to(FP64)
+    x = x / (x.square().sum((-2, -1), keepdim=True).sqrt() + eps)
+    tall = x.shape[-2] > x.shape[-1]
+    x = x.transpose(-2, -1) if tall else x
+    for a, b, c in each:
+        aa = x @ x.transpose(-2, -1)
+        x = a * x + (b * aa + c * (aa @ aa)) @ x
+    return x.transpose(-2, -1) if tall else x
+
+
+def orthogonal_bound(want, dtype, steps=5, growth=3.4445, depth=1):
+    """What the output may be off by, as a norm.  Every number between the products is off by 2^-22 of itself (or
+    2^-39, where the scale ends), a product's sum by as much again (its terms' lo lo part, and fp32 additions, whose
+    errors are independent of each other: sqrt(depth) 2^-24, 2^-18 at most for 4096 terms).  A step's P and X pass
+    on what they get multiplied by at most `growth` and add three such errors of a matrix of |X| <= |want|:
+    the last step's weigh 1, those of the one before `growth` of what X was then, which was that much smaller where
+    it grew (singular values that have stopped growing are multiplied by at most 1.6, the derivative of the quintic
+    on [0.7, 1.2]).  So 3 * steps * 1.6^4 * (2^-22 + sqrt(depth) 2^-24), and the output's rounding."""
+    return (3 * steps * 1.6**4 * (2.0**-22 + depth**0.5 * 2.0**-24) + UNIT[dtype]) * float(want.norm()) + 1e-30
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (2, 3, 5), (33, 31), (64, 64), (5, 40, 130), (130, 40), (100, 257),
+                                   (3, 2, 65, 129), (300, 520), (2, 513, 260), (129, 1000), (700, 700)])
+def test_orthogonalize(dtype, shape):
+    g = (torch.randn(shape, generator=gen(sum(shape))) * 1e-3).to(dtype)
+    want = newton_schulz(g)
+    got = _qr().orthogonalize(g.cuda())
+    assert got.dtype == dtype and got.shape == g.shape
+    got, want = got.cpu().to(FP64).reshape(-1, *shape[-2:]), want.reshape(-1, *shape[-2:])
+    for a, b in zip(got, want):
+        err, tol = float((a - b).norm()), orthogonal_bound(b, dtype, depth=max(shape[-2:]))
+        assert err <= tol, (err / float(b.norm()), tol / float(b.norm()))
