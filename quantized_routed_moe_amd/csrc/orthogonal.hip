@@ -44,13 +44,23 @@ __device__ __forceinline__ void unroll(F &&f) {
 }
 
 typedef __attribute__((address_space(3))) i16x4 *lds_i16x4;
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-// v as two fp16 numbers.  Each conversion rounds to nearest even: v is off by 2^-22 of itself, or 2^-25 where that is
-// more (the values are scaled to at most 2^15).
-__device__ __forceinline__ void split(float v, _Float16 &hi, _Float16 &lo) {
-    hi = (_Float16)v;
-    lo = (_Float16)(v - (float)hi);
+// Eight values as two fp16 numbers each, v = hi + lo, both rounded to nearest: v is off by 2^-22 of itself at most, or by
+// 2^-25 where that is more (the values are scaled to at most 2^15).  lo has to be taken from the hi that is stored: of
+// the two conversions that the compiler may use for it (v_cvt_f16_f32 and v_cvt_pk_f16_f32) one rounds some values the
+// other way, and a hi that is computed twice can come out a whole place apart.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void split8(const float (&v)[8], f16x8 &hi, f16x8 &lo) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t h = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[i], (_Float16)v[i + 1]});
+        asm("" : "+v"(h));  // this value and no other
+        const f16x2 p = __builtin_bit_cast(f16x2, h);
+        hi[i] = p.x;
+        hi[i + 1] = p.y;
+        lo[i] = (_Float16)(v[i] - (float)p.x);
+        lo[i + 1] = (_Float16)(v[i + 1] - (float)p.y);
+    }
 }
 
 struct GemmArgs {
@@ -349,13 +359,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
                     for (int e = 0; e < 8; ++e) v[e] *= scale;
                 }
                 f16x8 h, l;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    _Float16 x, y;
-                    split(v[e], x, y);
-                    h[e] = x;
-                    l[e] = y;
-                }
+                split8(v, h, l);
                 if (in) {
                     *reinterpret_cast<f16x8 *>(out + at) = h;
                     *reinterpret_cast<f16x8 *>(out + at + 64) = l;
@@ -480,14 +484,11 @@ __global__ __launch_bounds__(kThreads) void split_kernel(const void *g, int rows
         const int r = p >> 3, u = p & 7;
         const int row = m0 + r, col = n0 + 8 * u;
         if (row >= m || col >= (n + 31) / 32 * 32) continue;
-        f16x8 h, l;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            _Float16 a, d;
-            split(tile[r][8 * u + i], a, d);
-            h[i] = a;
-            l[i] = d;
-        }
+        for (int i = 0; i < 8; ++i) v[i] = tile[r][8 * u + i];
+        f16x8 h, l;
+        split8(v, h, l);
         uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
         *reinterpret_cast<f16x8 *>(o) = h;
         *reinterpret_cast<f16x8 *>(o + 64) = l;
