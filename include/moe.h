@@ -428,7 +428,8 @@ int moe_combine_grad(int32_t dtype, const void *dout, int32_t dout_dtype, int64_
  * the same on the transpose), to out of g's type; out may be g.  coefficients
  * is a host array [steps][3], read during the call; it is refused where a
  * singular value of at most 1 could pass 64.  Everything between the products
- * has 22 bits, products are summed in fp32.  A matrix of zeros gives zeros,
+ * has 22 bits (down to 2^-37, below which only a matrix far smaller than eps
+ * has its values), products are summed in fp32.  A matrix of zeros gives zeros,
  * one with a NaN or an infinity NaN throughout.  rows and cols: at most
  * 65536, the smaller at most 16384; steps at most 32.  The workspace holds as
  * many matrices as fit 4 GiB at a time. */

@@ -22,6 +22,7 @@
 // tile below is stored a second time, transposed on the way by LDS reads.
 // The norm is taken out as a power of two when X is made, which is exact; what
 // is left of it, a factor in (1, 2], goes into the first step's products.
+#include <algorithm>
 #include <type_traits>
 
 #include "mxfp4.hpp"
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kCus = 256, kXcds = 8;
 constexpr int kChunk = 128;  // bytes of 32 split elements
-enum : int { kGram = 0, kPoly = 1, kApply = 2 };
+enum : int { kSym = 0, kPoly = 1, kApply = 2 };  // x y^T, symmetric; P of A = x = y; x y
 
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void unroll(F &&f) {
@@ -44,6 +45,7 @@ __device__ __forceinline__ void unroll(F &&f) {
 }
 
 typedef __attribute__((address_space(3))) i16x4 *lds_i16x4;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Eight values as two fp16 numbers each, v = hi + lo, both rounded to nearest: v is off by 2^-22 of itself at most, or by
 // 2^-25 where that is more (the values are scaled to at most 2^15).  lo has to be taken from the hi that is stored: of
@@ -72,9 +74,13 @@ struct GemmArgs {
     int32_t y_rows;                 // kApply: contraction rows that y has
     int32_t steps;                  // chunks of the contraction
     int32_t batch, m_tiles, n_tiles;
-    float scale;                    // of the sum: kGram, kApply
+    int32_t rounds, tail, parts;    // whole tiles of each workgroup; tiles behind them, the parts each is cut into
+    float scale;                    // of the sum (not kPoly)
     float c0, c1, c2;               // kPoly: identity, A, A A
     const float *rest;              // what is left of each matrix's norm, or null
+    int32_t rest_power;             // how often it goes into the sum
+    float *partial;                 // [tail][parts] tiles of sums
+    int32_t *arrived;               // [tail], zeros between launches
 };
 
 // Place in the list of tiles of turn b: runs of `run` consecutive tiles go to one XCD.
@@ -83,12 +89,13 @@ __device__ __forceinline__ int xcd_tile(int b, int run) {
     return (i / run * kXcds + b % kXcds) * run + i % run;
 }
 
+// A tile, or part `part` of one of the tail: matrix, tile row and column, its steps k .. k + n - 1.
 struct Tile {
-    int b, m, n;  // matrix, tile row, tile column
+    int b, m, n, k, steps, part, slot;  // slot: of the tail, or -1
 };
 
 // XL, YL: whether the operand has a lo part.
-template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU>
+template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU, int RING>  // RING: stages of the LDS ring
 __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split_gemm_kernel(GemmArgs a) {
     constexpr bool YCOL = MODE == kApply, TRI = !YCOL;
     constexpr int NW = WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
@@ -96,21 +103,31 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
     constexpr int XC = BM / 8 / NW, YC = BN / 8 / NW;  // 1 KB copies of each wave and step
     constexpr int OUT_ROW = BN * 4;
     static_assert(!TRI || BM == BN, "tiles of a symmetric product are square");
-    __shared__ __align__(1024) uint8_t smem[2 * STAGE + 32 * OUT_ROW];
-    uint8_t *const sout = smem + 2 * STAGE;
+    __shared__ __align__(1024) uint8_t smem[RING * STAGE + 32 * OUT_ROW];
+    uint8_t *const sout = smem + RING * STAGE;
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
-    // ---- the list of tiles: lower triangle row by row, or eight row tiles advancing through the columns together
+    // ---- the list of tiles: lower triangle row by row, or eight row tiles advancing through the columns together.
+    // First whole tiles, as many for every workgroup; what is left over is cut along the contraction into as many
+    // parts as there are workgroups for (each XCD takes the same part of neighbouring tiles).
+    constexpr int kSlots = kCus * PER_CU, kRun = kSlots / kXcds;
     const int each = TRI ? a.m_tiles * (a.m_tiles + 1) / 2 : a.m_tiles * a.n_tiles;
-    const int total = each * a.batch, run = kCus / kXcds * PER_CU;
     auto find = [&](int turn, Tile &t) -> bool {
-        const int at = xcd_tile(blockIdx.x + turn * gridDim.x, run);
-        if (at >= total) {
-            t = Tile{0, 0, 0};
-            return false;
+        int at;
+        t = Tile{0, 0, 0, 0, a.steps, 0, -1};
+        if (turn < a.rounds) {
+            at = xcd_tile(blockIdx.x + turn * kSlots, kRun);
+        } else {
+            const int p = (blockIdx.x % kXcds) * kRun + blockIdx.x / kXcds;
+            if (turn > a.rounds || p >= a.tail * a.parts) return false;
+            at = a.rounds * kSlots + p % a.tail;
+            t.part = p / a.tail;
+            t.slot = a.parts > 1 ? p % a.tail : -1;
+            t.k = t.part * a.steps / a.parts;
+            t.steps = (t.part + 1) * a.steps / a.parts - t.k;
         }
         t.b = at / each;
         const int r = at - t.b * each;
@@ -142,15 +159,16 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
     auto next_tile = [&] {
         Tile t;
         const bool more = find(++cturn, t);
-        cleft = more ? a.steps : 0x7fffffff;  // past the end: copies of nothing
-        crows = a.y_rows;
-        cx = a.x + t.b * a.x_mat + (int64_t)t.m * BM * a.x_ld;
+        cleft = more ? t.steps : 0x7fffffff;  // past the end: copies of nothing
+        crows = a.y_rows - 32 * t.k;
+        cx = a.x + t.b * a.x_mat + (int64_t)t.m * BM * a.x_ld + (int64_t)t.k * kChunk;
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
             const int r = x_row(i);
             xoff[i] = more && t.m * BM + r < a.rows ? (uint32_t)(r * a.x_ld + 16 * ((lane & 7) ^ ((r >> 1) & 7))) : kOob;
         }
-        cy = a.y + t.b * a.y_mat + (YCOL ? (int64_t)t.n * BN * 4 : (int64_t)t.n * BN * a.y_ld);
+        cy = a.y + t.b * a.y_mat + (YCOL ? (int64_t)t.n * BN * 4 + (int64_t)t.k * 32 * a.y_ld
+                                         : (int64_t)t.n * BN * a.y_ld + (int64_t)t.k * kChunk);
 #pragma unroll
         for (int i = 0; i < YC; ++i) {
             const int r = y_row(i);
@@ -208,7 +226,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
     const int wrow = wm * MI * 32, wcol = wn * NI * 32;
     int stg = 0;
     f32x16 acc[MI][NI];
-    auto product = [&] {
+    auto product = [&](int steps) {
         i32x4 xh[MI], xl[XL ? MI : 1], yh[2][NI], yl[YL ? NI : 1];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -243,7 +261,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
 #pragma unroll
         for (int i = 0; i < MI; ++i) read_x(xh[i], stg, i, 0, 0);
 #pragma unroll 1
-        for (int k = 0; k < a.steps; ++k) {
+        for (int k = 0; k < steps; ++k) {
             // half 0
             group([&](auto i, auto j) { mul(yh[0][j], xh[i], acc[i][j]); },
                   std::integral_constant<int, (YL ? NI : 0) + (XL ? MI : 0)>{},
@@ -271,7 +289,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
             }
             // half 1; the last group runs on the other side of the barrier
             auto hand_over = [&] {
-                wait_vm<0>();
+                wait_vm<(RING - 2) * kCopies>();
                 lds_barrier();
             };
             auto ahead = [&](auto r) {  // the next step's first operands
@@ -294,7 +312,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
                     group([&](auto i, auto j) { mul(yl[j], xh[i], acc[i][j]); }, none, nothing, none, Copy{});
                 hand_over();
                 const Copy c = begin_copy(stg);
-                stg ^= 1;
+                stg = stg + 1 == RING ? 0 : stg + 1;
                 group([&](auto i, auto j) { mul(yh[1][j], xl[i], acc[i][j]); }, all, ahead, copies, c);
             } else {
                 // only hi hi: the operands are in registers, but xh is read for the next step while it is used
@@ -303,7 +321,7 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
                 for (int i = 0; i < MI; ++i) now[i] = xh[i];
                 hand_over();
                 const Copy c = begin_copy(stg);
-                stg ^= 1;
+                stg = stg + 1 == RING ? 0 : stg + 1;
                 group([&](auto i, auto j) { mul(yh[1][j], now[i], acc[i][j]); }, all, ahead, copies, c);
             }
             end_copy();
@@ -315,8 +333,8 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
     // eight hi and eight lo elements of the same place, from which the transposed copy is read.
     auto slot_of = [&](int r, int c) { return sout + r * OUT_ROW + ((c ^ (r & (OUT_ROW / 16 - 1))) << 4); };
     auto finish = [&](const Tile &t) {
-        const float rest = a.rest ? a.rest[t.b] : 1.0f;
-        const float scale = a.scale * (MODE == kGram ? rest * rest : rest);
+        const float rest = a.rest_power ? a.rest[t.b] : 1.0f;
+        const float scale = a.scale * (a.rest_power == 2 ? rest * rest : a.rest_power == 1 ? rest : 1.0f);
         uint8_t *out = a.out + t.b * a.out_mat;
         const uint8_t *add = a.add + t.b * a.out_mat;
         const int m0 = t.m * BM, n0 = t.n * BN;
@@ -395,20 +413,71 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
         });
     };
 
+    // ---- the parts of a tile of the tail: every part's sums go to memory, and the workgroup that comes last adds them
+    // up, in the order of the parts whichever it is.  Nobody waits.  True for the last.  The sums are stored and loaded
+    // past the XCD's own L2 (scope bit sc1), so that they need no fence, which would write back all of it: with fences
+    // a product of 13 x 519 x 519 took 151 us.
+    auto joined = [&](const Tile &t) -> bool {
+        constexpr int kQuads = MI * NI * 4, kTile = BM * BN * 4, kAgent = 16;
+        const auto sums = buf_rsrc((const uint8_t *)a.partial + (int64_t)t.slot * a.parts * kTile, a.parts * kTile);
+        auto at = [&](int part, int quad) { return part * kTile + (quad * NW * 64 + tid) * 16; };
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), sums,
+                                                           at(t.part, (i * NI + j) * 4 + q), 0, kAgent);
+                }
+        wait_vm<0>();  // this wave's sums are there
+        lds_barrier();
+        int *said = reinterpret_cast<int *>(sout);
+        if (tid == 0) *said = atomicAdd(a.arrived + t.slot, 1);
+        lds_barrier();
+        const bool last = *said == a.parts - 1;
+        lds_barrier();
+        if (!last) return false;
+        if (tid == 0) a.arrived[t.slot] = 0;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
+        constexpr int kAhead = 8;  // loads in flight
+#pragma unroll 1
+        for (int p = 0; p < a.parts; ++p)
+            unroll<kQuads / kAhead>([&](auto g_c) {
+                constexpr int g = decltype(g_c)::value * kAhead;
+                u32x4 v[kAhead];
+#pragma unroll
+                for (int n = 0; n < kAhead; ++n) v[n] = __builtin_amdgcn_raw_buffer_load_b128(sums, at(p, g + n), 0, kAgent);
+                __builtin_amdgcn_sched_barrier(0);
+                unroll<kAhead>([&](auto n_c) {
+                    constexpr int n = decltype(n_c)::value, quad = g + n, i = quad / 4 / NI, j = quad / 4 % NI, q = quad % 4;
+                    const f32x4 f = __builtin_bit_cast(f32x4, v[n]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[i][j][4 * q + u] += f[u];
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        return true;
+    };
+
     next_tile();
     auto copy_step = [&](int s) {
         const Copy c = begin_copy(s);
         unroll<kCopies>([&](auto i) { send(c, i); });
         end_copy();
     };
-    copy_step(0);
-    wait_vm<0>();
-    copy_step(1);
+#pragma unroll
+    for (int i = 0; i < RING; ++i) copy_step(i);
+    wait_vm<(RING - 1) * kCopies>();
     lds_barrier();
     Tile t;
     for (int turn = 0; find(turn, t); ++turn) {
-        product();
-        finish(t);
+        product(t.steps);
+        if (t.slot < 0 || joined(t)) finish(t);
     }
     wait_vm<0>();
 }
@@ -423,9 +492,12 @@ __device__ __forceinline__ float element(const void *p, int64_t at) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void norm_kernel(const void *g, int64_t n, int parts, double *sums) {
+__global__ __launch_bounds__(kThreads) void norm_kernel(const void *g, int64_t n, int parts, double *sums,
+                                                        int32_t *arrived) {
     __shared__ double part[kThreads / 64];
     const int tid = threadIdx.x;
+    if (blockIdx.x == 0)
+        for (int i = tid; i < 2 * kCus; i += kThreads) arrived[i] = 0;
     const int64_t b = blockIdx.x / parts, p = blockIdx.x % parts;
     const int64_t per = ((n + parts - 1) / parts + 7) / 8 * 8, lo = p * per, hi = min(n, lo + per);
     const int64_t base = b * n;
@@ -532,25 +604,75 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const uint8_t *x, int64_
 
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU>
-hipError_t launch_tiles(GemmArgs a, int out_cols, hipStream_t s) {
-    a.m_tiles = ceil_div(a.rows, BM);
-    a.n_tiles = ceil_div(out_cols, BN);
-    klaunch(split_gemm_kernel<MODE, XL, YL, BM, BN, WM, WN, PER_CU>, dim3(kCus * PER_CU), dim3(WM * WN * 64), s, a);
-    return hipGetLastError();
+// The tiles of a product: squares of `side`, which of them are whole and how the rest are cut.
+struct Cut {
+    int side, m_tiles, n_tiles, rounds, tail, parts;
+    int64_t bytes() const { return parts > 1 ? (int64_t)tail * parts * side * side * 4 : 0; }
+};
+constexpr int kLeastSteps = 4;  // of a part
+Cut cut_of(int mode, int64_t batch, int rows, int cols, int steps) {
+    auto of = [&](int side, int slots) {
+        Cut c;
+        c.side = side;
+        c.m_tiles = ceil_div(rows, side);
+        c.n_tiles = ceil_div(cols, side);
+        const int64_t tiles = batch * (mode == kApply ? (int64_t)c.m_tiles * c.n_tiles
+                                                      : (int64_t)c.m_tiles * (c.m_tiles + 1) / 2);
+        c.rounds = (int)(tiles / slots);
+        c.tail = (int)(tiles - (int64_t)c.rounds * slots);
+        c.parts = c.tail > 0 ? std::max(1, std::min(slots / c.tail, steps / kLeastSteps)) : 1;
+        return c;
+    };
+    const Cut big = of(256, kCus), small = of(128, kCus);
+    const int64_t area_big = (big.rounds * kCus + big.tail) * (int64_t)65536,
+                  area_small = (small.rounds * kCus + small.tail) * (int64_t)16384;
+    return area_big <= area_small + area_small / 10 ? big : small;
 }
 
 template <int MODE, bool XL, bool YL>
-hipError_t launch_product(const GemmArgs &a, hipStream_t s) {
-    const int64_t m = ceil_div(a.rows, 256), n = ceil_div(a.cols, 256);
-    const int64_t tiles = a.batch * (MODE == kApply ? m * n : m * (m + 1) / 2);
-    if (tiles >= kCus) return launch_tiles<MODE, XL, YL, 256, 256, 2, 4, 1>(a, a.cols, s);
-    return launch_tiles<MODE, XL, YL, 128, 128, 2, 2, 2>(a, a.cols, s);
+hipError_t launch_product(GemmArgs a, hipStream_t s) {
+    const Cut c = cut_of(MODE, a.batch, a.rows, a.cols, a.steps);
+    a.m_tiles = c.m_tiles;
+    a.n_tiles = c.n_tiles;
+    a.rounds = c.rounds;
+    a.tail = c.tail;
+    a.parts = c.parts;
+    if (c.side == 256) klaunch(split_gemm_kernel<MODE, XL, YL, 256, 256, 2, 4, 1, 2>, dim3(kCus), dim3(512), s, a);
+    else klaunch(split_gemm_kernel<MODE, XL, YL, 128, 128, 2, 2, 1, 4>, dim3(kCus), dim3(256), s, a);
+    return hipGetLastError();
 }
+
+// The buffers of a pass in the workspace.
+struct Layout {
+    uint8_t *x[2], *m[5];  // X and the X it becomes; A, P, Q and two more of their kind
+    float *partial;
+    double *sums;
+    float *rest;
+    int32_t *arrived;
+    int64_t bytes;
+    Layout(uint8_t *at, const OrthogonalSizes &z, int64_t batch) {
+        const uint8_t *begin = at;
+        auto take = [&](int64_t n) {
+            uint8_t *p = at;
+            at += (n + 255) / 256 * 256;
+            return p;
+        };
+        for (auto &p : x) p = take(batch * z.x_mat);
+        for (auto &p : m) p = take(z.gram ? batch * z.a_mat : &p < m + 2 ? batch * z.a_mat : 0);
+        const int mp = ceil_div(z.m, 32), np = ceil_div(z.n, 32);
+        const int64_t most = std::max({cut_of(kSym, batch, z.m, mp * 32, np).bytes(),
+                                       cut_of(kSym, batch, z.m, mp * 32, mp).bytes(),
+                                       cut_of(kApply, batch, z.m, np * 32, mp).bytes()});
+        partial = (float *)take(most);
+        sums = (double *)take(8 * batch * z.parts);
+        rest = (float *)take(4 * batch);
+        arrived = (int32_t *)take(4 * 2 * kCus);
+        bytes = at - begin;
+    }
+};
 
 }  // namespace
 
-// Buffers of the matrices of one pass, `each` bytes apart where they belong to one matrix.
 OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols) {
     OrthogonalSizes z;
     z.m = (int32_t)(rows < cols ? rows : cols);
@@ -559,78 +681,117 @@ OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols) {
     z.a_ld = (int64_t)ceil_div(z.m, 32) * kChunk;
     z.x_mat = z.m * z.x_ld;
     z.a_mat = z.m * z.a_ld;
+    z.gram = 4 * (int64_t)z.n >= 5 * (int64_t)z.m;
     const int64_t want = rows * cols / 32768;  // elements a workgroup sums
     z.parts = (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want);
     return z;
 }
+int64_t orthogonal_bytes(const OrthogonalSizes &z, int64_t batch) { return Layout(nullptr, z, batch).bytes; }
 
 hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
     const OrthogonalSizes z = orthogonal_sizes(o.rows, o.cols);
     const bool tall = o.rows > o.cols;
-    uint8_t *x[2] = {o.work, o.work + o.batch * z.x_mat}, *A = x[1] + o.batch * z.x_mat, *P = A + o.batch * z.a_mat;
-    double *sums = (double *)(P + o.batch * z.a_mat);
-    float *rest = (float *)(sums + o.batch * z.parts);
+    const Layout w(o.work, z, o.batch);
     const dim3 block(kThreads), blocks64(ceil_div(z.n, 64), ceil_div(z.m, 64), o.batch);
     auto in = [&](auto d) {
         constexpr int DT = decltype(d)::value;
-        klaunch(norm_kernel<DT>, dim3(o.batch * z.parts), block, s, o.g, (int64_t)o.rows * o.cols, (int)z.parts, sums);
+        klaunch(norm_kernel<DT>, dim3(o.batch * z.parts), block, s, o.g, (int64_t)o.rows * o.cols, (int)z.parts, w.sums,
+                w.arrived);
         klaunch(split_kernel<DT>, blocks64, block, s, o.g, (int)o.rows, (int)o.cols, tall, (int)z.parts,
-                (const double *)sums, o.eps, (int)o.step[0].x, x[0], z.x_ld, z.x_mat, rest);
+                (const double *)w.sums, o.eps, (int)o.step[0].x, w.x[0], z.x_ld, z.x_mat, w.rest);
         return hipGetLastError();
     };
     hipError_t err = dt == kDtF32 ? in(std::integral_constant<int, kDtF32>{})
                                   : dt == kDtBf16 ? in(std::integral_constant<int, kDtBf16>{})
                                                   : in(std::integral_constant<int, kDtF16>{});
-    for (int k = 0; k < o.steps && err == hipSuccess; ++k) {
-        const OrthogonalStep &t = o.step[k];
-        const uint8_t *now = x[k & 1];
+    // A split matrix and the power of two it is scaled by; of X also whether the norm's rest is still missing and
+    // whether it has a lo part (16-bit input has none: it is as it was but for a power of two).
+    struct Held {
+        uint8_t *p;
+        int scale;
+    };
+    bool fresh = true;
+    auto args = [&](Held x, Held y, Held out) {
         GemmArgs a{};
         a.batch = o.batch;
-        a.rest = k == 0 ? rest : nullptr;
-        // 16-bit input has no lo part: it is as it was but for a power of two
-        const bool lo = k > 0 || dt == kDtF32;
-        // A
-        a.x = a.y = now;
-        a.x_ld = a.y_ld = z.x_ld;
-        a.x_mat = a.y_mat = z.x_mat;
-        a.out = A;
-        a.out_ld = z.a_ld;
-        a.out_mat = z.a_mat;
+        a.x = x.p;
+        a.y = y.p;
+        a.out = out.p;
+        a.x_ld = a.y_ld = a.out_ld = z.a_ld;
+        a.x_mat = a.y_mat = a.out_mat = z.a_mat;
         a.rows = z.m;
         a.cols = ceil_div(z.m, 32) * 32;
-        a.steps = ceil_div(z.n, 32);
-        a.scale = ldexpf(1.0f, t.a - 2 * t.x);
-        err = lo ? launch_product<kGram, true, true>(a, s) : launch_product<kGram, false, false>(a, s);
-        if (err != hipSuccess) break;
-        // P
-        a.x = a.y = a.add = A;
-        a.x_ld = a.y_ld = z.a_ld;
-        a.x_mat = a.y_mat = z.a_mat;
-        a.out = P;
         a.steps = ceil_div(z.m, 32);
-        a.rest = nullptr;
-        a.c0 = ldexpf(t.c0, t.p);
-        a.c1 = ldexpf(t.c1, t.p - t.a);
-        a.c2 = ldexpf(t.c2, t.p - 2 * t.a);
-        err = launch_product<kPoly, true, true>(a, s);
-        if (err != hipSuccess) break;
-        // X
-        a.x = P;
-        a.y = now;
-        a.y_ld = z.x_ld;
-        a.y_mat = z.x_mat;
-        a.out = x[(k + 1) & 1];
-        a.out_ld = z.x_ld;
-        a.out_mat = z.x_mat;
+        a.scale = ldexpf(1.0f, out.scale - x.scale - y.scale);
+        a.partial = w.partial;
+        a.arrived = w.arrived;
+        a.rest = w.rest;
+        return a;
+    };
+    auto run = [&](hipError_t e) { err = err == hipSuccess ? e : err; };
+    auto sym = [&](Held x, Held y, Held out) {  // out = x y of symmetric matrices that commute
+        if (err == hipSuccess) run(launch_product<kSym, true, true>(args(x, y, out), s));
+    };
+    auto gram = [&](Held x, Held out) {  // out = x x^T
+        if (err != hipSuccess) return;
+        GemmArgs a = args(x, x, out);
+        a.x_ld = a.y_ld = z.x_ld;
+        a.x_mat = a.y_mat = z.x_mat;
+        a.steps = ceil_div(z.n, 32);
+        a.rest_power = fresh ? 2 : 0;
+        run(fresh && dt != kDtF32 ? launch_product<kSym, false, false>(a, s) : launch_product<kSym, true, true>(a, s));
+    };
+    auto poly = [&](const OrthogonalStep &t, Held A, Held out) {
+        if (err != hipSuccess) return;
+        GemmArgs a = args(A, A, out);
+        a.add = A.p;
+        a.c0 = ldexpf(t.c0, out.scale);
+        a.c1 = ldexpf(t.c1, out.scale - A.scale);
+        a.c2 = ldexpf(t.c2, out.scale - 2 * A.scale);
+        run(launch_product<kPoly, true, true>(a, s));
+    };
+    auto apply = [&](Held q, Held x, Held out) {  // out = q x
+        if (err != hipSuccess) return;
+        GemmArgs a = args(q, x, out);
+        a.y_ld = a.out_ld = z.x_ld;
+        a.y_mat = a.out_mat = z.x_mat;
         a.cols = ceil_div(z.n, 32) * 32;
         a.y_rows = z.m;
-        a.rest = k == 0 ? rest : nullptr;
-        a.scale = ldexpf(1.0f, o.step[k + 1].x - t.x - t.p);
-        err = lo ? launch_product<kApply, true, true>(a, s) : launch_product<kApply, true, false>(a, s);
+        a.rest_power = fresh ? 1 : 0;
+        run(fresh && dt != kDtF32 ? launch_product<kApply, true, false>(a, s) : launch_product<kApply, true, true>(a, s));
+        fresh = false;
+    };
+    int now = 0;  // which X
+    for (int k = 0; k < o.steps;) {
+        const int end = z.gram ? std::min(k + kOrthogonalRun, (int)o.steps) : k + 1;
+        const Held X{w.x[now], o.step[k].x}, next{w.x[now ^ 1], o.step[end].x};
+        uint8_t *A = w.m[0], *P = w.m[1], *Q = nullptr, *spare[3] = {w.m[2], w.m[3], w.m[4]};
+        int q_scale = 0;
+        gram(X, {A, o.step[k].a});
+        for (int i = k; i < end; ++i) {
+            const OrthogonalStep &t = o.step[i];
+            poly(t, {A, t.a}, {P, t.p});
+            if (i + 1 < end) {  // A <- P A P
+                sym({P, t.p}, {A, t.a}, {spare[0], t.pa});
+                sym({spare[0], t.pa}, {P, t.p}, {A, o.step[i + 1].a});
+            }
+            if (!Q) {  // the first P is what there is of Q
+                Q = P;
+                q_scale = t.p;
+                P = spare[1];
+            } else {
+                sym({P, t.p}, {Q, q_scale}, {spare[2], t.q});
+                std::swap(Q, spare[2]);
+                q_scale = t.q;
+            }
+        }
+        apply({Q, q_scale}, X, next);
+        now ^= 1;
+        k = end;
     }
     if (err != hipSuccess) return err;
     auto k = dt == kDtF32 ? join_kernel<kDtF32> : dt == kDtBf16 ? join_kernel<kDtBf16> : join_kernel<kDtF16>;
-    klaunch(k, blocks64, block, s, (const uint8_t *)x[o.steps & 1], z.x_ld, z.x_mat, (int)o.step[o.steps].x, (int)o.rows,
+    klaunch(k, blocks64, block, s, (const uint8_t *)w.x[now], z.x_ld, z.x_mat, (int)o.step[o.steps].x, (int)o.rows,
             (int)o.cols, tall, o.out);
     return hipGetLastError();
 }

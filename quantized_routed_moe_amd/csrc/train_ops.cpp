@@ -109,7 +109,8 @@ int check_cols(int64_t cols) {
 // tiles for 256 CUs at any size), one at least.
 constexpr int64_t kOrthogonalBytes = (int64_t)4 << 30;
 int64_t orthogonal_pass(const OrthogonalSizes &z, int64_t batch) {
-    return std::max<int64_t>(1, std::min({batch, kOrthogonalBytes / z.bytes(), (int64_t)65535}));
+    const int64_t each = 2 * z.x_mat + (z.gram ? 5 : 2) * z.a_mat;
+    return std::max<int64_t>(1, std::min({batch, kOrthogonalBytes / each, (int64_t)65535}));
 }
 
 // The largest |c0 s + c1 s^3 + c2 s^5| (odd) or |c0 + c1 l + c2 l^2| over s in [0, u], l = s^2: at the ends or where
@@ -137,18 +138,21 @@ double largest(const float *c, double u, bool odd) {
 // The power of two that takes values of at most `most` to 2^14 .. 2^15, half of what fp16 holds.
 int32_t scale_of(double most) { return most > 0 ? std::min(15, (int)std::floor(std::log2(32768.0 / most))) : 15; }
 
-// Scales of every step from the largest singular values that can come up; past 64 the steps do not converge.
+// Scales of every step from the largest singular values that can come up; past 64 the steps do not converge.  A P A is
+// A of the step after, and P A has singular values of at most the two steps' X multiplied.
 int plan_orthogonal(const float *c, int32_t steps, OrthogonalArgs &o) {
-    double u = 1;
+    double u = 1, q = 1;
     for (int32_t k = 0; k < steps; ++k) {
         OrthogonalStep &t = o.step[k];
-        const float *q = c + 3 * k;
-        if (!std::isfinite(q[0]) || !std::isfinite(q[1]) || !std::isfinite(q[2])) return MOE_ERR_INVALID_ARG;
-        t = OrthogonalStep{q[0], q[1], q[2], scale_of(u), scale_of(u * u), scale_of(largest(q, u, false))};
-        u = largest(q, u, true) * 1.001;  // fp32's rounding is far below that
+        const float *f = c + 3 * k;
+        if (!std::isfinite(f[0]) || !std::isfinite(f[1]) || !std::isfinite(f[2])) return MOE_ERR_INVALID_ARG;
+        const double p = largest(f, u, false), next = largest(f, u, true) * 1.001;  // fp32's rounding is far below that
+        q = k % kOrthogonalRun == 0 ? p : q * p;
+        t = OrthogonalStep{f[0], f[1], f[2], scale_of(u), scale_of(u * u), scale_of(p), scale_of(u * next), scale_of(q)};
+        u = next;
         if (!(u <= 64)) return MOE_ERR_INVALID_ARG;
     }
-    o.step[steps] = OrthogonalStep{0, 0, 0, scale_of(u), 0, 0};
+    o.step[steps] = OrthogonalStep{0, 0, 0, scale_of(u), 0, 0, 0, 0};
     return MOE_OK;
 }
 
@@ -160,7 +164,9 @@ size_t moe_orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols) {
     if (batch < 1 || rows < 1 || cols < 1 || std::max(rows, cols) > kMaxFeatures || std::min(rows, cols) > kMaxOrthogonal)
         return 0;
     const OrthogonalSizes z = orthogonal_sizes(rows, cols);
-    return (size_t)(orthogonal_pass(z, batch) * z.bytes());
+    // a last, smaller pass may cut its tiles into more parts
+    const int64_t pass = orthogonal_pass(z, batch), left = batch % pass;
+    return (size_t)std::max(orthogonal_bytes(z, pass), left ? orthogonal_bytes(z, left) : 0);
 }
 
 int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows, int64_t cols, int32_t steps,

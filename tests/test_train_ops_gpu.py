@@ -598,8 +598,11 @@ def orthogonal_bound(want, dtype, steps=5, growth=3.4445, depth=1):
     on what they get multiplied by at most `growth` and add three such errors of a matrix of |X| <= |want|:
     the last step's weigh 1, those of the one before `growth` of what X was then, which was that much smaller where
     it grew (singular values that have stopped growing are multiplied by at most 1.6, the derivative of the quintic
-    on [0.7, 1.2]).  So 3 * steps * 1.6^4 * (2^-22 + sqrt(depth) 2^-24), and the output's rounding."""
-    return (3 * steps * 1.6**4 * (2.0**-22 + depth**0.5 * 2.0**-24) + UNIT[dtype]) * float(want.norm()) + 1e-30
+    on [0.7, 1.2]).  So 3 * steps * 1.6^4 * (2^-22 + sqrt(depth) 2^-24), and the output's rounding.  Of a matrix so
+    small beside eps that its numbers fall below the scale's end, 2^-39 for each of X's elements and steps is left, times
+    the growth of the steps after it: nothing but for results that are as small themselves."""
+    floor = 2.0**-39 * steps * growth**steps * want.numel() ** 0.5
+    return (3 * steps * 1.6**4 * (2.0**-22 + depth**0.5 * 2.0**-24) + UNIT[dtype]) * float(want.norm()) + floor
 
 
 @pytest.mark.parametrize("dtype", ALL)
@@ -614,3 +617,123 @@ def test_orthogonalize(dtype, shape):
     for a, b in zip(got, want):
         err, tol = float((a - b).norm()), orthogonal_bound(b, dtype, depth=max(shape[-2:]))
         assert err <= tol, (err / float(b.norm()), tol / float(b.norm()))
+
+
+def test_orthogonalize_one_product():
+    """X' = c0 X keeps X: each of the three roundings to 22 bits (of X, of the identity, of the product) is within 2^-22,
+    and 2^-39 where the scale ends."""
+    for shape in ((300, 300), (1000, 519), (64, 2000)):
+        g = torch.randn(shape, generator=gen(1))
+        got = _qr().orthogonalize(g.cuda(), steps=1, coefficients=(1.0, 0.0, 0.0)).cpu().to(FP64)
+        want = g.to(FP64) / (g.to(FP64).norm() + 1e-7)
+        assert bool(((got - want).abs() <= 3.1 * 2.0**-22 * want.abs() + 2.0**-37).all())
+
+
+@pytest.mark.parametrize("rows,cols", [(200, 200), (519, 1000), (96, 3000), (700, 900)])
+@pytest.mark.parametrize("coefficients", [(0.0, 1.0, 0.0), (1.5, -0.5, 0.0)])
+def test_orthogonalize_two_products(rows, cols, coefficients):
+    """Products of positive terms, where errors cannot hide behind a sum that cancels: a first step's A, P and X are off
+    by 2^-22 for each of the two roundings of every operand (six), and by the fp32 sum's additions, of which no term
+    meets more than one for each 16 elements of three products, twice: 2^-24 each at most."""
+    g = torch.rand(rows, cols, generator=gen(2)) + 0.1
+    want = newton_schulz(g, 1, coefficients)
+    got = _qr().orthogonalize(g.cuda(), steps=1, coefficients=coefficients).cpu().to(FP64)
+    x = g.to(FP64) / g.to(FP64).norm()
+    a, b, _ = (abs(c) for c in coefficients)
+    m = x if rows <= cols else x.t()
+    mag = a * m + b * (m @ m.t()) @ m
+    n = 3 * (rows + cols) / 16
+    tol = (6 * 2.0**-22 + n * 2.0**-24) * (mag if rows <= cols else mag.t())
+    assert bool(((got - want).abs() <= tol + 2.0**-37).all())
+
+
+def test_orthogonalize_batches_and_steps():
+    """Every way of cutting tiles: whole rounds and a tail, parts of one matrix; each number of steps."""
+    qr = _qr()
+    g = torch.randn(7, 600, 900, generator=gen(3)).to(BF16)
+    one = [qr.orthogonalize(m.cuda()).cpu() for m in g]
+    want = newton_schulz(g)
+    got = qr.orthogonalize(g.cuda()).cpu()
+    for a, b, w in zip(got, one, want):
+        tol = orthogonal_bound(w, BF16, depth=900)
+        assert float((a.to(FP64) - w).norm()) <= tol and float((b.to(FP64) - w).norm()) <= tol
+    for steps in range(1, 9):
+        x = torch.randn(2, 70, 150, generator=gen(steps))
+        y = qr.orthogonalize(x.cuda(), steps=steps).cpu().to(FP64)
+        for a, w in zip(y, newton_schulz(x, steps)):
+            assert float((a - w).norm()) <= orthogonal_bound(w, FP32, steps, depth=150)
+    each = [(3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)]
+    x = torch.randn(90, 260, generator=gen(4))
+    y = qr.orthogonalize(x.cuda(), steps=3, coefficients=each).cpu().to(FP64)
+    w = newton_schulz(x, 3, each)
+    assert float((y - w).norm()) <= orthogonal_bound(w, FP32, 3, depth=260)
+    many = torch.randn(300, 20, 33, generator=gen(5)).to(FP16)
+    y, w = qr.orthogonalize(many.cuda()).cpu().to(FP64), newton_schulz(many)
+    assert all(float((a - b).norm()) <= orthogonal_bound(b, FP16, depth=33) for a, b in zip(y, w))
+
+
+def test_orthogonalize_large():
+    """Tiles of 256 x 256, several rounds of them, both orders, against 64 bits on the GPU."""
+    qr = _qr()
+    for shape in ((6, 2048, 1024), (9, 1024, 2048), (5, 1792, 1800)):
+        g = torch.randn(shape, generator=gen(6)).to(BF16).cuda()
+        got = qr.orthogonalize(g)
+        for a, b in zip(got, g):
+            w = newton_schulz(b)
+            assert float((a.to(FP64) - w).norm()) <= orthogonal_bound(w, BF16, depth=2048)
+        again = qr.orthogonalize(g)
+        assert torch.equal(got, again)
+
+
+def test_orthogonalize_special_matrices():
+    qr = _qr()
+    g = torch.randn(6, 40, 70, generator=gen(7))
+    g[0] = 0
+    g[1, 3, 4], g[2, 0, 0] = math.nan, math.inf
+    g[3] *= 1e30
+    g[4] *= 1e-30
+    got = qr.orthogonalize(g.cuda()).cpu()
+    assert (got[0] == 0).all() and got[1].isnan().all() and got[2].isnan().all()
+    want = newton_schulz(g[3:])
+    for a, w in zip(got[3:], want):
+        assert float((a.to(FP64) - w).norm()) <= orthogonal_bound(w, FP32, depth=70)
+    # no eps: a matrix of zeros still gives zeros, a tiny one its singular vectors
+    tiny = g[5:6] * 1e-38
+    got = qr.orthogonalize(torch.cat([g[:1], tiny]).cuda(), eps=0.0).cpu()
+    w = newton_schulz(tiny[0], eps=0.0)
+    assert (got[0] == 0).all() and float((got[1].to(FP64) - w).norm()) <= orthogonal_bound(w, FP32, depth=70)
+    # one direction only: the others stay nothing
+    u, v = torch.randn(50, 1, generator=gen(8)), torch.randn(1, 90, generator=gen(9))
+    got, w = qr.orthogonalize((u @ v).cuda()).cpu().to(FP64), newton_schulz(u @ v)
+    # fp32's own rounding of u v is the other directions' content, which grows 3.4445 a step in both alike; so does the
+    # 2^-22 that the first products add to it: 3.4445^4 of it at most
+    assert float((got - w).norm()) <= 141 * 2.0**-22 * 6 * float(w.norm())
+
+
+def test_orthogonalize_in_place_streams_and_graphs():
+    qr = _qr()
+    g = torch.randn(3, 100, 300, generator=gen(10)).cuda()
+    want = qr.orthogonalize(g)
+    out = torch.empty_like(g)
+    assert qr.orthogonalize(g, out=out) is out and torch.equal(out, want)
+    same = g.clone()
+    qr.orthogonalize(same, out=same)
+    assert torch.equal(same, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    x = qr.orthogonalize(g, stream=s)
+    s.synchronize()
+    assert torch.equal(x, want)
+    static = g.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        res = qr.orthogonalize(static)
+    for i in range(3):
+        static.copy_(torch.randn(3, 100, 300, generator=gen(20 + i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res, qr.orthogonalize(static)), i
+    odd = torch.randn(1 + 3 * 35 * 41, generator=gen(11)).to(BF16).cuda()[1:].view(3, 35, 41)  # aligned to an element only
+    assert torch.equal(qr.orthogonalize(odd), qr.orthogonalize(odd.clone()))
+    assert qr.orthogonalize(torch.empty(0, 4, 5).cuda()).shape == (0, 4, 5)
