@@ -14,7 +14,7 @@ constexpr int kMaxTopK = 8, kMaxGroups = 16;
 struct PairOrder {
     int64_t *perm, *place;
     int32_t *rows, *offsets;
-    int32_t *hist;         // [chunks][E + 1] pairs of each expert (the last: of none) in each chunk
+    int32_t *hist;         // [chunks + 1][E + 1] pairs of each expert (the last: of none) in each chunk; their sums
     int32_t chunk, chunks; // tokens of a chunk, number of chunks
 };
 

@@ -9,12 +9,14 @@
 // apart than it can be wrong, 64 bits where they are not.  Without a bias the
 // order of the scores is that of the logits, which needs no arithmetic at all.
 //
-// L lanes hold a token (4, 2 or 1 tokens a wave), PER keys each: expert
-// lane + L i in slot i.  A key is the order-preserving image of its fp32 value
-// with the low four bits replaced by the slot (lower slots larger), so that a
-// lane sorts them with plain integer minima and maxima and the largest head
-// of L lanes is found by a butterfly; of equal heads, which are of one slot,
-// the lowest lane has the lowest expert.
+// L lanes hold a token.  A key is a double: the fp32 key, which leaves 29 bits
+// of it free, and the expert's number in the lowest ten, so that minima and
+// maxima of 64-bit floats order keys and settle ties by themselves.  A lane
+// takes eight experts at a time, sorts them with a network and merges them
+// into its eight best so far; lanes then merge their lists with a butterfly
+// (the larger of one list's i-th and the other's (7 - i)-th are the eight best
+// of both) until all of them hold the token's.  The largest key that did not
+// make it is kept beside the list: it is the ninth.
 #include <cfloat>
 #include <type_traits>
 
@@ -24,18 +26,9 @@ namespace qrmoe {
 
 namespace {
 
-// f(integral_constant 0), ..., f(integral_constant N - 1)
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void unroll(F &&f) {
-    if constexpr (I < N) {
-        f(std::integral_constant<int, I>{});
-        unroll<N, I + 1>(f);
-    }
-}
+constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
+constexpr int kSortThreads = 1024;
 
-constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 template <int DT>
@@ -60,7 +53,8 @@ __device__ __forceinline__ float exp_neg(float x) {
     const float n = rintf(x * kHi), f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
     return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
-// sigmoid, within 2^-22
+// sigmoid, within 2^-22: its argument's rounding, at most .225 |l| 2^-23 / |l|, and a unit each of 2^-23 s (1 - s) for the
+// power, 2^-24 s for the sum and 2^-23 s for the reciprocal
 __device__ __forceinline__ float sigmoid_near(float l) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * l));
 }
@@ -78,42 +72,100 @@ template <class T>
 __device__ __forceinline__ T number(T key, T least) {
     return key != key ? least : key;
 }
-__device__ __forceinline__ uint32_t image_of(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+// Of packed keys, which are never NaN.  (The builtins first make sure that a NaN would be a quiet one.)
+__device__ __forceinline__ double larger(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
-__device__ __forceinline__ float value_of(uint32_t image) {
-    return __uint_as_float(image & 0x80000000u ? image ^ 0x80000000u : ~image);
+__device__ __forceinline__ double lesser(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
-constexpr uint32_t kThere = 0x00800000u;  // the image of -FLT_MAX; that of -inf is below
+// fp32 keys as doubles that carry the expert in their low ten bits: of equal ones the lower expert is the larger.
+// Infinities, which have no room for it, are +-kFar; an expert that is not there has -kFar.
+constexpr double kFar = 0x1p200;
+__device__ __forceinline__ double pack_key(float key, int e) {
+    const double d = lesser(larger((double)key, -kFar), kFar);
+    const uint64_t u = (uint64_t)__double_as_longlong(d);
+    const uint32_t hi = (uint32_t)(u >> 32), low = (uint32_t)u | ((uint32_t)e ^ (1023u & ~(uint32_t)((int)hi >> 31)));
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | low));
+}
+__device__ __forceinline__ int expert_of(double k) {
+    const uint64_t u = (uint64_t)__double_as_longlong(k);
+    return (int)(((uint32_t)u ^ ~(uint32_t)((int)(u >> 32) >> 31)) & 1023u);
+}
+__device__ __forceinline__ bool there(double k) { return k > -0x1p199; }
+__device__ __forceinline__ float value_of(double k) {  // the fp32 key
+    return (float)__longlong_as_double(__double_as_longlong(k) & ~1023ll);
+}
 
-// v sorted, the largest first (odd-even merge network)
-template <int N>
-__device__ __forceinline__ void sort_keys(uint32_t (&v)[N]) {
+constexpr int kList = 8;
+__device__ __forceinline__ void order2(double &a, double &b) {
+    const double x = larger(a, b);
+    b = lesser(a, b);
+    a = x;
+}
+// The largest first: odd-even merge sort
+__device__ __forceinline__ void sort_list(double (&v)[kList]) {
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
+    for (int p = 1; p < kList; p *= 2)
 #pragma unroll
         for (int q = p; q >= 1; q /= 2)
 #pragma unroll
-            for (int j = q % p; j + q < N; j += 2 * q)
+            for (int j = q % p; j + q < kList; j += 2 * q)
 #pragma unroll
                 for (int i = 0; i < q; ++i)
-                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const uint32_t a = v[i + j], b = v[i + j + q];
-                        v[i + j] = umax(a, b);
-                        v[i + j + q] = umin(a, b);
-                    }
+                    if (i + j + q < kList && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order2(v[i + j], v[i + j + q]);
+}
+// v: the eight best of the sorted lists v and o; ninth: the largest of what either has lost, where it is asked for.
+__device__ __forceinline__ void merge_list(double (&v)[kList], const double (&o)[kList], double &ninth, bool want) {
+    if (want) {
+#pragma unroll
+        for (int i = 0; i < kList; ++i) ninth = larger(ninth, lesser(v[i], o[kList - 1 - i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kList; ++i) v[i] = larger(v[i], o[kList - 1 - i]);
+#pragma unroll
+    for (int q = kList / 2; q >= 1; q /= 2)  // falls, then rises (or any rotation of that): sorted by halves
+#pragma unroll
+        for (int i = 0; i < kList; ++i)
+            if ((i & q) == 0) order2(v[i], v[i + q]);
+}
+template <int D>
+__device__ __forceinline__ double partner(double v) {  // of the butterfly at distance D; DPP only where that is enough
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    uint32_t a, b, c, d;
+    bfly_pair_u32<D>((uint32_t)u, a, b);
+    bfly_pair_u32<D>((uint32_t)(u >> 32), c, d);
+    const bool upper = (threadIdx.x & D) != 0;
+    const uint32_t lo = D <= 8 ? b : upper ? a : b, hi = D <= 8 ? d : upper ? c : d;
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+template <int L, int D = 1>
+__device__ __forceinline__ void merge_lanes(double (&v)[kList], double &ninth, bool want) {
+    if constexpr (D < L) {
+        double o[kList];
+#pragma unroll
+        for (int i = 0; i < kList; ++i) o[i] = partner<D>(v[i]);
+        const double other = want ? partner<D>(ninth) : 0.0;
+        merge_list(v, o, ninth, want);
+        if (want) ninth = larger(ninth, other);
+        merge_lanes<L, 2 * D>(v, ninth, want);
+    }
 }
 
 // ------------------------------------------------- one token in 64 bits
 // The whole wave decides for token t: lanes r < k get the expert of rank r
 // (-1: none left).  top, z: the row's largest logit and sum of e^(l - top).
 // A function of its own, so that the registers of what hardly ever runs stay out of what always does.
-template <int DT, int S>  // S slots of 64 experts
-__device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t t, float top, int lane) {
+template <int DT>
+__device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t t, float top, bool biased, int lane) {
+    const int S = (a.E + 63) / 64;  // slots of 64 experts
     const int64_t row = t * a.ld;
-    const bool soft = a.score == kSoftmax, by_logit = !a.bias && a.groups == 1;
-    double key[S];
+    const bool soft = a.score == kSoftmax, by_logit = !biased && a.groups == 1;
+    double key[16];  // in memory: registers would cost every other token
     double z = 0;
     if (soft && !by_logit) {
         for (int e = lane; e < a.E; e += 64) z += exp((double)load_logit<DT>(a.logits, row + e) - (double)top);
@@ -127,7 +179,7 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
         if (!score) return number(l, -DBL_MAX);
         return number((soft ? exp(l - (double)top) / z : sigmoid_f64(l)) + b, -DBL_MAX);
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
         key[i] = -INFINITY;
         if (64 * i < a.E && lane + 64 * i < a.E) key[i] = key_of(lane + 64 * i, !by_logit);
@@ -141,7 +193,7 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
                 t2 = fmax(t2, fmin(t1, x));
                 t1 = fmax(t1, x);
             };
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < S; ++i)
                 if (64 * i < a.E && (lane + 64 * i) / size == g) add(key[i]);
 #pragma unroll
@@ -159,28 +211,28 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
             before += o > mine || (o == mine && g < lane);
         }
         const uint64_t kept = __ballot(lane < a.groups && before < a.keep);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < S; ++i) {
             const int g = (lane + 64 * i) / size;
             if (64 * i < a.E && g < a.groups) {
                 if (!((kept >> g) & 1)) key[i] = -INFINITY;
                 // the scores of the chosen groups rank as their logits do
-                else if (!a.bias && key[i] != -INFINITY) key[i] = key_of(lane + 64 * i, false);
+                else if (!biased && key[i] != -INFINITY) key[i] = key_of(lane + 64 * i, false);
             }
         }
     }
     int id = -1;
     for (int r = 0; r < a.k; ++r) {
         double m = key[0];
-#pragma unroll
+#pragma unroll 1
         for (int i = 1; i < S; ++i) m = fmax(m, key[i]);
         m = group_reduce<64>(m, [](double x, double y) { return fmax(x, y); });
         if (m == -INFINITY) break;
         uint32_t at = 0xffffffffu;
-#pragma unroll
+#pragma unroll 1
         for (int i = S - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)(lane + 64 * i) : at;
         at = group_reduce<64>(at, umin);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < S; ++i)
             if ((uint32_t)(lane + 64 * i) == at) key[i] = -INFINITY;
         if (lane == r) id = (int)at;
@@ -189,35 +241,46 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
 }
 
 // -------------------------------------------------------------- pair order
-// Stable counting sort.  hist holds the pairs of each expert in each chunk of
-// tokens; a chunk's workgroup adds up the chunks before its own by itself,
-// which costs less than another launch.
+// Stable counting sort: the pairs of each expert in each chunk of tokens are
+// counted, the counts summed over the chunks before, the pairs placed.
+template <int THREADS>
 struct SortShared {
-    int fill[1025], before[1025], wcnt[kRouteWaves][1025];
-    int tmp[kRouteWaves];
+    int fill[1025], wcnt[THREADS / 64][1025];
+    int tmp[THREADS / 64];
 };
 
-// fill[b] for b <= E: how many pairs stand before those of bucket b, from total[b] (LDS; the buckets' pairs).
+// fill[b] for b <= E: how many pairs stand before those of bucket b, from total[b] (LDS; the buckets' pairs; may be fill).
+template <int THREADS>
 __device__ __forceinline__ void exclusive_scan(const int *total, int *fill, int E, int *tmp) {
+    constexpr int N = (1024 + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int v = tid < E ? total[tid] : 0;
-    const int inc = wave_incl_scan(v);
+    int v[N], sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = N * tid + i < E ? total[N * tid + i] : 0;
+        sum += v[i];
+    }
+    const int inc = wave_incl_scan(sum);
     if (lane == 63) tmp[wave] = inc;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < wave; ++w) base += tmp[w];
-    if (tid < E) fill[tid] = base + inc - v;
-    if (tid == kRouteThreads - 1) fill[E] = base + inc;
+    int at = inc - sum;
+    for (int w = 0; w < wave; ++w) at += tmp[w];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (N * tid + i < E) fill[N * tid + i] = at;
+        at += v[i];
+    }
+    if (tid == THREADS - 1) fill[E] = at;
     __syncthreads();
 }
 
 // Places pairs [p0, p1) in order; sh.fill[b] is the next free place of bucket b, sh.wcnt is zero.
-template <class Id>
+template <int THREADS, class Id>
 __device__ __forceinline__ void place_pairs(const Id *ids, int64_t p0, int64_t p1, int E, int k, const PairOrder &o,
-                                            SortShared &sh) {
+                                            SortShared<THREADS> &sh) {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
-    for (int64_t base = p0; base < p1; base += kRouteThreads) {
+    for (int64_t base = p0; base < p1; base += THREADS) {
         const int64_t p = base + tid;
         const bool valid = p < p1;
         int e = 2047;  // no bucket's
@@ -238,7 +301,7 @@ __device__ __forceinline__ void place_pairs(const Id *ids, int64_t p0, int64_t p
             int at = sh.fill[e] + rank;
             for (int w = 0; w < wave; ++w) at += sh.wcnt[w][e];
             o.perm[at] = p;
-            o.rows[at] = (int32_t)(p / k);
+            o.rows[at] = (int32_t)((uint32_t)p / (uint32_t)k);
             o.place[p] = at;
         }
         __syncthreads();
@@ -250,128 +313,188 @@ __device__ __forceinline__ void place_pairs(const Id *ids, int64_t p0, int64_t p
     }
 }
 
-template <class Id>
-__global__ __launch_bounds__(kRouteThreads) void place_kernel(const Id *ids, int64_t P, int E, int k, PairOrder o) {
-    __shared__ SortShared sh;
-    const int tid = threadIdx.x, c = blockIdx.x, buckets = E + 1;
-    for (int i = tid; i < kRouteWaves * 1025; i += kRouteThreads) (&sh.wcnt[0][0])[i] = 0;
-    for (int i = tid; i < buckets; i += kRouteThreads) sh.before[i] = sh.fill[i] = 0;
+// Turns the counts of the chunks into how many pairs of a bucket stand in the chunks before, and the row behind the last
+// chunk into their totals.  A workgroup takes 32 buckets, 32 threads for the rows of each.
+__global__ __launch_bounds__(kSortThreads) void scan_kernel(int E, PairOrder o) {
+    __shared__ int part[32][33];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, buckets = E + 1, b = blockIdx.x * 32 + c;
+    const int each = (o.chunks + 31) / 32, r0 = min(g * each, o.chunks), r1 = min(r0 + each, o.chunks);
+    int sum = 0;
+    if (b < buckets)
+        for (int r = r0; r < r1; ++r) sum += o.hist[(int64_t)r * buckets + b];
+    part[g][c] = sum;
     __syncthreads();
-    // rows of hist shared out over as many threads as there are for each bucket
-    const int width = buckets <= 128 ? 128 : buckets <= 256 ? 256 : buckets <= 512 ? 512 : 1024;
-    const int parts = kRouteThreads / width, part = tid / width;
-    for (int b = tid % width; b < buckets; b += width) {
-        int total = 0, before = 0;
-#pragma unroll 8
-        for (int i = part; i < o.chunks; i += parts) {
-            const int v = o.hist[(int64_t)i * buckets + b];
-            total += v;
-            before += i < c ? v : 0;
-        }
-        atomicAdd(&sh.fill[b], total);
-        atomicAdd(&sh.before[b], before);
+    int at = 0;
+    for (int i = 0; i < g; ++i) at += part[i][c];
+    if (b >= buckets) return;
+    if (g == 31) o.hist[(int64_t)o.chunks * buckets + b] = at + sum;
+    for (int r = r0; r < r1; ++r) {
+        const int v = o.hist[(int64_t)r * buckets + b];
+        o.hist[(int64_t)r * buckets + b] = at;
+        at += v;
     }
+}
+
+template <class Id>
+__global__ __launch_bounds__(kSortThreads) void place_kernel(const Id *ids, int64_t P, int E, int k, PairOrder o) {
+    __shared__ SortShared<kSortThreads> sh;
+    const int tid = threadIdx.x, c = blockIdx.x, buckets = E + 1;
+    for (int i = tid; i < kSortThreads / 64 * 1025; i += kSortThreads) (&sh.wcnt[0][0])[i] = 0;
+    for (int i = tid; i < buckets; i += kSortThreads) sh.fill[i] = o.hist[(int64_t)o.chunks * buckets + i];
     __syncthreads();
-    exclusive_scan(sh.fill, sh.fill, E, sh.tmp);
-    for (int i = tid; i < buckets; i += kRouteThreads) {
+    exclusive_scan<kSortThreads>(sh.fill, sh.fill, E, sh.tmp);
+    for (int i = tid; i < buckets; i += kSortThreads) {
         if (c == 0) o.offsets[i] = sh.fill[i];
-        sh.fill[i] += sh.before[i];
+        sh.fill[i] += o.hist[(int64_t)c * buckets + i];
     }
     __syncthreads();
     const int64_t p0 = (int64_t)c * o.chunk * k, p1 = min(P, p0 + (int64_t)o.chunk * k);
-    place_pairs(ids, p0, p1, E, k, o, sh);
+    place_pairs<kSortThreads>(ids, p0, p1, E, k, o, sh);
 }
 
 // The counts of one chunk; where it is the only one, the whole order.
 template <class Id>
-__global__ __launch_bounds__(kRouteThreads) void count_kernel(const Id *ids, int64_t P, int E, int k, PairOrder o) {
-    __shared__ SortShared sh;
+__global__ __launch_bounds__(kSortThreads) void count_kernel(const Id *ids, int64_t P, int E, int k, PairOrder o) {
+    __shared__ SortShared<kSortThreads> sh;
     const int tid = threadIdx.x, c = blockIdx.x;
-    for (int i = tid; i <= E; i += kRouteThreads) sh.fill[i] = 0;
+    for (int i = tid; i <= E; i += kSortThreads) sh.fill[i] = 0;
     __syncthreads();
     const int64_t p0 = (int64_t)c * o.chunk * k, p1 = min(P, p0 + (int64_t)o.chunk * k);
-    for (int64_t p = p0 + tid; p < p1; p += kRouteThreads) {
+    for (int64_t p = p0 + tid; p < p1; p += kSortThreads) {
         const Id id = ids[p];
         atomicAdd(&sh.fill[id < 0 || id >= (Id)E ? E : (int)id], 1);
     }
     __syncthreads();
     if (o.chunks > 1) {
-        for (int i = tid; i <= E; i += kRouteThreads) o.hist[(int64_t)c * (E + 1) + i] = sh.fill[i];
+        for (int i = tid; i <= E; i += kSortThreads) o.hist[(int64_t)c * (E + 1) + i] = sh.fill[i];
         return;
     }
-    for (int i = tid; i < kRouteWaves * 1025; i += kRouteThreads) (&sh.wcnt[0][0])[i] = 0;
-    exclusive_scan(sh.fill, sh.fill, E, sh.tmp);
-    for (int i = tid; i <= E; i += kRouteThreads) o.offsets[i] = sh.fill[i];
-    place_pairs(ids, p0, p1, E, k, o, sh);
+    for (int i = tid; i < kSortThreads / 64 * 1025; i += kSortThreads) (&sh.wcnt[0][0])[i] = 0;
+    exclusive_scan<kSortThreads>(sh.fill, sh.fill, E, sh.tmp);
+    for (int i = tid; i <= E; i += kSortThreads) o.offsets[i] = sh.fill[i];
+    place_pairs<kSortThreads>(ids, p0, p1, E, k, o, sh);
+}
+
+// The order of few pairs by comparing each with all; `few` has the pairs' buckets.
+constexpr int kFewPairs = 64;
+__device__ __forceinline__ void order_few(const int *few, int P, int E, int k, const PairOrder &o) {
+    const int tid = threadIdx.x;
+    for (int e = tid; e <= E; e += kRouteThreads) {
+        int n = 0;
+        for (int q = 0; q < P; ++q) n += few[q] < e;
+        o.offsets[e] = n;
+    }
+    if (tid < P) {
+        const int e = few[tid];
+        int at = 0;
+        for (int q = 0; q < P; ++q) at += few[q] < e || (few[q] == e && q < tid);
+        o.perm[at] = tid;
+        o.rows[at] = (int32_t)((uint32_t)tid / (uint32_t)k);
+        o.place[tid] = at;
+    }
 }
 
 // ------------------------------------------------------------------ router
-template <int DT, int L, int PER, bool GROUPS>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+constexpr int kGroupKeys = 1024;  // keys that a wave keeps in LDS to choose groups: L = E / 16 lanes a token at least
+
+template <int DT, int L, bool GROUPS, bool SOFT>
+__global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(RouteArgs a) {
     constexpr int TW = 64 / L, TB = TW * kRouteWaves;  // tokens of a wave, of a workgroup's pass
     // keys of a wave's tokens by expert; afterwards, in a single workgroup, the order of the pairs
     __shared__ union Shared {
-        float keys[GROUPS ? kRouteWaves : 1][GROUPS ? TW * L * PER : 1];
-        SortShared sort;
+        float keys[GROUPS ? kRouteWaves : 1][GROUPS ? kGroupKeys : 1];
+        SortShared<kRouteThreads> sort;
     } sh;
-    __shared__ int hist[1025];
+    __shared__ int hist[1025];  // pairs of each expert; few pairs: the expert of each
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & (L - 1), base = lane & ~(L - 1);  // this lane among its token's; the first of them
     const int E = a.E, k = a.k;
-    const bool order = a.o.perm != nullptr, soft = a.score == kSoftmax;
-    if (order) {
+    const bool order = a.o.perm != nullptr, few = order && a.T * k <= kFewPairs;
+    if (order && !few) {
         for (int i = tid; i <= E; i += kRouteThreads) hist[i] = 0;
         __syncthreads();
     }
+    // a bias that is the same for every expert changes no order: then, as without one, the logits are the keys
+    bool biased = false;
+    if (a.bias) {
+        const float first = a.bias[0];
+        bool same = fabsf(first) < INFINITY;
+        for (int e0 = 0; e0 < E; e0 += 256) {
+            float b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = a.bias[min(e0 + 64 * i + lane, E - 1)];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) same &= b[i] == first;
+        }
+        biased = __ballot(!same) != 0;
+    }
+    const bool ninth_wanted = k == kList && biased;
+    const bool scored = biased || GROUPS;
     const int t_end = min(a.T, (int)(blockIdx.x + 1) * a.o.chunk);
     for (int t0 = (int)blockIdx.x * a.o.chunk + wave * TW; t0 < t_end; t0 += TB) {
         const int t = t0 + lane / L;
         const bool live = t < t_end;
         const int64_t row = (int64_t)min(t, t_end - 1) * a.ld;
+        // this lane's logits of experts e0 + L i + j; -inf past the last
+        auto logits = [&](int e0, float (&l)[kList]) {
+#pragma unroll
+            for (int i = 0; i < kList; ++i) l[i] = load_logit<DT>(a.logits, row + min(e0 + L * i + j, E - 1));
+#pragma unroll
+            for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
+        };
 
-        // ---- logits, scores, keys
-        float l[PER];
+        float top = 0, z = 1, rz = 1;
+        // a key's error: of the score (sigmoid_near; e^x and the sum, against the largest probability, 1 / z)
+        float slack = 0x1p-22f;
+        if (SOFT && (scored || !a.renorm)) {
+            float l[kList];
+            top = -INFINITY;
+            for (int e0 = 0; e0 < E; e0 += kList * L) {
+                logits(e0, l);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = j + L * i;
-            const float v = load_logit<DT>(a.logits, row + min(e, E - 1));
-            l[i] = e < E ? v : -INFINITY;
-        }
-        float top = 0, z = 1;
-        if (soft) {
-            top = l[0];
-#pragma unroll
-            for (int i = 1; i < PER; ++i) top = fmaxf(top, l[i]);
+                for (int i = 0; i < kList; ++i) top = fmaxf(top, l[i]);
+            }
             top = group_max<L>(top);
             if (top == -INFINITY) top = 0;
-        }
-        // a key's error: of the score (sigmoid_near; e^x and the sum, against the largest probability, 1 / z)
-        float slack = 0x1p-21f;
-        const bool scored = a.bias || GROUPS;
-        if (soft && (scored || !a.renorm)) {
             float part = 0;
+            for (int e0 = 0; e0 < E; e0 += kList * L) {
+                logits(e0, l);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) part += exp_neg(l[i] - top);
+                for (int i = 0; i < kList; ++i) part += exp_neg(l[i] - top);
+            }
             z = group_sum<L>(part);
             if (z == 0) z = 1;
-            slack = 0x1p-20f / z;
+            rz = 1.0f / z;
+            slack = 0x1p-20f * rz;
         }
-        auto score_of_l = [&](float x) { return soft ? exp_neg(x - top) / z : sigmoid_near(x); };
-        uint32_t v[PER];
-        bool unsure = false;
-        if constexpr (GROUPS) {
-            float *keys = sh.keys[wave] + (lane / L) * L * PER;
+        // fp32 keys by score; -inf: not there
+        auto by_score = [&](int e0, const float (&l)[kList], float (&f)[kList]) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = j + L * i;
-                float f = score_of_l(l[i]) + (a.bias && e < E ? a.bias[e] : 0.0f);
-                f = l[i] == -INFINITY ? -INFINITY : number(f, -FLT_MAX);
-                keys[e] = f;
-                if (a.bias) v[i] = image_of(f);
+            for (int i = 0; i < kList; ++i) {
+                f[i] = SOFT ? __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504f) * rz : sigmoid_near(l[i]);
+                if (a.bias) f[i] += a.bias[min(e0 + L * i + j, E - 1)];
+                f[i] = number(f[i], -FLT_MAX);
+                f[i] = l[i] == -INFINITY ? -INFINITY : f[i];
+            }
+        };
+
+        bool unsure = false;
+        uint32_t kept = 0;
+        const int size = GROUPS ? E / a.groups : 1;
+        const uint32_t recip = ((1u << 20) + size - 1) / size;  // e / size for e < 1024
+        float *const keys = GROUPS ? sh.keys[wave] + (lane / L) * (kGroupKeys / TW) : nullptr;
+        if constexpr (GROUPS) {
+            wave_sync();  // the tokens before are done with the keys
+            for (int e0 = 0; e0 < E; e0 += kList * L) {
+                float l[kList], f[kList];
+                logits(e0, l);
+                by_score(e0, l, f);
+#pragma unroll
+                for (int i = 0; i < kList; ++i)
+                    if (e0 + L * i + j < E) keys[e0 + L * i + j] = f[i];
             }
             // lane g < groups: group g's score; lanes start at places of their own in it (banks)
             wave_sync();
-            const int size = E / a.groups;
             float t1 = -INFINITY, t2 = -INFINITY;
             if (j < a.groups) {
                 int at = j % size;
@@ -382,7 +505,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
                     at = at + 1 == size ? 0 : at + 1;
                 }
             }
-            wave_sync();
             const float mine = a.best == 2 && t2 != -INFINITY ? t1 + t2 : t1;
             // what the rounding of its sum is relative to
             const float size_of = (t1 == -INFINITY ? 0.0f : fabsf(t1)) + (t2 == -INFINITY ? 0.0f : fabsf(t2));
@@ -395,93 +517,114 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             // the least of the kept must be clearly above the largest of the others
             const float least = -group_max<L>(in ? -mine : -INFINITY);
             const float most = group_max<L>(!in && j < a.groups ? mine : -INFINITY);
-            if (most != -INFINITY)
-                unsure = !(least - most > 4 * slack + 0x1p-20f * group_max<L>(size_of));
-            const uint32_t kept = (uint32_t)(__ballot(in) >> base) & 0xffffu;
-            const uint32_t recip = ((1u << 20) + size - 1) / size;  // e / size for e < 1024
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t g = ((uint32_t)(j + L * i) * recip) >> 20;
-                if (!a.bias) v[i] = image_of(number(l[i] + 0.0f, -FLT_MAX));
-                v[i] = (kept >> g) & 1 ? v[i] : 0;
-            }
-        } else if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = j + L * i;
-                const float f = score_of_l(l[i]) + a.bias[min(e, E - 1)];
-                v[i] = l[i] == -INFINITY ? 0 : image_of(number(f, -FLT_MAX));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) v[i] = image_of(number(l[i] + 0.0f, -FLT_MAX));  // -0 as 0
+            if (most != -INFINITY) unsure = !(least - most > 4 * slack + 0x1p-20f * group_max<L>(size_of));
+            kept = (uint32_t)(__ballot(in) >> base) & 0xffffu;
         }
 
-        // ---- the k largest and the one after them
+        // ---- the eight largest keys, and the ninth
+        double list[kList], ninth = -kFar;
+        for (int e0 = 0; e0 < E; e0 += kList * L) {
+            double v[kList];
+            float l[kList], f[kList];
+            if (!GROUPS || !biased) logits(e0, l);
+            if (!biased) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = (v[i] & ~15u) | (15 - i);
-        sort_keys(v);
-        uint32_t last = 0;
-        int id = -1;  // lane r of the token: its expert of rank r
-        unroll<kMaxTopK + 1>([&](auto rank) {
-            constexpr int r = decltype(rank)::value;
-            if (r > k) return;
-            const uint32_t m = group_reduce<L>(v[0], umax);
-            const uint64_t hits = __ballot(v[0] == m) >> base;
-            const int owner = __ffsll((long long)(L == 64 ? hits : hits & ((1ull << (L & 63)) - 1))) - 1;
-            // is it clearly below the one before?
-            if (r > 0 && m >= kThere) {
-                if (a.bias) {
-                    const float hi = value_of(last & ~15u), lo = value_of(m & ~15u);
-                    unsure |= !(hi - lo > 2 * slack + 0x1p-18f * fmaxf(fabsf(hi), fabsf(lo)));
-                } else if (DT == kDtF32) {
-                    unsure |= (last ^ m) < 16;
-                }
+                for (int i = 0; i < kList; ++i) f[i] = number(l[i] + 0.0f, -FLT_MAX);  // -0 as 0
+            } else if constexpr (GROUPS) {
+#pragma unroll
+                for (int i = 0; i < kList; ++i) f[i] = keys[min(e0 + L * i + j, E - 1)];
+            } else {
+                by_score(e0, l, f);
             }
-            last = m;
-            if (r < k && j == r && m >= kThere) id = owner + L * (int)(15 - (m & 15));
-            const bool mine = j == owner;
 #pragma unroll
-            for (int i = 0; i + 1 < PER && i < kMaxTopK - r; ++i) v[i] = mine ? v[i + 1] : v[i];
-            if (kMaxTopK - r >= PER) v[PER - 1] = mine ? 0 : v[PER - 1];
-        });
-        // ---- where fp32 cannot tell, the whole wave decides in 64 bits, a token at a time
+            for (int i = 0; i < kList; ++i) {
+                const int e = e0 + L * i + j;
+                const bool in = e < E && (!GROUPS || (kept >> ((((uint32_t)e * recip) >> 20) & 31) & 1));
+                v[i] = pack_key(in ? f[i] : -INFINITY, e);
+            }
+            sort_list(v);
+            if (e0 == 0) {
+#pragma unroll
+                for (int i = 0; i < kList; ++i) list[i] = v[i];
+            } else {
+                merge_list(list, v, ninth, ninth_wanted);
+            }
+        }
+        merge_lanes<L>(list, ninth, ninth_wanted);
+        // lanes 0 .. 7 of the token: a candidate each, its logit, its score in 64 bits
+        double cand = -kFar;
+#pragma unroll
+        for (int i = 0; i < kList; ++i) cand = j == i ? list[i] : cand;
+        int id = there(cand) ? expert_of(cand) : -1, rank = j;
+        if (biased) {
+            // Keys by score may be off.  Sigmoids: the candidates are the right ones if a clear step comes between rank
+            // k and what is not among them, and their order is settled below.  (Behind a softmax's key is a sum that
+            // only choose_f64 forms in 64 bits: all steps have to be clear.)
+            bool any = false, all = true;
+#pragma unroll
+            for (int i = 0; i < kList; ++i) {
+                const double next = i + 1 < kList ? list[i + 1 < kList ? i + 1 : i] : ninth;
+                const float hi = value_of(list[i]), lo = value_of(next);
+                const bool clear = !there(next) || hi - lo > 2 * slack + 0x1p-23f * fmaxf(fabsf(hi), fabsf(lo));
+                any |= i >= k - 1 && (i + 1 < kList || ninth_wanted) && clear;
+                all &= i >= k || clear;
+            }
+            unsure |= SOFT ? !all : !any;
+        }
+        // where fp32 cannot tell, the whole wave decides in 64 bits, a token at a time
         uint64_t todo = __ballot(unsure && live && j == 0);
         while (todo) {
             const int at = __ffsll((long long)todo) - 1;
             todo &= todo - 1;
-            const int r = choose_f64<DT, L * PER / 64>(a, t0 + at / L, __shfl(top, at), lane);
-            const int mine = __shfl(r, j);
-            if (base == at) id = j < k ? mine : -1;
+            const int r = choose_f64<DT>(a, t0 + at / L, __shfl(top, at), biased, lane);
+            const int theirs = __shfl(r, j);
+            if (base == at) id = j < k ? theirs : -1;
         }
-        // ---- weights, in 64 bits
+        // Weights, in 64 bits.  Renormalised, a softmax needs no sum over all.
+        const float l = id >= 0 ? load_logit<DT>(a.logits, row + id) : -INFINITY;
+        const float about = SOFT && a.renorm ? group_max<L>(l) : top;
         double s = 0;
-        if (id >= 0) {
-            const double x = load_logit<DT>(a.logits, row + id);
-            s = soft ? exp(x - (double)top) / (double)z : sigmoid_f64(x);
+        if (id >= 0) s = SOFT ? exp((double)l - (double)about) / (a.renorm ? 1.0 : (double)z) : sigmoid_f64(l);
+        if (!SOFT && biased) {  // rank by the keys in 64 bits (a token that choose_f64 has ranked stays as it is)
+            const double key = id < 0 ? -INFINITY : number(s + (double)a.bias[id], -DBL_MAX);
+            int before = 0;
+#pragma unroll
+            for (int i = 0; i < kList; ++i) {
+                const double o = __shfl(key, base + i);
+                const int other = __shfl(id, base + i);
+                before += o > key || (o == key && other < id);
+            }
+            rank = j >= kList ? L : id < 0 ? j : before;
         }
+        const bool chosen = rank < k;
+        if (!chosen) s = 0;
         if (a.renorm) {
             const double sum = group_reduce<L>(s, [](double x, double y) { return x + y; });
             s = sum == 0 ? 0 : s / sum;
         }
-        if (live && j < k) {
-            const int64_t p = (int64_t)t * k + j;
+        if (live && chosen) {
+            const int64_t p = (int64_t)t * k + rank;
             a.ids[p] = id;
             a.w[p] = (float)(s * a.scale);
-            if (order) atomicAdd(&hist[id < 0 ? E : id], 1);
+            if (few) hist[p] = id < 0 ? E : id;
+            else if (order) atomicAdd(&hist[id < 0 ? E : id], 1);
         }
     }
     if (!order) return;
     __syncthreads();
+    if (few) {
+        order_few(hist, a.T * k, E, k, a.o);
+        return;
+    }
     if (a.o.chunks > 1) {
         for (int i = tid; i <= E; i += kRouteThreads) a.o.hist[(int64_t)blockIdx.x * (E + 1) + i] = hist[i];
         return;
     }
     // a single workgroup: its stores of ids have been made (the barrier waits for them)
     for (int i = tid; i < kRouteWaves * 1025; i += kRouteThreads) (&sh.sort.wcnt[0][0])[i] = 0;
-    exclusive_scan(hist, sh.sort.fill, E, sh.sort.tmp);
+    exclusive_scan<kRouteThreads>(hist, sh.sort.fill, E, sh.sort.tmp);
     for (int i = tid; i <= E; i += kRouteThreads) a.o.offsets[i] = sh.sort.fill[i];
-    place_pairs(a.ids, 0, (int64_t)a.T * k, E, k, a.o, sh.sort);
+    place_pairs<kRouteThreads>(a.ids, 0, (int64_t)a.T * k, E, k, a.o, sh.sort);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -547,36 +690,34 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteArgs a) {
     }
 }
 
-template <int DT, bool GROUPS>
-void route_by_size(const RouteArgs &a, dim3 grid, hipStream_t s) {
-    const dim3 block(kRouteThreads);
-    if (a.E <= 64) klaunch(route_kernel<DT, 16, 4, GROUPS>, grid, block, s, a);
-    else if (a.E <= 128) klaunch(route_kernel<DT, 16, 8, GROUPS>, grid, block, s, a);
-    else if (a.E <= 256) klaunch(route_kernel<DT, 16, 16, GROUPS>, grid, block, s, a);
-    else if (a.E <= 512) klaunch(route_kernel<DT, 32, 16, GROUPS>, grid, block, s, a);
-    else klaunch(route_kernel<DT, 64, 16, GROUPS>, grid, block, s, a);
-}
-
 template <class Id>
 hipError_t place(const Id *ids, int64_t P, int E, int k, const PairOrder &o, hipStream_t s) {
-    klaunch(place_kernel<Id>, dim3(o.chunks), dim3(kRouteThreads), s, ids, P, E, k, o);
+    klaunch(scan_kernel, dim3((E + 1 + 31) / 32), dim3(kSortThreads), s, E, o);
+    klaunch(place_kernel<Id>, dim3(o.chunks), dim3(kSortThreads), s, ids, P, E, k, o);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// At most 256 chunks, which every one of them reads the counts of, of 64 tokens at least (a pass of a workgroup).
+// At most 512 chunks of 64 tokens at least (a pass of a workgroup).
 int32_t order_chunk(int64_t tokens) {
-    const int64_t each = (tokens + 255) / 256;
+    const int64_t each = (tokens + 511) / 512;
     return (int32_t)((each < 64 ? 64 : each) + 63) / 64 * 64;
 }
 
 hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)((a.T + a.o.chunk - 1) / a.o.chunk));
+    const dim3 block(kRouteThreads);
     auto go = [&](auto d) {
         constexpr int DT = decltype(d)::value;
-        if (a.groups > 1) route_by_size<DT, true>(a, grid, s);
-        else route_by_size<DT, false>(a, grid, s);
+        auto pick = [&](auto soft) {
+            constexpr bool SOFT = decltype(soft)::value;
+            if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT>, grid, block, s, a);
+            else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT>, grid, block, s, a);
+            else klaunch(route_kernel<DT, 64, true, SOFT>, grid, block, s, a);
+        };
+        if (a.score == kSoftmax) pick(std::true_type{});
+        else pick(std::false_type{});
     };
     if (dt == kDtF32) go(std::integral_constant<int, kDtF32>{});
     else if (dt == kDtBf16) go(std::integral_constant<int, kDtBf16>{});
@@ -596,7 +737,7 @@ hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
 
 hipError_t launch_sort_pairs(const void *ids, bool wide, int64_t tokens, int32_t k, int32_t E, const PairOrder &o,
                              hipStream_t s) {
-    const dim3 grid(o.chunks), block(kRouteThreads);
+    const dim3 grid(o.chunks), block(kSortThreads);
     const int64_t P = tokens * k;
     if (wide) klaunch(count_kernel<int64_t>, grid, block, s, (const int64_t *)ids, P, (int)E, (int)k, o);
     else klaunch(count_kernel<int32_t>, grid, block, s, (const int32_t *)ids, P, (int)E, (int)k, o);

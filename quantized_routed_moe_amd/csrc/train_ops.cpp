@@ -208,7 +208,7 @@ int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows,
 size_t moe_pair_order_bytes(int64_t tokens, int32_t n_experts) {
     if (tokens < 0 || tokens > MOE_MAX_PAIRS || n_experts < 1 || n_experts > 1024) return 0;
     const int32_t chunks = order_chunks(tokens);
-    return chunks > 1 ? (size_t)chunks * (n_experts + 1) * 4 : 0;
+    return chunks > 1 ? (size_t)(chunks + 1) * (n_experts + 1) * 4 : 0;
 }
 
 int moe_route(const moe_router *r, int32_t dtype, const void *logits, int64_t stride, int64_t tokens, int32_t *ids,
