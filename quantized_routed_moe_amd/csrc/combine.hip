@@ -13,8 +13,6 @@ namespace qrmoe {
 
 namespace {
 
-constexpr int kTogether = 8;  // pairs of a token whose rows are loaded together
-
 // Threads take eight columns each: whole workgroups of one token where rows are long, several tokens where not.
 template <int DT, int OUT, int K>  // K pairs a token; 0: any number
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
@@ -64,60 +62,81 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
 }
 
 // One workgroup a token.
-template <int DT, int DOUT>
+template <int DT, int DOUT, int K>  // K pairs a token; 0: any number
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineArgs a) {
-    __shared__ float part[kThreads / 64][kTogether];
+    constexpr int N = K > 0 ? K : 4;  // pairs whose rows are loaded together
+    __shared__ float part[kThreads / 64][N];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
-    const int per = (int)(a.H / 8);
+    const int per = (int)(a.H / 8), k = K > 0 ? K : a.k;
     const int64_t t = blockIdx.x;
-    for (int j0 = 0; j0 < a.k; j0 += kTogether) {
-        const int n = min(a.k - j0, kTogether);
-        int64_t p[kTogether];
-        float f[kTogether], dot[kTogether];
+    for (int j0 = 0; j0 < k; j0 += N) {
+        int64_t p[N];
+        float f[N], dot[N];
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            p[j] = j < n ? a.place[t * a.k + j0 + j] : -1;
+        for (int j = 0; j < N; ++j) {
+            const bool in = K > 0 || j0 + j < k;
+            p[j] = in ? a.place[t * k + j0 + j] : -1;
             if ((uint64_t)p[j] >= (uint64_t)a.P) p[j] = -1;
-            f[j] = j >= n ? 0.0f : a.w ? a.w[t * a.k + j0 + j] : 1.0f;
+            f[j] = !in ? 0.0f : a.w ? a.w[t * k + j0 + j] : 1.0f;
             dot[j] = 0;
         }
         for (int c = tid; c < per; c += threads) {
-            float d[8], y[kTogether][8];
+            float d[8], y[N][8];
             load8<DOUT>(a.dout, t * a.out_ld + 8 * c, d);
             if (a.dw) {
 #pragma unroll
-                for (int j = 0; j < kTogether; ++j)
+                for (int j = 0; j < N; ++j)
                     if (p[j] >= 0) load8<DT>(a.y, p[j] * a.y_ld + 8 * c, y[j]);
             }
+            if (a.dy) {
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
-                if (p[j] < 0) continue;
-                if (a.dw) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(y[j][i], d[i], dot[j]);
-                }
-                if (a.dy) {
+                for (int j = 0; j < N; ++j) {
+                    if (p[j] < 0) continue;
                     float v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = f[j] * d[i];
                     store8<DT>(a.dy, p[j] * a.dy_ld + 8 * c, v);
                 }
             }
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (p[j] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(y[j][i], d[i], dot[j]);
+                }
+            }
         }
         if (!a.dw) continue;
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
+        for (int j = 0; j < N; ++j) {
             const float s = group_sum<64>(dot[j]);
             if (lane == 0) part[wave][j] = s;
         }
         __syncthreads();
-        if (tid < n) {
+        if (tid < N && j0 + tid < k) {
             float s = 0;
             for (int v = 0; v < threads / 64; ++v) s += part[v][tid];
-            a.dw[t * a.k + j0 + tid] = s;
+            a.dw[t * k + j0 + tid] = s;
         }
         __syncthreads();
     }
+}
+
+// f(integral_constant k) for k of at most eight, else f(0).
+template <class F>
+hipError_t by_pairs(int k, F &&f) {
+    switch (k) {
+        case 1: return f(std::integral_constant<int, 1>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        case 3: return f(std::integral_constant<int, 3>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+        case 5: return f(std::integral_constant<int, 5>{});
+        case 6: return f(std::integral_constant<int, 6>{});
+        case 7: return f(std::integral_constant<int, 7>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+    }
+    return f(std::integral_constant<int, 0>{});
 }
 
 }  // namespace
@@ -127,20 +146,11 @@ hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStr
     const int64_t blocks = per >= kThreads ? a.T * ((per + kThreads - 1) / kThreads)
                                            : (a.T + kThreads / per - 1) / (kThreads / per);
     auto go = [&](auto dt_c, auto out_c) {
-        constexpr int DT = decltype(dt_c)::value, OUT = decltype(out_c)::value;
-        auto k = combine_kernel<DT, OUT, 0>;
-        switch (a.k) {
-            case 1: k = combine_kernel<DT, OUT, 1>; break;
-            case 2: k = combine_kernel<DT, OUT, 2>; break;
-            case 3: k = combine_kernel<DT, OUT, 3>; break;
-            case 4: k = combine_kernel<DT, OUT, 4>; break;
-            case 5: k = combine_kernel<DT, OUT, 5>; break;
-            case 6: k = combine_kernel<DT, OUT, 6>; break;
-            case 7: k = combine_kernel<DT, OUT, 7>; break;
-            case 8: k = combine_kernel<DT, OUT, 8>; break;
-        }
-        klaunch(k, dim3((unsigned)blocks), dim3(kThreads), s, a);
-        return hipGetLastError();
+        return by_pairs(a.k, [&](auto k_c) {
+            klaunch(combine_kernel<decltype(dt_c)::value, decltype(out_c)::value, decltype(k_c)::value>,
+                    dim3((unsigned)blocks), dim3(kThreads), s, a);
+            return hipGetLastError();
+        });
     };
     constexpr std::integral_constant<int, kDtF32> f32{};
     constexpr std::integral_constant<int, kDtBf16> bf16{};
@@ -153,14 +163,19 @@ hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStr
 hipError_t launch_combine_grad(int dt, int dout_dt, const CombineArgs &a, hipStream_t s) {
     const int64_t per = a.H / 8;
     const dim3 grid((unsigned)a.T), block(per <= 64 ? 64 : per <= 128 ? 128 : kThreads);
-    auto go = [&](auto k) {
-        klaunch(k, grid, block, s, a);
-        return hipGetLastError();
+    auto go = [&](auto dt_c, auto dout_c) {
+        return by_pairs(a.k, [&](auto k_c) {
+            klaunch(combine_grad_kernel<decltype(dt_c)::value, decltype(dout_c)::value, decltype(k_c)::value>, grid, block, s,
+                    a);
+            return hipGetLastError();
+        });
     };
-    if (dt == kDtF32) return go(combine_grad_kernel<kDtF32, kDtF32>);
-    if (dt == kDtBf16)
-        return dout_dt == kDtF32 ? go(combine_grad_kernel<kDtBf16, kDtF32>) : go(combine_grad_kernel<kDtBf16, kDtBf16>);
-    return dout_dt == kDtF32 ? go(combine_grad_kernel<kDtF16, kDtF32>) : go(combine_grad_kernel<kDtF16, kDtF16>);
+    constexpr std::integral_constant<int, kDtF32> f32{};
+    constexpr std::integral_constant<int, kDtBf16> bf16{};
+    constexpr std::integral_constant<int, kDtF16> f16{};
+    if (dt == kDtF32) return go(f32, f32);
+    if (dt == kDtBf16) return dout_dt == kDtF32 ? go(bf16, f32) : go(bf16, bf16);
+    return dout_dt == kDtF32 ? go(f16, f32) : go(f16, f16);
 }
 
 }  // namespace qrmoe

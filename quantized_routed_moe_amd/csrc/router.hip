@@ -37,13 +37,6 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t at) {
     else if constexpr (DT == kDtBf16) return (float)((const __bf16 *)p)[at];
     else return (float)((const _Float16 *)p)[at];
 }
-template <int DT>
-__device__ __forceinline__ void store_logit(void *p, int64_t at, float v) {
-    if constexpr (DT == kDtF32) ((float *)p)[at] = v;
-    else if constexpr (DT == kDtBf16) ((__bf16 *)p)[at] = (__bf16)v;
-    else ((_Float16 *)p)[at] = (_Float16)v;
-}
-
 // e^x for x <= 0 (or NaN) with a relative error of a few units of 2^-24: the integer part of x log2(e) is put on as an
 // exponent, what is left is formed without the rounding of the product.
 __device__ __forceinline__ float exp_neg(float x) {
@@ -631,58 +624,117 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
 //   G_j = dw_j scale;  renormalised: G_j <- (G_j - sum_i G_i s_i / S) / S
 //   sigmoid: dl_j = G_j s_j (1 - s_j) at the chosen, 0 elsewhere
 //   softmax: dl_e = s_e (G_e - sum_j G_j s_j); renormalised the sum is 0
-// One wave a token; what the chosen get passes through LDS, one after the
-// other, so that an expert named twice gets both.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteArgs a) {
-    __shared__ float rows[kThreads / 64][1024];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E, k = a.k;
-    float *mine = rows[wave];
-    for (int e = lane; e < E; e += 64) mine[e] = 0;
-    const bool soft = a.score == kSoftmax, dense = soft && !a.renorm;
-    for (int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave; t < a.T; t += (int64_t)gridDim.x * (kThreads / 64)) {
-        const int64_t row = t * a.ld;
-        float top = -INFINITY, z = 0;
-        if (soft) {
-            for (int e = lane; e < E; e += 64) top = fmaxf(top, load_logit<DT>(a.logits, row + e));
-            top = group_max<64>(top);
-            if (top == -INFINITY) top = 0;
-            if (dense) {
-                for (int e = lane; e < E; e += 64) z += exp_neg(load_logit<DT>(a.logits, row + e) - top);
-                z = group_sum<64>(z);
-            }
-        }
-        if (!dense || z == 0) z = 1;
-        int id = lane < k ? a.ids[t * k + lane] : -1;
+// What it has to move is the gradient of every logit, and the logits where all of them have one (DENSE: softmax, not
+// renormalised); those are read once and their exponentials stay in registers.  L lanes a token, V consecutive experts
+// a lane and access.  What the chosen get passes through LDS, one after the other, so that an expert named twice gets
+// both.
+constexpr int kGradThreads = 256;
+template <int DT, int V>
+__device__ __forceinline__ void load_some(const void *p, int64_t at, float (&v)[V]) {
+    typedef typename std::conditional<DT == kDtF32, float, typename std::conditional<DT == kDtBf16, __bf16, _Float16>::type>::type T;
+    typedef T TV __attribute__((ext_vector_type(V)));
+    if constexpr (V == 1) {
+        v[0] = (float)((const T *)p)[at];
+    } else {
+        const TV x = *reinterpret_cast<const TV *>((const T *)p + at);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)x[i];
+    }
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_some(void *p, int64_t at, const float (&v)[V]) {
+    typedef typename std::conditional<DT == kDtF32, float, typename std::conditional<DT == kDtBf16, __bf16, _Float16>::type>::type T;
+    typedef T TV __attribute__((ext_vector_type(V)));
+    if constexpr (V == 1) {
+        ((T *)p)[at] = (T)v[0];
+    } else {
+        TV x;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = (T)v[i];
+        *reinterpret_cast<TV *>((T *)p + at) = x;
+    }
+}
+
+template <int DT, int L, int PER, int V, bool DENSE>
+__global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
+    constexpr int TW = 64 / L, WAVES = kGradThreads / 64, N = PER / V;  // accesses of a lane
+    __shared__ float rows[WAVES][TW][L * PER];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & (L - 1), E = a.E, k = a.k;
+    float *mine = rows[wave][lane / L];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[L * i + j] = 0;
+    wave_sync();
+    const bool soft = DENSE || a.score == kSoftmax;
+    const int64_t step = (int64_t)gridDim.x * WAVES * TW;
+    for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + wave) * TW; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + lane / L, tt = t < a.T ? t : a.T - 1;
+        const int64_t row = tt * a.ld;
+        int id = j < k ? a.ids[tt * k + j] : -1;
         if ((uint32_t)id >= (uint32_t)E) id = -1;
-        double s = 0, rest = 0, g = 0;  // score, its complement, the gradient of the score
-        if (id >= 0) {
-            const double x = load_logit<DT>(a.logits, row + id);
-            if (soft) {
-                s = exp(x - (double)top) / (double)z;
-            } else {
-                const double e = exp(-fabs(x)), q = 1.0 / (1.0 + e);
-                s = x < 0 ? e * q : q;
-                rest = x < 0 ? q : e * q;
+        const float dw = j < k ? a.dw[tt * k + j] : 0.0f;
+        const float l = id >= 0 ? load_logit<DT>(a.logits, row + id) : -INFINITY;
+        float ex[N][V], top = 0, rz = 1;
+        if constexpr (DENSE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = (i * L + j) * V;  // all of the V or none are experts
+                load_some<DT, V>(a.logits, row + min(e, E - V), ex[i]);
+#pragma unroll
+                for (int u = 0; u < V; ++u) ex[i][u] = e < E ? ex[i][u] : -INFINITY;
             }
-            g = (double)a.dw[t * k + lane] * a.scale;
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int u = 0; u < V; ++u) top = fmaxf(top, ex[i][u]);
+            top = group_max<L>(top);
+            if (top == -INFINITY) top = 0;
+            float z = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    ex[i][u] = exp_neg(ex[i][u] - top);
+                    z += ex[i][u];
+                }
+            z = group_sum<L>(z);
+            rz = z == 0 ? 1.0f : 1.0f / z;
         }
-        double gs = wave_sum_f64(g * s);
-        if (a.renorm) {
-            double sum = wave_sum_f64(s);
-            if (sum == 0) sum = 1;
-            g = (g - gs / sum) / sum;
+        float d, c = 0;
+        if constexpr (DENSE) {
+            // the sum over the chosen may cancel: in 64 bits, and with it the scores of which it is made
+            const double g = id >= 0 ? (double)dw * a.scale * (exp((double)l - (double)top) * (double)rz) : 0.0;
+            d = (float)g;
+            c = (float)(group_reduce<L>(g, [](double x, double y) { return x + y; }) * (double)rz);
+        } else {
+            double s = 0, rest = 0, g = id >= 0 ? (double)dw * a.scale : 0.0;  // score, its complement, the gradient of the score
+            const float about = soft ? group_max<L>(l) : 0.0f;
+            if (id >= 0) {
+                const double x = soft ? (double)l - (double)about : (double)l, e = exp(soft ? x : -fabs(x)), q = 1.0 / (1.0 + e);
+                s = soft ? e : x < 0 ? e * q : q;
+                rest = soft ? 1.0 : x < 0 ? q : e * q;
+            }
+            auto add = [](double x, double y) { return x + y; };
+            if (a.renorm) {
+                const double gs = group_reduce<L>(g * s, add), sum = group_reduce<L>(s, add), r = sum == 0 ? 1.0 : 1.0 / sum;
+                g = (g - gs * r) * r;
+            }
+            d = (float)(g * s * rest);
         }
-        const float d = (float)(soft ? g * s : g * s * rest);
         for (int r = 0; r < k; ++r) {
-            if (lane == r && id >= 0) mine[id] += d;
+            if (j == r && id >= 0) mine[id] += d;
             wave_sync();
         }
-        const float c = (float)gs;
-        for (int e = lane; e < E; e += 64) {
-            float v = mine[e];
-            if (dense) v -= exp_neg(load_logit<DT>(a.logits, row + e) - top) / z * c;
-            store_logit<DT>(a.dlogits, t * a.d_ld + e, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = (i * L + j) * V;
+            float v[V];
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                v[u] = mine[e + u];
+                if constexpr (DENSE) v[u] = __builtin_fmaf(-c, ex[i][u], v[u]);
+            }
+            if (e < E && t < a.T) store_some<DT, V>(a.dlogits, t * a.d_ld + e, v);
         }
         wave_sync();
         if (id >= 0) mine[id] = 0;
@@ -728,10 +780,29 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
-    auto k = dt == kDtF32 ? route_grad_kernel<kDtF32>
-                          : dt == kDtBf16 ? route_grad_kernel<kDtBf16> : route_grad_kernel<kDtF16>;
-    const int64_t blocks = (a.T + kThreads / 64 - 1) / (kThreads / 64);
-    klaunch(k, dim3((unsigned)(blocks > 8192 ? 8192 : blocks)), dim3(kThreads), s, a);
+    const bool dense = a.score == kSoftmax && !a.renorm;
+    const uintptr_t at = (uintptr_t)a.logits | (uintptr_t)a.dlogits;
+    const bool four = (a.E | a.ld | a.d_ld) % 4 == 0 && at % (dt == kDtF32 ? 16 : 8) == 0;
+    auto go = [&](auto d_c, auto dense_c, auto v_c) {
+        constexpr int DT = decltype(d_c)::value, V = decltype(v_c)::value;
+        constexpr bool DENSE = decltype(dense_c)::value;
+        auto with = [&](auto k, int tokens) {
+            const int64_t blocks = (a.T + tokens - 1) / tokens;
+            klaunch(k, dim3((unsigned)(blocks > 4096 ? 4096 : blocks)), dim3(kGradThreads), s, a);
+        };
+        if (a.E <= 64) with(route_grad_kernel<DT, 16, 4, V, DENSE>, 16);
+        else if (a.E <= 256) with(route_grad_kernel<DT, 16, 16, V, DENSE>, 16);
+        else with(route_grad_kernel<DT, 64, 16, V, DENSE>, 4);
+    };
+    auto pick = [&](auto d_c) {
+        constexpr std::integral_constant<int, 1> one{};
+        constexpr std::integral_constant<int, 4> some{};
+        if (dense) four ? go(d_c, std::true_type{}, some) : go(d_c, std::true_type{}, one);
+        else four ? go(d_c, std::false_type{}, some) : go(d_c, std::false_type{}, one);
+    };
+    if (dt == kDtF32) pick(std::integral_constant<int, kDtF32>{});
+    else if (dt == kDtBf16) pick(std::integral_constant<int, kDtBf16>{});
+    else pick(std::integral_constant<int, kDtF16>{});
     return hipGetLastError();
 }
 
