@@ -37,6 +37,14 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t at) {
     else if constexpr (DT == kDtBf16) return (float)((const __bf16 *)p)[at];
     else return (float)((const _Float16 *)p)[at];
 }
+// The same through a buffer descriptor, offsets in bytes; past its end: 0.
+template <int DT>
+__device__ __forceinline__ float load_logit(__amdgpu_buffer_rsrc_t r, int at) {
+    if constexpr (DT == kDtF32) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+    else if constexpr (DT == kDtBf16) return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0) << 16);
+    else return (float)__builtin_bit_cast(_Float16, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+}
+
 // e^x for x <= 0 (or NaN) with a relative error of a few units of 2^-24: the integer part of x log2(e) is put on as an
 // exponent, what is left is formed without the rounding of the product.
 __device__ __forceinline__ float exp_neg(float x) {
@@ -77,20 +85,21 @@ __device__ __forceinline__ double lesser(double a, double b) {
     return r;
 }
 // fp32 keys as doubles that carry the expert in their low ten bits: of equal ones the lower expert is the larger.
-// Infinities, which have no room for it, are +-kFar; an expert that is not there has -kFar.
-constexpr double kFar = 0x1p200;
-__device__ __forceinline__ double pack_key(float key, int e) {
-    const double d = lesser(larger((double)key, -kFar), kFar);
-    const uint64_t u = (uint64_t)__double_as_longlong(d);
-    const uint32_t hi = (uint32_t)(u >> 32), low = (uint32_t)u | ((uint32_t)e ^ (1023u & ~(uint32_t)((int)hi >> 31)));
+// +-infinity, which has no room for it, is +-kFar, a NaN kNan; an expert that is not there has kAbsent.
+constexpr double kFar = 0x1p200, kNan = -0x1p150, kAbsent = -0x1p300;
+__device__ __forceinline__ double pack_key(float key, int e, bool in) {
+    // (a NaN gives way to the other operand)
+    const uint64_t u = (uint64_t)__double_as_longlong(lesser(larger((double)key, kNan), kFar));
+    const uint32_t top = (uint32_t)(u >> 32), hi = in ? top : (uint32_t)((uint64_t)__builtin_bit_cast(uint64_t, kAbsent) >> 32);
+    const uint32_t low = (uint32_t)u | ((uint32_t)e ^ (1023u & ~(uint32_t)((int)top >> 31)));
     return __longlong_as_double((long long)((uint64_t)hi << 32 | low));
 }
 __device__ __forceinline__ int expert_of(double k) {
     const uint64_t u = (uint64_t)__double_as_longlong(k);
     return (int)(((uint32_t)u ^ ~(uint32_t)((int)(u >> 32) >> 31)) & 1023u);
 }
-__device__ __forceinline__ bool there(double k) { return k > -0x1p199; }
-__device__ __forceinline__ float value_of(double k) {  // the fp32 key
+__device__ __forceinline__ bool there(double k) { return k > -0x1p299; }
+__device__ __forceinline__ float value_of(double k) {  // the fp32 key (a NaN's: -infinity)
     return (float)__longlong_as_double(__double_as_longlong(k) & ~1023ll);
 }
 
@@ -242,6 +251,12 @@ struct SortShared {
     int tmp[THREADS / 64];
 };
 
+template <int THREADS>
+__device__ __forceinline__ void zero_counts(SortShared<THREADS> &sh, int E) {
+    for (int w = 0; w < THREADS / 64; ++w)
+        for (int i = threadIdx.x; i <= E; i += THREADS) sh.wcnt[w][i] = 0;
+}
+
 // fill[b] for b <= E: how many pairs stand before those of bucket b, from total[b] (LDS; the buckets' pairs; may be fill).
 template <int THREADS>
 __device__ __forceinline__ void exclusive_scan(const int *total, int *fill, int E, int *tmp) {
@@ -332,7 +347,7 @@ template <class Id>
 __global__ __launch_bounds__(kSortThreads) void place_kernel(const Id *ids, int64_t P, int E, int k, PairOrder o) {
     __shared__ SortShared<kSortThreads> sh;
     const int tid = threadIdx.x, c = blockIdx.x, buckets = E + 1;
-    for (int i = tid; i < kSortThreads / 64 * 1025; i += kSortThreads) (&sh.wcnt[0][0])[i] = 0;
+    zero_counts<kSortThreads>(sh, E);
     for (int i = tid; i < buckets; i += kSortThreads) sh.fill[i] = o.hist[(int64_t)o.chunks * buckets + i];
     __syncthreads();
     exclusive_scan<kSortThreads>(sh.fill, sh.fill, E, sh.tmp);
@@ -362,7 +377,7 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const Id *ids, int6
         for (int i = tid; i <= E; i += kSortThreads) o.hist[(int64_t)c * (E + 1) + i] = sh.fill[i];
         return;
     }
-    for (int i = tid; i < kSortThreads / 64 * 1025; i += kSortThreads) (&sh.wcnt[0][0])[i] = 0;
+    zero_counts<kSortThreads>(sh, E);
     exclusive_scan<kSortThreads>(sh.fill, sh.fill, E, sh.tmp);
     for (int i = tid; i <= E; i += kSortThreads) o.offsets[i] = sh.fill[i];
     place_pairs<kSortThreads>(ids, p0, p1, E, k, o, sh);
@@ -390,7 +405,8 @@ __device__ __forceinline__ void order_few(const int *few, int P, int E, int k, c
 // ------------------------------------------------------------------ router
 constexpr int kGroupKeys = 1024;  // keys that a wave keeps in LDS to choose groups: L = E / 16 lanes a token at least
 
-template <int DT, int L, bool GROUPS, bool SOFT>
+// FULL: the experts fill whole accesses of the lanes.
+template <int DT, int L, bool GROUPS, bool SOFT, bool FULL>
 __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(RouteArgs a) {
     constexpr int TW = 64 / L, TB = TW * kRouteWaves;  // tokens of a wave, of a workgroup's pass
     // keys of a wave's tokens by expert; afterwards, in a single workgroup, the order of the pairs
@@ -407,6 +423,14 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         for (int i = tid; i <= E; i += kRouteThreads) hist[i] = 0;
         __syncthreads();
     }
+    constexpr int B = DT == kDtF32 ? 4 : 2;
+    const int first_t = (int)blockIdx.x * a.o.chunk, t_end = min(a.T, first_t + a.o.chunk);
+    // offsets are relative to the chunk's first row and have 31 bits (checked on the host)
+    const uint8_t *const chunk = (const uint8_t *)a.logits + (int64_t)first_t * a.ld * B;
+    const auto from = buf_rsrc(chunk, (uint32_t)(((int64_t)(t_end - first_t - 1) * a.ld + E) * B));
+    const auto bias_from = buf_rsrc(a.bias, a.bias ? 4 * E : 0);  // no bias: zeros
+    // the first logits are asked for before anything is waited for
+    const float ahead = load_logit<DT>(from, (int)(min(wave * TW + lane / L, t_end - first_t - 1) * a.ld + min(j, E - 1)) * B);
     // a bias that is the same for every expert changes no order: then, as without one, the logits are the keys
     bool biased = false;
     if (a.bias) {
@@ -421,19 +445,21 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         }
         biased = __ballot(!same) != 0;
     }
+    asm volatile("" ::"v"(ahead));
     const bool ninth_wanted = k == kList && biased;
     const bool scored = biased || GROUPS;
-    const int t_end = min(a.T, (int)(blockIdx.x + 1) * a.o.chunk);
-    for (int t0 = (int)blockIdx.x * a.o.chunk + wave * TW; t0 < t_end; t0 += TB) {
+    for (int t0 = first_t + wave * TW; t0 < t_end; t0 += TB) {
         const int t = t0 + lane / L;
         const bool live = t < t_end;
-        const int64_t row = (int64_t)min(t, t_end - 1) * a.ld;
+        const int row = (int)((min(t, t_end - 1) - first_t) * a.ld) * B;  // bytes behind the chunk's first
         // this lane's logits of experts e0 + L i + j; -inf past the last
         auto logits = [&](int e0, float (&l)[kList]) {
 #pragma unroll
-            for (int i = 0; i < kList; ++i) l[i] = load_logit<DT>(a.logits, row + min(e0 + L * i + j, E - 1));
+            for (int i = 0; i < kList; ++i) l[i] = load_logit<DT>(from, row + (e0 + j) * B + L * i * B);
+            if constexpr (!FULL) {
 #pragma unroll
-            for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
+                for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
+            }
         };
 
         float top = 0, z = 1, rz = 1;
@@ -460,15 +486,14 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
             rz = 1.0f / z;
             slack = 0x1p-20f * rz;
         }
-        // fp32 keys by score; -inf: not there
+        // fp32 keys by score; a logit of -inf needs its own look
         auto by_score = [&](int e0, const float (&l)[kList], float (&f)[kList]) {
+            float b[kList];
 #pragma unroll
-            for (int i = 0; i < kList; ++i) {
-                f[i] = SOFT ? __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504f) * rz : sigmoid_near(l[i]);
-                if (a.bias) f[i] += a.bias[min(e0 + L * i + j, E - 1)];
-                f[i] = number(f[i], -FLT_MAX);
-                f[i] = l[i] == -INFINITY ? -INFINITY : f[i];
-            }
+            for (int i = 0; i < kList; ++i) b[i] = load_logit<kDtF32>(bias_from, (e0 + j) * 4 + L * i * 4);
+#pragma unroll
+            for (int i = 0; i < kList; ++i)
+                f[i] = (SOFT ? __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504f) * rz : sigmoid_near(l[i])) + b[i];
         };
 
         bool unsure = false;
@@ -484,27 +509,36 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
                 by_score(e0, l, f);
 #pragma unroll
                 for (int i = 0; i < kList; ++i)
-                    if (e0 + L * i + j < E) keys[e0 + L * i + j] = f[i];
+                    if (FULL || e0 + L * i + j < E)
+                        keys[e0 + L * i + j] = l[i] == -INFINITY ? -INFINITY : number(f[i], -FLT_MAX);
             }
             // lane g < groups: group g's score; lanes start at places of their own in it (banks)
             wave_sync();
             float t1 = -INFINITY, t2 = -INFINITY;
             if (j < a.groups) {
                 int at = j % size;
-                for (int n = 0; n < size; ++n) {
-                    const float x = keys[j * size + at];
-                    t2 = fmaxf(t2, fminf(t1, x));
-                    t1 = fmaxf(t1, x);
-                    at = at + 1 == size ? 0 : at + 1;
+                for (int n = 0; n < size; n += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        x[u] = n + u < size ? keys[j * size + at] : -INFINITY;
+                        at = at + 1 == size ? 0 : at + 1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        t2 = fmaxf(t2, fminf(t1, x[u]));
+                        t1 = fmaxf(t1, x[u]);
+                    }
                 }
             }
             const float mine = a.best == 2 && t2 != -INFINITY ? t1 + t2 : t1;
             // what the rounding of its sum is relative to
             const float size_of = (t1 == -INFINITY ? 0.0f : fabsf(t1)) + (t2 == -INFINITY ? 0.0f : fabsf(t2));
             int before = 0;
-            for (int g = 0; g < a.groups; ++g) {
+#pragma unroll
+            for (int g = 0; g < kMaxGroups; ++g) {
                 const float o = __shfl(mine, base + g);
-                before += o > mine || (o == mine && g < j);
+                before += g < a.groups && (o > mine || (o == mine && g < j));
             }
             const bool in = j < a.groups && before < a.keep;
             // the least of the kept must be clearly above the largest of the others
@@ -515,25 +549,27 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         }
 
         // ---- the eight largest keys, and the ninth
-        double list[kList], ninth = -kFar;
+        double list[kList], ninth = kAbsent;
         for (int e0 = 0; e0 < E; e0 += kList * L) {
             double v[kList];
             float l[kList], f[kList];
-            if (!GROUPS || !biased) logits(e0, l);
+            logits(e0, l);
             if (!biased) {
 #pragma unroll
-                for (int i = 0; i < kList; ++i) f[i] = number(l[i] + 0.0f, -FLT_MAX);  // -0 as 0
+                for (int i = 0; i < kList; ++i) f[i] = l[i] + 0.0f;  // -0 as 0
             } else if constexpr (GROUPS) {
 #pragma unroll
-                for (int i = 0; i < kList; ++i) f[i] = keys[min(e0 + L * i + j, E - 1)];
+                for (int i = 0; i < kList; ++i) f[i] = keys[FULL ? e0 + L * i + j : min(e0 + L * i + j, E - 1)];
             } else {
                 by_score(e0, l, f);
             }
 #pragma unroll
             for (int i = 0; i < kList; ++i) {
                 const int e = e0 + L * i + j;
-                const bool in = e < E && (!GROUPS || (kept >> ((((uint32_t)e * recip) >> 20) & 31) & 1));
-                v[i] = pack_key(in ? f[i] : -INFINITY, e);
+                bool in = l[i] != -INFINITY;
+                if constexpr (GROUPS) in = in && f[i] != -INFINITY && (kept >> ((((uint32_t)e * recip) >> 20) & 31) & 1);
+                else if (biased) in = in && f[i] != -INFINITY;
+                v[i] = pack_key(f[i], e, in);
             }
             sort_list(v);
             if (e0 == 0) {
@@ -545,7 +581,7 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         }
         merge_lanes<L>(list, ninth, ninth_wanted);
         // lanes 0 .. 7 of the token: a candidate each, its logit, its score in 64 bits
-        double cand = -kFar;
+        double cand = kAbsent;
 #pragma unroll
         for (int i = 0; i < kList; ++i) cand = j == i ? list[i] : cand;
         int id = there(cand) ? expert_of(cand) : -1, rank = j;
@@ -569,12 +605,13 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         while (todo) {
             const int at = __ffsll((long long)todo) - 1;
             todo &= todo - 1;
-            const int r = choose_f64<DT>(a, t0 + at / L, __shfl(top, at), biased, lane);
+            const RouteArgs copy = a;  // in memory, where the call needs it; `a` itself stays in scalar registers
+            const int r = choose_f64<DT>(copy, t0 + at / L, __shfl(top, at), biased, lane);
             const int theirs = __shfl(r, j);
             if (base == at) id = j < k ? theirs : -1;
         }
         // Weights, in 64 bits.  Renormalised, a softmax needs no sum over all.
-        const float l = id >= 0 ? load_logit<DT>(a.logits, row + id) : -INFINITY;
+        const float l = id >= 0 ? load_logit<DT>(from, row + id * B) : -INFINITY;
         const float about = SOFT && a.renorm ? group_max<L>(l) : top;
         double s = 0;
         if (id >= 0) s = SOFT ? exp((double)l - (double)about) / (a.renorm ? 1.0 : (double)z) : sigmoid_f64(l);
@@ -614,7 +651,7 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         return;
     }
     // a single workgroup: its stores of ids have been made (the barrier waits for them)
-    for (int i = tid; i < kRouteWaves * 1025; i += kRouteThreads) (&sh.sort.wcnt[0][0])[i] = 0;
+    zero_counts<kRouteThreads>(sh.sort, E);
     exclusive_scan<kRouteThreads>(hist, sh.sort.fill, E, sh.sort.tmp);
     for (int i = tid; i <= E; i += kRouteThreads) a.o.offsets[i] = sh.sort.fill[i];
     place_pairs<kRouteThreads>(a.ids, 0, (int64_t)a.T * k, E, k, a.o, sh.sort);
@@ -751,10 +788,10 @@ hipError_t place(const Id *ids, int64_t P, int E, int k, const PairOrder &o, hip
 
 }  // namespace
 
-// At most 512 chunks of 64 tokens at least (a pass of a workgroup).
+// At most 512 chunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens.
 int32_t order_chunk(int64_t tokens) {
     const int64_t each = (tokens + 511) / 512;
-    return (int32_t)((each < 64 ? 64 : each) + 63) / 64 * 64;
+    return tokens <= 64 ? 64 : (int32_t)((each < 32 ? 32 : each) + 31) / 32 * 32;
 }
 
 hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
@@ -764,9 +801,10 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
         constexpr int DT = decltype(d)::value;
         auto pick = [&](auto soft) {
             constexpr bool SOFT = decltype(soft)::value;
-            if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT>, grid, block, s, a);
-            else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT>, grid, block, s, a);
-            else klaunch(route_kernel<DT, 64, true, SOFT>, grid, block, s, a);
+            if (a.groups == 1 && a.E % 64 == 0) klaunch(route_kernel<DT, 8, false, SOFT, true>, grid, block, s, a);
+            else if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT, false>, grid, block, s, a);
+            else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT, false>, grid, block, s, a);
+            else klaunch(route_kernel<DT, 64, true, SOFT, false>, grid, block, s, a);
         };
         if (a.score == kSoftmax) pick(std::true_type{});
         else pick(std::false_type{});

@@ -230,6 +230,8 @@ int moe_route(const moe_router *r, int32_t dtype, const void *logits, int64_t st
     if (order) MOE_TRY(check_order(order, tokens, pairs, r->n_experts, m, a.o));
     a.o.chunk = order_chunk(tokens);
     a.o.chunks = order_chunks(tokens);
+    // the kernel addresses the rows of a chunk with 31-bit offsets (no logits that fit the GPU come near)
+    if (a.o.chunk * stride > 0x7fffffff / dt_bytes(dtype)) return MOE_ERR_UNSUPPORTED;
     if (tokens == 0)  // no pairs: the offsets are zeros
         return order ? status_of(launch_sort_pairs(ids, false, 0, r->top_k, r->n_experts, a.o, (hipStream_t)stream))
                      : MOE_OK;
