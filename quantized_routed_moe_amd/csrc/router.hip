@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
 constexpr int kSortThreads = 1024;
+constexpr int kMaxChunks = 512;  // of the pairs' order
 
 __device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
@@ -325,21 +326,25 @@ __device__ __forceinline__ void place_pairs(const Id *ids, int64_t p0, int64_t p
 // chunk into their totals.  A workgroup takes 32 buckets, 32 threads for the rows of each.
 __global__ __launch_bounds__(kSortThreads) void scan_kernel(int E, PairOrder o) {
     __shared__ int part[32][33];
+    constexpr int kEach = kMaxChunks / 32;
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5, buckets = E + 1, b = blockIdx.x * 32 + c;
-    const int each = (o.chunks + 31) / 32, r0 = min(g * each, o.chunks), r1 = min(r0 + each, o.chunks);
-    int sum = 0;
-    if (b < buckets)
-        for (int r = r0; r < r1; ++r) sum += o.hist[(int64_t)r * buckets + b];
+    const int each = (o.chunks + 31) / 32, r0 = g * each;
+    auto mine = [&](int i) { return i < each && r0 + i < o.chunks && b < buckets; };
+    int v[kEach], sum = 0;  // all on their way at once
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = mine(i) ? o.hist[(int64_t)(r0 + i) * buckets + b] : 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += v[i];
     part[g][c] = sum;
     __syncthreads();
     int at = 0;
-    for (int i = 0; i < g; ++i) at += part[i][c];
-    if (b >= buckets) return;
-    if (g == 31) o.hist[(int64_t)o.chunks * buckets + b] = at + sum;
-    for (int r = r0; r < r1; ++r) {
-        const int v = o.hist[(int64_t)r * buckets + b];
-        o.hist[(int64_t)r * buckets + b] = at;
-        at += v;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) at += i < g ? part[i][c] : 0;
+    if (g == 31 && b < buckets) o.hist[(int64_t)o.chunks * buckets + b] = at + sum;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (mine(i)) o.hist[(int64_t)(r0 + i) * buckets + b] = at;
+        at += v[i];
     }
 }
 
@@ -407,7 +412,7 @@ constexpr int kGroupKeys = 1024;  // keys that a wave keeps in LDS to choose gro
 
 // FULL: the experts fill whole accesses of the lanes.
 template <int DT, int L, bool GROUPS, bool SOFT, bool FULL>
-__global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
     constexpr int TW = 64 / L, TB = TW * kRouteWaves;  // tokens of a wave, of a workgroup's pass
     // keys of a wave's tokens by expert; afterwards, in a single workgroup, the order of the pairs
     __shared__ union Shared {
@@ -497,9 +502,7 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         };
 
         bool unsure = false;
-        uint32_t kept = 0;
         const int size = GROUPS ? E / a.groups : 1;
-        const uint32_t recip = ((1u << 20) + size - 1) / size;  // e / size for e < 1024
         float *const keys = GROUPS ? sh.keys[wave] + (lane / L) * (kGroupKeys / TW) : nullptr;
         if constexpr (GROUPS) {
             wave_sync();  // the tokens before are done with the keys
@@ -517,6 +520,7 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
             float t1 = -INFINITY, t2 = -INFINITY;
             if (j < a.groups) {
                 int at = j % size;
+#pragma unroll 1
                 for (int n = 0; n < size; n += 8) {
                     float x[8];
 #pragma unroll
@@ -532,20 +536,61 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
                 }
             }
             const float mine = a.best == 2 && t2 != -INFINITY ? t1 + t2 : t1;
-            // what the rounding of its sum is relative to
+            // what its roundings are relative to: three of 2^-24 at most
             const float size_of = (t1 == -INFINITY ? 0.0f : fabsf(t1)) + (t2 == -INFINITY ? 0.0f : fabsf(t2));
             int before = 0;
-#pragma unroll
-            for (int g = 0; g < kMaxGroups; ++g) {
+#pragma unroll 1
+            for (int g = 0; g < a.groups; ++g) {
                 const float o = __shfl(mine, base + g);
-                before += g < a.groups && (o > mine || (o == mine && g < j));
+                before += o > mine || (o == mine && g < j);
             }
-            const bool in = j < a.groups && before < a.keep;
+            bool in = j < a.groups && before < a.keep;
             // the least of the kept must be clearly above the largest of the others
             const float least = -group_max<L>(in ? -mine : -INFINITY);
             const float most = group_max<L>(!in && j < a.groups ? mine : -INFINITY);
-            if (most != -INFINITY) unsure = !(least - most > 4 * slack + 0x1p-20f * group_max<L>(size_of));
-            kept = (uint32_t)(__ballot(in) >> base) & 0xffffu;
+            if (most != -INFINITY) unsure = !(least - most > 4 * slack + 0x1p-21f * group_max<L>(size_of));
+            // Where it is not, the groups' best experts are scored in 64 bits (not with a softmax's sum and a bias: that
+            // sum is in fp32).  They have to be the best beyond doubt, else choose_f64 decides.
+            if ((!SOFT || !biased) && __ballot(unsure) != 0) {
+                // the best two by key (the third may be too near to tell), or without a bias by logit, which is exact
+                int i1 = 0, i2 = 0;
+                float b1 = -INFINITY, b2 = -INFINITY, t3 = -INFINITY;
+                if (j < a.groups) {
+#pragma unroll 1
+                    for (int n = 0; n < size; ++n) {
+                        float x = keys[j * size + n];
+                        if (!biased && x != -INFINITY) x = load_logit<DT>(from, row + (j * size + n) * B);
+                        t3 = fmaxf(t3, x > b2 ? b2 : x);
+                        if (x > b1) b2 = b1, i2 = i1, b1 = x, i1 = n;
+                        else if (x > b2) b2 = x, i2 = n;
+                    }
+                }
+                auto exactly = [&](int n) -> double {
+                    const double l = load_logit<DT>(from, row + (j * size + n) * B);
+                    return (SOFT ? exp(l - (double)top) : sigmoid_f64(l)) + load_logit<kDtF32>(bias_from, (j * size + n) * 4);
+                };
+                const bool two = a.best == 2 && t2 != -INFINITY;
+                double score = -INFINITY;
+                if (j < a.groups && t1 > -FLT_MAX) score = exactly(i1);
+                if (j < a.groups && two && t2 > -FLT_MAX) score += exactly(i2);
+                const float last = a.best == 2 ? t2 : t1, next = a.best == 2 ? t3 : t2;
+                const bool clear = !biased || next == -INFINITY ||
+                                   last - next > 2 * slack + 0x1p-23f * fmaxf(fabsf(last), fabsf(next));
+                // (a NaN among a group's best counts as the least number: left to choose_f64)
+                const bool vague = j < a.groups && (!clear || t1 == -FLT_MAX || (two && t2 == -FLT_MAX));
+                before = 0;
+#pragma unroll 1
+                for (int g = 0; g < a.groups; ++g) {
+                    const double o = __shfl(score, base + g);
+                    before += o > score || (o == score && g < j);
+                }
+                in = j < a.groups && before < a.keep;
+                unsure = unsure && ((__ballot(vague) >> base) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) != 0;
+            }
+            wave_sync();
+            if (j < a.groups && !in)
+                for (int n = 0; n < size; ++n) keys[j * size + n] = -INFINITY;
+            wave_sync();
         }
 
         // ---- the eight largest keys, and the ninth
@@ -553,23 +598,28 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         for (int e0 = 0; e0 < E; e0 += kList * L) {
             double v[kList];
             float l[kList], f[kList];
-            logits(e0, l);
-            if (!biased) {
+            if constexpr (GROUPS) {  // keys of groups that are out have become -inf
 #pragma unroll
-                for (int i = 0; i < kList; ++i) f[i] = l[i] + 0.0f;  // -0 as 0
-            } else if constexpr (GROUPS) {
+                for (int i = 0; i < kList; ++i) f[i] = e0 + L * i + j < E ? keys[e0 + L * i + j] : -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kList; ++i) f[i] = keys[FULL ? e0 + L * i + j : min(e0 + L * i + j, E - 1)];
+                for (int i = 0; i < kList; ++i) v[i] = pack_key(f[i], e0 + L * i + j, f[i] != -INFINITY);
+                if (!biased) {
+                    logits(e0, l);
+#pragma unroll
+                    for (int i = 0; i < kList; ++i)
+                        v[i] = pack_key(l[i] + 0.0f, e0 + L * i + j, f[i] != -INFINITY && l[i] != -INFINITY);
+                }
             } else {
-                by_score(e0, l, f);
-            }
+                logits(e0, l);
+                if (biased) {
+                    by_score(e0, l, f);
 #pragma unroll
-            for (int i = 0; i < kList; ++i) {
-                const int e = e0 + L * i + j;
-                bool in = l[i] != -INFINITY;
-                if constexpr (GROUPS) in = in && f[i] != -INFINITY && (kept >> ((((uint32_t)e * recip) >> 20) & 31) & 1);
-                else if (biased) in = in && f[i] != -INFINITY;
-                v[i] = pack_key(f[i], e, in);
+                    for (int i = 0; i < kList; ++i)
+                        v[i] = pack_key(f[i], e0 + L * i + j, l[i] != -INFINITY && f[i] != -INFINITY);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kList; ++i) v[i] = pack_key(l[i] + 0.0f, e0 + L * i + j, l[i] != -INFINITY);  // -0 as 0
+                }
             }
             sort_list(v);
             if (e0 == 0) {
@@ -618,7 +668,7 @@ __global__ __launch_bounds__(kRouteThreads, GROUPS ? 3 : 4) void route_kernel(Ro
         if (!SOFT && biased) {  // rank by the keys in 64 bits (a token that choose_f64 has ranked stays as it is)
             const double key = id < 0 ? -INFINITY : number(s + (double)a.bias[id], -DBL_MAX);
             int before = 0;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < kList; ++i) {
                 const double o = __shfl(key, base + i);
                 const int other = __shfl(id, base + i);
@@ -788,9 +838,9 @@ hipError_t place(const Id *ids, int64_t P, int E, int k, const PairOrder &o, hip
 
 }  // namespace
 
-// At most 512 chunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens.
+// At most kMaxChunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens.
 int32_t order_chunk(int64_t tokens) {
-    const int64_t each = (tokens + 511) / 512;
+    const int64_t each = (tokens + kMaxChunks - 1) / kMaxChunks;
     return tokens <= 64 ? 64 : (int32_t)((each < 32 ? 32 : each) + 31) / 32 * 32;
 }
 
