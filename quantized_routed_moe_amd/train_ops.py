@@ -44,12 +44,15 @@ def _router(n_experts, top_k, score, renormalize, scale, bias=None, groups=1, ke
 
 
 def _order(tokens, top_k, n_experts, like, stream):
-    """New arrays for a pairs' order and the C struct that names them."""
-    perm, place = (_new(like, (tokens * top_k,), torch.int64, stream) for _ in range(2))
-    rows = _new(like, (tokens * top_k,), torch.int32, stream)
-    offsets = _new(like, (n_experts + 1,), torch.int32, stream)
+    """New arrays for a pairs' order (perm, offsets, rows, place), its workspace and the C struct that names them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _order(tokens, top_k, n_experts, like, None)
+    new, pairs = like.new_empty, (tokens * top_k,)
+    perm, place, rows = new(pairs, dtype=torch.int64), new(pairs, dtype=torch.int64), new(pairs, dtype=torch.int32)
+    offsets = new((n_experts + 1,), dtype=torch.int32)
     n = _lib.moe_pair_order_bytes(tokens, n_experts)
-    work = _new(like, (n,), torch.uint8, stream) if n else None
+    work = new((n,), dtype=torch.uint8) if n else None
     return (perm, offsets, rows, place), work, PairOrder(perm.data_ptr(), place.data_ptr(), rows.data_ptr(),
                                                          offsets.data_ptr(), work.data_ptr() if n else None, n)
 
@@ -65,10 +68,10 @@ def _route(call, logits, top_k, score, bias, groups, keep_groups, group_best, re
         _layout(bias, "bias", torch.float32, (E,))
         at = _plain(bias, "bias", index)
     r = _router(E, top_k, score, renormalize, scale, at, groups, keep_groups, group_best)
-    k = max(int(top_k), 0)
+    k = top_k if 0 < top_k <= E else 0  # else the call below refuses
     ids, w = _new(logits, (T, k), torch.int32, side), _new(logits, (T, k), torch.float32, side)
     order = work = struct = None
-    if ordered and T * k <= MAX_PAIRS and 1 <= E <= MAX_EXPERTS:  # else the call below refuses
+    if ordered and T * k <= MAX_PAIRS and 1 <= E <= MAX_EXPERTS:
         order, work, struct = _order(T, k, E, logits, side)
     _check(_lib.moe_route(ctypes.byref(r), DT[logits.dtype], logits.data_ptr(), ld, T, ids.data_ptr(), w.data_ptr(),
                           None if struct is None else ctypes.byref(struct), raw), call)
@@ -173,19 +176,23 @@ def combine(y, place, w=None, out=None, dtype=torch.float32, stream=None):
 
 
 def _combine_grad(dout, y, place, w, pairs, dtype, dy, dw, stream):
-    """The C call on checked outputs (None: not wanted); y is looked at for dw only."""
-    ldd = _matrix(dout, "dout", dout.dtype, place.shape[0], dout.shape[-1])
+    """The C call (dy, dw: outputs, None where not wanted); y is looked at for dw only."""
     T, k = _pairs_of(place, w)
+    ldd = _matrix(dout, "dout", dout.dtype, T, dout.shape[-1])
     n = dout.shape[1]
     index, raw, side = _target(dout, "dout", stream)
-    ldy = 0 if y is None else _matrix(y, "y", dtype, pairs, n)
-    ldg = 0 if dy is None else _matrix(dy, "dy", dtype, pairs, n)
-    _layout(dw, "dw", torch.float32, (T, k))
-    _check(_lib.moe_combine_grad(DT[dtype], _pointer(dout, "dout", index), DT[dout.dtype], ldd,
-                                 None if y is None else _pointer(y, "y", index), ldy, pairs,
-                                 _plain(place, "place", index), None if w is None else _plain(w, "w", index), T, k, n,
-                                 None if dy is None else _pointer(dy, "dy", index), ldg,
-                                 None if dw is None else _plain(dw, "dw", index), raw), "moe_combine_grad")
+    ldy = ldg = 0
+    py = pw = pdy = pdw = None
+    if dw is not None:
+        ldy, py = _matrix(y, "y", dtype, pairs, n), _pointer(y, "y", index)
+        _layout(dw, "dw", torch.float32, (T, k))
+        pdw = _plain(dw, "dw", index)
+    if dy is not None:
+        ldg, pdy = _matrix(dy, "dy", dtype, pairs, n), _pointer(dy, "dy", index)
+    if w is not None:
+        pw = _plain(w, "w", index)
+    _check(_lib.moe_combine_grad(DT[dtype], _pointer(dout, "dout", index), DT[dout.dtype], ldd, py, ldy, pairs,
+                                 _plain(place, "place", index), pw, T, k, n, pdy, ldg, pdw, raw), "moe_combine_grad")
     _hold(side, dout, y, place, w, dy, dw)
 
 
@@ -198,22 +205,23 @@ def combine_grad(dout, y, place, w=None, dy=None, dw=None, stream=None):
     _dtype(dout, "dout", (y.dtype, torch.float32))
     if y.dim() != 2 or dout.dim() != 2 or dout.shape[1] != y.shape[1]:
         raise ValueError(f"y and dout: expected [pairs, n] and [tokens, n], got {tuple(y.shape)}, {tuple(dout.shape)}")
-    T, k = _pairs_of(place, w)
-    _, _, side = _target(y, "y", stream)
+    if place.dim() != 2:
+        raise ValueError(f"place: expected [tokens, k], got {tuple(place.shape)}")
+    P, shape = y.shape[0], tuple(place.shape)
     operands = (dout, y) if w is None else (dout, y, w)
-    given = tuple(t for t in (dy, dw) if t is not None)
     graph = None
-    for t in given or (None,):
-        graph = _graph("combine_grad", t, *operands, instead="use Routing.combine")
-    P = y.shape[0]
+    for t in {None} if dy is None and dw is None else (dy, dw):
+        graph = _graph("combine_grad", t, *operands, instead="use Routing.combine") or graph
+    given = dy, dw
     if dy is None:
-        if P != T * k:
-            raise ValueError(f"place: names {T * k} of {P} rows of y (pass dy to leave rows out)")
-        dy = _new(y, tuple(y.shape), y.dtype, side)
+        if P != shape[0] * shape[1]:
+            raise ValueError(f"place: names {shape[0] * shape[1]} of {P} rows of y (pass dy to leave rows out)")
+        dy = _new(y, tuple(y.shape), y.dtype, stream)
     if dw is None:
-        dw = _new(y, (T, k), torch.float32, side)
+        dw = _new(y, shape, torch.float32, stream)
     _combine_grad(dout, y, place, w, P, y.dtype, dy, dw, stream)
-    _written(*given)
+    if given != (None, None):
+        _written(*given)
     if graph is None:
         return dy, dw
     return tuple(_Refusal.apply(graph, t, *operands) for t in (dy, dw))
