@@ -54,13 +54,14 @@ struct OrthogonalArgs {
     void *out;
     uint8_t *work;
     int32_t batch, rows, cols, steps;
+    int32_t run;  // steps that are taken on A before X is formed anew
     float eps;
     OrthogonalStep step[kMaxOrthogonalSteps + 1];  // the last: X only
 };
 // X is m x n, m <= n; strides in bytes.
 struct OrthogonalSizes {
     int32_t m, n, parts;
-    bool gram;  // steps are taken on A, which is enough smaller than X
+    bool gram;  // steps may be taken on A: it is enough smaller than X
     int64_t x_ld, a_ld, x_mat, a_mat;
 };
 
@@ -73,10 +74,6 @@ hipError_t launch_sort_pairs(const void *ids, bool wide, int64_t tokens, int32_t
 hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStream_t s);
 OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols);
 int64_t orthogonal_bytes(const OrthogonalSizes &z, int64_t batch);  // of the workspace of a pass
-// Steps whose P are multiplied with each other before they meet X.  Their A follow from the first one's, which
-// squares what an error is multiplied by in every step: three steps in a row add less than the rest
-// (relative errors of 5 steps on 384 x 384 in one / three and two / one by one: 8.6e-6 / 5.0e-7 / 4.8e-7).
-constexpr int kOrthogonalRun = 3;
 hipError_t launch_orthogonal(int dt, const OrthogonalArgs &a, hipStream_t s);
 hipError_t launch_combine_grad(int dt, int dout_dt, const CombineArgs &a, hipStream_t s);
 

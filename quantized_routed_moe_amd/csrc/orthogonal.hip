@@ -763,7 +763,7 @@ hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
     };
     int now = 0;  // which X
     for (int k = 0; k < o.steps;) {
-        const int end = z.gram ? std::min(k + kOrthogonalRun, (int)o.steps) : k + 1;
+        const int end = std::min(k + o.run, o.steps);
         const Held X{w.x[now], o.step[k].x}, next{w.x[now ^ 1], o.step[end].x};
         uint8_t *A = w.m[0], *P = w.m[1], *Q = nullptr, *spare[3] = {w.m[2], w.m[3], w.m[4]};
         int q_scale = 0;
