@@ -46,7 +46,8 @@ struct CombineArgs {
 // One step's coefficients and the powers of two by which its split matrices are scaled.
 struct OrthogonalStep {
     float c0, c1, c2;
-    int32_t x, a, p, pa, q;  // of X, A, P, P A and the product of the steps' P so far
+    int32_t x, a, p, pa, q;  // of X, A, P, P A and the product of the run's P so far
+    bool anew;               // X is formed before this step: a new run of steps on A begins
 };
 constexpr int kMaxOrthogonalSteps = 32, kMaxOrthogonal = 16384;  // steps; the shorter side
 struct OrthogonalArgs {
@@ -54,7 +55,6 @@ struct OrthogonalArgs {
     void *out;
     uint8_t *work;
     int32_t batch, rows, cols, steps;
-    int32_t run;  // steps that are taken on A before X is formed anew
     float eps;
     OrthogonalStep step[kMaxOrthogonalSteps + 1];  // the last: X only
 };

@@ -95,8 +95,8 @@ struct Tile {
 };
 
 // XL, YL: whether the operand has a lo part.
-template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int PER_CU, int RING>  // RING: stages of the LDS ring
-__global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split_gemm_kernel(GemmArgs a) {
+template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int RING>  // RING: stages of the LDS ring
+__global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void split_gemm_kernel(GemmArgs a) {
     constexpr bool YCOL = MODE == kApply, TRI = !YCOL;
     constexpr int NW = WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int XB = BM * kChunk, YB = BN * kChunk, STAGE = XB + YB;
@@ -113,17 +113,17 @@ __global__ __launch_bounds__(WM *WN * 64, (WM * WN * PER_CU + 3) / 4) void split
     // ---- the list of tiles: lower triangle row by row, or eight row tiles advancing through the columns together.
     // First whole tiles, as many for every workgroup; what is left over is cut along the contraction into as many
     // parts as there are workgroups for (each XCD takes the same part of neighbouring tiles).
-    constexpr int kSlots = kCus * PER_CU, kRun = kSlots / kXcds;
+    constexpr int kRun = kCus / kXcds;
     const int each = TRI ? a.m_tiles * (a.m_tiles + 1) / 2 : a.m_tiles * a.n_tiles;
     auto find = [&](int turn, Tile &t) -> bool {
         int at;
         t = Tile{0, 0, 0, 0, a.steps, 0, -1};
         if (turn < a.rounds) {
-            at = xcd_tile(blockIdx.x + turn * kSlots, kRun);
+            at = xcd_tile(blockIdx.x + turn * kCus, kRun);
         } else {
             const int p = (blockIdx.x % kXcds) * kRun + blockIdx.x / kXcds;
             if (turn > a.rounds || p >= a.tail * a.parts) return false;
-            at = a.rounds * kSlots + p % a.tail;
+            at = a.rounds * kCus + p % a.tail;
             t.part = p / a.tail;
             t.slot = a.parts > 1 ? p % a.tail : -1;
             t.k = t.part * a.steps / a.parts;
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const void *g, int64_t n
     __shared__ double part[kThreads / 64];
     const int tid = threadIdx.x;
     if (blockIdx.x == 0)
-        for (int i = tid; i < 2 * kCus; i += kThreads) arrived[i] = 0;
+        for (int i = tid; i < kCus; i += kThreads) arrived[i] = 0;
     const int64_t b = blockIdx.x / parts, p = blockIdx.x % parts;
     const int64_t per = ((n + parts - 1) / parts + 7) / 8 * 8, lo = p * per, hi = min(n, lo + per);
     const int64_t base = b * n;
@@ -607,26 +607,36 @@ inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // The tiles of a product: squares of `side`, which of them are whole and how the rest are cut.
 struct Cut {
     int side, m_tiles, n_tiles, rounds, tail, parts;
+    double cost;
     int64_t bytes() const { return parts > 1 ? (int64_t)tail * parts * side * side * 4 : 0; }
 };
-constexpr int kLeastSteps = 4;  // of a part
+// The side and the number of parts that cost least by what was measured, in steps of a 128x128 tile (0.78 us): a step
+// of a tile, its end (sums to hi and lo, stores, the mirrored tile), each part of one that is joined.  Of 256 x 256 a
+// step costs 3.1, not 4: half the copies and LDS reads for an element.  But with few tiles CUs stay idle, and joining
+// parts is slow, as one workgroup reads them all.  A symmetric product in tiles of 256 / 128: 1 x 2048 x 2048 95 / 56
+// us, 8 x 1536 x 1536 130 / 109, 16 x 2048 x 2048 430 / 445; P X of 1 x 4096 x 4096 318 / 398.
 Cut cut_of(int mode, int64_t batch, int rows, int cols, int steps) {
-    auto of = [&](int side, int slots) {
+    auto of = [&](int side, double step, double end, double join) {
         Cut c;
         c.side = side;
         c.m_tiles = ceil_div(rows, side);
         c.n_tiles = ceil_div(cols, side);
         const int64_t tiles = batch * (mode == kApply ? (int64_t)c.m_tiles * c.n_tiles
                                                       : (int64_t)c.m_tiles * (c.m_tiles + 1) / 2);
-        c.rounds = (int)(tiles / slots);
-        c.tail = (int)(tiles - (int64_t)c.rounds * slots);
-        c.parts = c.tail > 0 ? std::max(1, std::min(slots / c.tail, steps / kLeastSteps)) : 1;
+        c.rounds = (int)(tiles / kCus);
+        c.tail = (int)(tiles - (int64_t)c.rounds * kCus);
+        c.parts = 1;
+        c.cost = c.rounds * (steps * step + end);
+        if (c.tail > 0) {
+            auto cut = [&](int p) { return step * ceil_div(steps, p) + end + (p > 1 ? p * join : 0); };
+            for (int p = 2; p <= std::min(kCus / c.tail, steps); ++p)
+                if (cut(p) < cut(c.parts)) c.parts = p;
+            c.cost += cut(c.parts);
+        }
         return c;
     };
-    const Cut big = of(256, kCus), small = of(128, kCus);
-    const int64_t area_big = (big.rounds * kCus + big.tail) * (int64_t)65536,
-                  area_small = (small.rounds * kCus + small.tail) * (int64_t)16384;
-    return area_big <= area_small + area_small / 10 ? big : small;
+    const Cut big = of(256, 3.1, 12, 11), small = of(128, 1, 5, 2.7);
+    return big.cost <= small.cost ? big : small;
 }
 
 template <int MODE, bool XL, bool YL>
@@ -637,8 +647,8 @@ hipError_t launch_product(GemmArgs a, hipStream_t s) {
     a.rounds = c.rounds;
     a.tail = c.tail;
     a.parts = c.parts;
-    if (c.side == 256) klaunch(split_gemm_kernel<MODE, XL, YL, 256, 256, 2, 4, 1, 2>, dim3(kCus), dim3(512), s, a);
-    else klaunch(split_gemm_kernel<MODE, XL, YL, 128, 128, 2, 2, 1, 4>, dim3(kCus), dim3(256), s, a);
+    if (c.side == 256) klaunch(split_gemm_kernel<MODE, XL, YL, 256, 256, 2, 4, 2>, dim3(kCus), dim3(512), s, a);
+    else klaunch(split_gemm_kernel<MODE, XL, YL, 128, 128, 2, 2, 4>, dim3(kCus), dim3(256), s, a);
     return hipGetLastError();
 }
 
@@ -666,7 +676,7 @@ struct Layout {
         partial = (float *)take(most);
         sums = (double *)take(8 * batch * z.parts);
         rest = (float *)take(4 * batch);
-        arrived = (int32_t *)take(4 * 2 * kCus);
+        arrived = (int32_t *)take(4 * kCus);
         bytes = at - begin;
     }
 };
@@ -681,6 +691,9 @@ OrthogonalSizes orthogonal_sizes(int64_t rows, int64_t cols) {
     z.a_ld = (int64_t)ceil_div(z.m, 32) * kChunk;
     z.x_mat = z.m * z.x_ld;
     z.a_mat = z.m * z.a_ld;
+    // A step on A alone is three or four products of m x m x m in place of m x m x n and m x n x m.  16-bit, on X / on A:
+    // 16 x 1024 x 1152 1492 / 1561 us, x 1280 1602 / 1582, x 1536 1746 / 1639, x 2048 1962 / 1710; 4 x 2048 x 2304 3008
+    // / 3159, x 3584 3738 / 3428.
     z.gram = 4 * (int64_t)z.n >= 5 * (int64_t)z.m;
     const int64_t want = rows * cols / 32768;  // elements a workgroup sums
     z.parts = (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want);
@@ -763,7 +776,8 @@ hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
     };
     int now = 0;  // which X
     for (int k = 0; k < o.steps;) {
-        const int end = std::min(k + o.run, o.steps);
+        int end = k + 1;
+        while (!o.step[end].anew) ++end;
         const Held X{w.x[now], o.step[k].x}, next{w.x[now ^ 1], o.step[end].x};
         uint8_t *A = w.m[0], *P = w.m[1], *Q = nullptr, *spare[3] = {w.m[2], w.m[3], w.m[4]};
         int q_scale = 0;

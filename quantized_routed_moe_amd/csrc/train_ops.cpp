@@ -138,29 +138,33 @@ double largest(const float *c, double u, bool odd) {
 // The power of two that takes values of at most `most` to 2^14 .. 2^15, half of what fp16 holds.
 int32_t scale_of(double most) { return most > 0 ? std::min(15, (int)std::floor(std::log2(32768.0 / most))) : 15; }
 
-// Steps that are taken on A alone, their P multiplied with each other, before X is formed anew.  A P A is a smaller
-// product than X X^T and P X, but what an error of A has beside the singular values that are still small grows by the
-// square of X's factor a step, so a run has to end while that is below the result's rounding.  40 shapes of 8 .. 4096, 5
-// steps of the quintic, relative norm of the error at runs of 1 / 2 / 3 / 5: at most 3e-6 / 1.1e-5 / 1.2e-5 / 5.6e-5
-// (fp32 operations: 3.7e-6; the rounding to fp16: 2.1e-4, to bf16: 1.7e-3).  16 x 4096 x 2048 bf16 in runs of 3 / 5:
-// 9.83 / 9.13 ms.
-int32_t orthogonal_run(int32_t dtype) { return dtype == MOE_DT_BF16 ? 5 : dtype == MOE_DT_F16 ? 3 : 1; }
-
 // Scales of every step from the largest singular values that can come up; past 64 the steps do not converge.  A P A is
 // A of the step after, and P A has singular values of at most the two steps' X multiplied.
-int plan_orthogonal(const float *c, int32_t steps, OrthogonalArgs &o) {
-    double u = 1, q = 1;
+//
+// Where a step on A alone is cheaper than one on X (gram), several are taken so, their P multiplied with each other,
+// before X is formed anew.  But A holds squares: what its 22 bits lose of singular values that are still small beside
+// the largest grows by P^2 a step, and is c1 / c0 of P's own value there.  A run ends before that passes an eighth of
+// the result's rounding: with the quintic after three steps for 16-bit results, after one for fp32.  Norm of the error
+// that runs of 1 / 3 / 5 add to the quintic's five steps: normal matrices 3e-6 / 1.2e-5 / 5.6e-5, one singular value of
+// 1 and 511 of 1e-4 4e-5 / 4e-5 / 9e-3 (the rounding of bf16: 1.7e-3, of fp16: 2e-4).  16 x 4096 x 2048 bf16: 12.2 /
+// 10.0 / 9.3 ms.
+int plan_orthogonal(const float *c, int32_t steps, int32_t dtype, bool gram, OrthogonalArgs &o) {
+    const double half_step = dtype == MOE_DT_F32 ? 0x1p-24 : dtype == MOE_DT_F16 ? 0x1p-11 : 0x1p-8;
+    double u = 1, q = 1, lost = 0;
     for (int32_t k = 0; k < steps; ++k) {
         OrthogonalStep &t = o.step[k];
         const float *f = c + 3 * k;
         if (!std::isfinite(f[0]) || !std::isfinite(f[1]) || !std::isfinite(f[2])) return MOE_ERR_INVALID_ARG;
         const double p = largest(f, u, false), next = largest(f, u, true) * 1.001;  // fp32's rounding is far below that
-        q = k % o.run == 0 ? p : q * p;
-        t = OrthogonalStep{f[0], f[1], f[2], scale_of(u), scale_of(u * u), scale_of(p), scale_of(u * next), scale_of(q)};
+        const bool anew = k == 0 || !gram || f[0] == 0 ||
+                          !(lost * std::fabs(f[1]) <= half_step / 8 * std::fabs(f[0]));
+        q = anew ? p : q * p;
+        lost = (anew ? 0x1p-22 : lost) * p * p;
+        t = OrthogonalStep{f[0], f[1], f[2], scale_of(u), scale_of(u * u), scale_of(p), scale_of(u * next), scale_of(q), anew};
         u = next;
         if (!(u <= 64)) return MOE_ERR_INVALID_ARG;
     }
-    o.step[steps] = OrthogonalStep{0, 0, 0, scale_of(u), 0, 0, 0, 0};
+    o.step[steps] = OrthogonalStep{0, 0, 0, scale_of(u), 0, 0, 0, 0, true};
     return MOE_OK;
 }
 
@@ -190,8 +194,8 @@ int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows,
     MOE_TRY(check_array(mg));
     MOE_TRY(check_array(mo));
     OrthogonalArgs o{};
-    o.run = orthogonal_sizes(rows, cols).gram ? orthogonal_run(dtype) : 1;
-    MOE_TRY(plan_orthogonal(coefficients, steps, o));
+    const OrthogonalSizes z = orthogonal_sizes(rows, cols);
+    MOE_TRY(plan_orthogonal(coefficients, steps, dtype, z.gram, o));
     if (g != out && overlap(mo, mg)) return MOE_ERR_INVALID_ARG;
     if (batch == 0) return MOE_OK;
     const size_t need = moe_orthogonalize_bytes(batch, rows, cols);
@@ -199,7 +203,7 @@ int moe_orthogonalize(int32_t dtype, const void *g, int64_t batch, int64_t rows,
     const Mat mw = array(workspace, (int64_t)need, 1);
     MOE_TRY(check_array(mw));
     if (overlap(mw, mg) || overlap(mw, mo)) return MOE_ERR_INVALID_ARG;
-    const int64_t pass = orthogonal_pass(orthogonal_sizes(rows, cols), batch);
+    const int64_t pass = orthogonal_pass(z, batch);
     o.work = (uint8_t *)workspace;
     o.rows = (int32_t)rows;
     o.cols = (int32_t)cols;
@@ -239,8 +243,8 @@ int moe_route(const moe_router *r, int32_t dtype, const void *logits, int64_t st
     if (order) MOE_TRY(check_order(order, tokens, pairs, r->n_experts, m, a.o));
     a.o.chunk = order_chunk(tokens);
     a.o.chunks = order_chunks(tokens);
-    // the kernel addresses the rows of a chunk with 31-bit offsets (no logits that fit the GPU come near)
-    if (a.o.chunk * stride > 0x7fffffff / dt_bytes(dtype)) return MOE_ERR_UNSUPPORTED;
+    // the kernel addresses the rows of a chunk with 31-bit offsets
+    if (std::min<int64_t>(a.o.chunk, tokens) * stride > 0x7fffffff / dt_bytes(dtype)) return MOE_ERR_UNSUPPORTED;
     if (tokens == 0)  // no pairs: the offsets are zeros
         return order ? status_of(launch_sort_pairs(ids, false, 0, r->top_k, r->n_experts, a.o, (hipStream_t)stream))
                      : MOE_OK;

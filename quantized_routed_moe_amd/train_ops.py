@@ -212,7 +212,7 @@ def combine_grad(dout, y, place, w=None, dy=None, dw=None, stream=None):
     graph = None
     for t in {None} if dy is None and dw is None else (dy, dw):
         graph = _graph("combine_grad", t, *operands, instead="use Routing.combine") or graph
-    given = dy, dw
+    given = [t for t in (dy, dw) if t is not None]
     if dy is None:
         if P != shape[0] * shape[1]:
             raise ValueError(f"place: names {shape[0] * shape[1]} of {P} rows of y (pass dy to leave rows out)")
@@ -220,8 +220,7 @@ def combine_grad(dout, y, place, w=None, dy=None, dw=None, stream=None):
     if dw is None:
         dw = _new(y, shape, torch.float32, stream)
     _combine_grad(dout, y, place, w, P, y.dtype, dy, dw, stream)
-    if given != (None, None):
-        _written(*given)
+    _written(*given)
     if graph is None:
         return dy, dw
     return tuple(_Refusal.apply(graph, t, *operands) for t in (dy, dw))

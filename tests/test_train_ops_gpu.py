@@ -574,6 +574,75 @@ def test_a_layer_from_logits_to_gradients(dtype):
         assert float((got.detach().cpu().to(FP64) - ref).norm() / ref.norm()) <= tol
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_training_step(dtype):
+    """Router, experts, their gradients and the banks' orthogonalised updates, with padding (tokens without experts) and
+    tokens that fewer experts than top_k are left to; then captured and replayed on new inputs."""
+    qr = _qr()
+    T, E, k, H, F = 50, 8, 3, 64, 40
+    g = gen(8)
+
+    def inputs():
+        lo = torch.randn(T, E, generator=g)
+        lo[:4] = -math.inf
+        lo[4:7, 1:] = -math.inf
+        return lo, torch.randn(T, H, generator=g).to(dtype)
+
+    lo, x = inputs()
+    gate_up = (torch.randn(E, 2 * F, H, generator=g) / H**0.5).to(dtype)
+    down = (torch.randn(E, H, F, generator=g) / F**0.5).to(dtype)
+    dout = torch.randn(T, H, generator=g)
+    statics = [t.cuda() for t in (lo, x, gate_up, down)]
+    d = dout.cuda()
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in statics]
+        r = qr.Routing.from_logits(leaves[0], k, "softmax", scale=1.5)
+        out = qr.expert_ffn(leaves[1], r, *leaves[2:])
+        grads = torch.autograd.grad(out, leaves, d)
+        return (r.ids, out.detach(), *grads, *(qr.orthogonalize(b) for b in grads[2:]))
+
+    ids, out, *grads, up_gu, up_d = (t.cpu() for t in step())
+    want_ids, _ = reference(lo, k, score="softmax")
+    assert torch.equal(ids, want_ids) and (ids[:4] == -1).all() and (ids[4:7, 1:] == -1).all()
+    leaves = [t.to(FP64).requires_grad_() for t in (lo, x, gate_up, down)]
+    p = leaves[0].exp()
+    rows = []
+    for t in range(T):
+        mine = [int(e) for e in ids[t] if e >= 0]
+        acc = 0 * leaves[1][t]
+        for e in mine:
+            gu = leaves[2][e] @ leaves[1][t]
+            y = leaves[3][e] @ (torch.nn.functional.silu(gu[:F]) * gu[F:])
+            acc = acc + 1.5 * p[t, e] / sum(p[t, i] for i in mine) * y
+        rows.append(acc)
+    want = torch.stack(rows)
+    ref = torch.autograd.grad(want, leaves, dout.to(FP64))
+    assert (out[:4] == 0).all() and (grads[0][:7] == 0).all() and (grads[1][:4] == 0).all()
+    for a, b in zip((out, *grads), (want.detach(), *ref)):
+        assert float((a.to(FP64) - b).norm() / b.norm()) <= 8 * UNIT[dtype]
+    for update, grad in ((up_gu, grads[2]), (up_d, grads[3])):
+        for a, b in zip(update, newton_schulz(grad)):
+            assert float((a.to(FP64) - b).norm()) <= orthogonal_bound(b, dtype, depth=80)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        res = step()
+    for i in range(3):
+        for t, new in zip(statics, inputs()):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in res]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), i
+
+
 # ------------------------------------------------------ orthogonalised update
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -708,6 +777,45 @@ def test_orthogonalize_special_matrices():
     # fp32's own rounding of u v is the other directions' content, which grows 3.4445 a step in both alike; so does the
     # 2^-22 that the first products add to it: 3.4445^4 of it at most
     assert float((got - w).norm()) <= 141 * 2.0**-22 * 6 * float(w.norm())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rank,rest", [(1, 1e-2), (1, 1e-4), (4, 1e-3), (32, 1e-4), (0, 0.0)])
+def test_orthogonalize_few_directions(dtype, rank, rest):
+    """A few singular values far above the others (rank 0: 1 / k^2), as momenta have.  Six roundings of 2^-22 of the
+    first step's products put what the largest direction has into the others, which grow 3.4445 a step: 6 2^-22
+    3.4445^4 of the norm, as far as they go.  Where two further steps are taken on squares (16-bit results), what those
+    have lost grows by 3.4445^2 a step and goes through the derivative of P, at most 4.775: 6 2^-22 4.775 3.4445^4
+    more.  Then the output's rounding."""
+    m, n = 300, 520
+    g = gen(rank)
+    u = torch.linalg.qr(torch.randn(m, m, generator=g, dtype=FP64))[0]
+    v = torch.linalg.qr(torch.randn(n, m, generator=g, dtype=FP64))[0]
+    k = torch.arange(m, dtype=FP64)
+    x = ((u * (torch.where(k < rank, 1.0, rest) if rank else 1 / (k + 1) ** 2)) @ v.t()).to(dtype)
+    want = newton_schulz(x)
+    got = _qr().orthogonalize(x.cuda()).cpu().to(FP64)
+    grown = 6 * 2.0**-22 * 3.4445**4
+    tol = UNIT[dtype] + grown * (1 if dtype is FP32 else 1 + 4.775)
+    assert float((got - want).norm()) <= tol * float(want.norm())
+
+
+def test_orthogonalize_steep_steps():
+    """Steps that let small singular values grow faster, 6 and then 3.75 a step: as above, with what steps on squares lose
+    held to an eighth of the output's rounding each for the six."""
+    each = [(6.0, -14.0, 9.0)] + [(3.75, -3.418, 0.858)] * 4  # 1.6 at most
+    m, n = 200, 420
+    g = gen(12)
+    u = torch.linalg.qr(torch.randn(m, m, generator=g, dtype=FP64))[0]
+    v = torch.linalg.qr(torch.randn(n, m, generator=g, dtype=FP64))[0]
+    s = torch.full((m,), 1e-4, dtype=FP64)
+    s[0] = 1
+    for dtype in ALL:
+        x = ((u * s) @ v.t()).to(dtype)
+        want = newton_schulz(x, 5, each)
+        got = _qr().orthogonalize(x.cuda(), steps=5, coefficients=each).cpu().to(FP64)
+        tol = (1 + 6 / 8) * UNIT[dtype] + 6 * 2.0**-22 * 6 * 3.75**3
+        assert float((got - want).norm()) <= tol * float(want.norm()), dtype
 
 
 def test_orthogonalize_in_place_streams_and_graphs():
