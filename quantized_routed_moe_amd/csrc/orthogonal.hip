@@ -523,17 +523,17 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const void *g, int64_t n
 }
 
 // X split and scaled to 2^scale times g / 2^e, 2^e the power of two above the norm; rest: 2^e / norm.  A workgroup
-// takes 64 rows by 64 columns of X; where g is tall they are read transposed, through LDS.
+// takes 64 rows by 64 columns of X; where g is tall they are read transposed, through LDS.  wide: rows of g are whole
+// aligned runs of eight.  16-bit elements are fp16 numbers but for a power of two: they have no lo part, and what is
+// in its place is never multiplied.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void split_kernel(const void *g, int rows, int cols, bool tall, int parts,
+__global__ __launch_bounds__(kThreads) void split_kernel(const void *g, int rows, int cols, bool tall, bool wide, int parts,
                                                          const double *sums, float eps, int scale, uint8_t *x,
                                                          int64_t x_ld, int64_t x_mat, float *rest) {
     __shared__ float tile[64][65];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t b = blockIdx.z;
-    double s = 0;
-    for (int i = 0; i < parts; ++i) s += sums[b * parts + i];
-    const double norm = sqrt(s) + eps;
+    const double norm = sqrt(wave_sum_f64(lane < parts ? sums[b * parts + lane] : 0.0)) + eps;
     int e = 0;
     frexp(norm, &e);  // norm = f 2^e, f in [1/2, 1)
     const bool usual = norm > 0 && norm < INFINITY;
@@ -543,27 +543,48 @@ __global__ __launch_bounds__(kThreads) void split_kernel(const void *g, int rows
     const int m = tall ? cols : rows, n = tall ? rows : cols;  // of X
     const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
     const int64_t base = b * rows * cols;
-    const int c = tid & 63;
-    for (int r = tid >> 6; r < 64; r += kThreads / 64) {
-        // consecutive threads read consecutive elements of g
-        const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + c;
-        const float v = gr < rows && gc < cols ? ldexpf(element<DT>(g, base + (int64_t)gr * cols + gc), scale - e) : 0.0f;
-        if (tall) tile[c][r] = v;
-        else tile[r][c] = v;
-    }
-    __syncthreads();
-    for (int p = tid; p < 64 * 8; p += kThreads) {
-        const int r = p >> 3, u = p & 7;
-        const int row = m0 + r, col = n0 + 8 * u;
-        if (row >= m || col >= (n + 31) / 32 * 32) continue;
-        float v[8];
+    constexpr int kEach = 64 * 8 / kThreads;  // runs of eight of a thread
+    float v[kEach][8];
+    if (wide) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = tile[r][8 * u + i];
+        for (int i = 0; i < kEach; ++i) {
+            const int r = (i * kThreads + tid) >> 3, u = tid & 7, gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + 8 * u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0;
+            if (gr < rows && gc < cols) load8<DT>(g, base + (int64_t)gr * cols + gc, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] = ldexpf(v[i][j], scale - e);
+                if (tall) tile[8 * (tid & 7) + j][(i * kThreads + tid) >> 3] = v[i][j];
+            }
+    } else {
+        for (int r = tid >> 6; r < 64; r += kThreads / 64) {
+            // consecutive threads read consecutive elements of g
+            const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + lane;
+            const float f = gr < rows && gc < cols ? ldexpf(element<DT>(g, base + (int64_t)gr * cols + gc), scale - e) : 0.0f;
+            if (tall) tile[lane][r] = f;
+            else tile[r][lane] = f;
+        }
+    }
+    if (!wide || tall) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = tile[(i * kThreads + tid) >> 3][8 * (tid & 7) + j];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int row = m0 + ((i * kThreads + tid) >> 3), col = n0 + 8 * (tid & 7);
+        if (row >= m || col >= (n + 31) / 32 * 32) continue;
         f16x8 h, l;
-        split8(v, h, l);
+        split8(v[i], h, l);
         uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
         *reinterpret_cast<f16x8 *>(o) = h;
-        *reinterpret_cast<f16x8 *>(o + 64) = l;
+        if constexpr (DT == kDtF32) *reinterpret_cast<f16x8 *>(o + 64) = l;
     }
 }
 
@@ -574,31 +595,53 @@ __device__ __forceinline__ void put(void *p, int64_t at, float v) {
     else ((_Float16 *)p)[at] = (_Float16)v;
 }
 
-// The way back.
+// The way back.  wide: rows of out are whole aligned runs of eight.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void join_kernel(const uint8_t *x, int64_t x_ld, int64_t x_mat, int scale,
-                                                        int rows, int cols, bool tall, void *out) {
+                                                        int rows, int cols, bool tall, bool wide, void *out) {
     __shared__ float tile[64][65];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t b = blockIdx.z;
     const int m = tall ? cols : rows, n = tall ? rows : cols;
     const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
     const float back = ldexpf(1.0f, -scale);
-    for (int p = tid; p < 64 * 8; p += kThreads) {
-        const int r = p >> 3, u = p & 7;
-        const int row = m0 + r, col = n0 + 8 * u;
-        if (row >= m || col >= (n + 31) / 32 * 32) continue;
-        const uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
-        const f16x8 h = *reinterpret_cast<const f16x8 *>(o), l = *reinterpret_cast<const f16x8 *>(o + 64);
+    constexpr int kEach = 64 * 8 / kThreads;
+    float v[kEach][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tile[r][8 * u + i] = ((float)h[i] + (float)l[i]) * back;
+    for (int i = 0; i < kEach; ++i) {
+        const int row = m0 + ((i * kThreads + tid) >> 3), col = n0 + 8 * (tid & 7);
+        f16x8 h{}, l{};
+        if (row < m && col < (n + 31) / 32 * 32) {
+            const uint8_t *o = x + b * x_mat + row * x_ld + (col >> 5) * kChunk + (col & 31) * 2;
+            h = *reinterpret_cast<const f16x8 *>(o);
+            l = *reinterpret_cast<const f16x8 *>(o + 64);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = ((float)h[j] + (float)l[j]) * back;
     }
-    __syncthreads();
+    if (!wide || tall) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) tile[(i * kThreads + tid) >> 3][8 * (tid & 7) + j] = v[i][j];
+        __syncthreads();
+    }
     const int64_t base = b * rows * cols;
-    const int c = tid & 63;
-    for (int r = tid >> 6; r < 64; r += kThreads / 64) {
-        const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + c;
-        if (gr < rows && gc < cols) put<DT>(out, base + (int64_t)gr * cols + gc, tall ? tile[c][r] : tile[r][c]);
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int r = (i * kThreads + tid) >> 3, u = tid & 7, gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + 8 * u;
+            if (tall) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = tile[8 * u + j][r];
+            }
+            if (gr < rows && gc < cols) store8<DT>(out, base + (int64_t)gr * cols + gc, v[i]);
+        }
+    } else {
+        for (int r = tid >> 6; r < 64; r += kThreads / 64) {
+            const int gr = (tall ? n0 : m0) + r, gc = (tall ? m0 : n0) + lane;
+            if (gr < rows && gc < cols) put<DT>(out, base + (int64_t)gr * cols + gc, tall ? tile[lane][r] : tile[r][lane]);
+        }
     }
 }
 
@@ -706,11 +749,12 @@ hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
     const bool tall = o.rows > o.cols;
     const Layout w(o.work, z, o.batch);
     const dim3 block(kThreads), blocks64(ceil_div(z.n, 64), ceil_div(z.m, 64), o.batch);
+    auto wide = [&](const void *p) { return o.cols % 8 == 0 && (uintptr_t)p % 16 == 0; };
     auto in = [&](auto d) {
         constexpr int DT = decltype(d)::value;
         klaunch(norm_kernel<DT>, dim3(o.batch * z.parts), block, s, o.g, (int64_t)o.rows * o.cols, (int)z.parts, w.sums,
                 w.arrived);
-        klaunch(split_kernel<DT>, blocks64, block, s, o.g, (int)o.rows, (int)o.cols, tall, (int)z.parts,
+        klaunch(split_kernel<DT>, blocks64, block, s, o.g, (int)o.rows, (int)o.cols, tall, wide(o.g), (int)z.parts,
                 (const double *)w.sums, o.eps, (int)o.step[0].x, w.x[0], z.x_ld, z.x_mat, w.rest);
         return hipGetLastError();
     };
@@ -806,7 +850,7 @@ hipError_t launch_orthogonal(int dt, const OrthogonalArgs &o, hipStream_t s) {
     if (err != hipSuccess) return err;
     auto k = dt == kDtF32 ? join_kernel<kDtF32> : dt == kDtBf16 ? join_kernel<kDtBf16> : join_kernel<kDtF16>;
     klaunch(k, blocks64, block, s, (const uint8_t *)w.x[now], z.x_ld, z.x_mat, (int)o.step[o.steps].x, (int)o.rows,
-            (int)o.cols, tall, o.out);
+            (int)o.cols, tall, wide(o.out), o.out);
     return hipGetLastError();
 }
 
