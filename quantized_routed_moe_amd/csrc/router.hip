@@ -17,6 +17,16 @@
 // (the larger of one list's i-th and the other's (7 - i)-th are the eight best
 // of both) until all of them hold the token's.  The largest key that did not
 // make it is kept beside the list: it is the ninth.
+//
+// What bounds it: vector instructions, 1360 for a wave's eight tokens of 256
+// experts, half of them the network's (65536 tokens of fp32: 29 us, the vector
+// units busy 58% of it; reading the logits takes 14).  Eight lanes a token
+// rather than more, as each doubling of the lanes adds a merge.  Arguments stay
+// in scalar registers and logits come through buffer loads, whose addresses
+// cost one instruction (63 -> 46 us); two workgroups of 512 threads have to fit
+// a CU (128 registers), or the launch itself takes longer than the work
+// (8192 tokens of eight groups 44 -> 25 us).  One token: 7.5 us, a wave's
+// latency.  The order of many pairs is two launches behind it, 4 and 7 us.
 #include <cfloat>
 #include <type_traits>
 
@@ -245,7 +255,11 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
 
 // -------------------------------------------------------------- pair order
 // Stable counting sort: the pairs of each expert in each chunk of tokens are
-// counted, the counts summed over the chunks before, the pairs placed.
+// counted, the counts summed over the chunks before, the pairs placed.  Ranks
+// within a wave come from ballots on the bucket's bits, so that neither order
+// nor places depend on timing.  65536 tokens of six pairs: the router counts on
+// the way, the sums take 5 us, the placing 10 (a workgroup a chunk, three
+// barriers for 1024 pairs).
 template <int THREADS>
 struct SortShared {
     int fill[1025], wcnt[THREADS / 64][1025];
@@ -388,8 +402,9 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const Id *ids, int6
     place_pairs<kSortThreads>(ids, p0, p1, E, k, o, sh);
 }
 
-// The order of few pairs by comparing each with all; `few` has the pairs' buckets.
-constexpr int kFewPairs = 64;
+// The order of few pairs by comparing each with all; `few` has the pairs' buckets.  Router and order of 1 / 4 / 10 tokens of
+// six pairs so 6.1 / 6.6 / 8.1 us, by counting 7.2 / 7.2 / 7.4.
+constexpr int kFewPairs = 32;
 __device__ __forceinline__ void order_few(const int *few, int P, int E, int k, const PairOrder &o) {
     const int tid = threadIdx.x;
     for (int e = tid; e <= E; e += kRouteThreads) {
@@ -410,8 +425,7 @@ __device__ __forceinline__ void order_few(const int *few, int P, int E, int k, c
 // ------------------------------------------------------------------ router
 constexpr int kGroupKeys = 1024;  // keys that a wave keeps in LDS to choose groups: L = E / 16 lanes a token at least
 
-// FULL: the experts fill whole accesses of the lanes.
-template <int DT, int L, bool GROUPS, bool SOFT, bool FULL>
+template <int DT, int L, bool GROUPS, bool SOFT>
 __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
     constexpr int TW = 64 / L, TB = TW * kRouteWaves;  // tokens of a wave, of a workgroup's pass
     // keys of a wave's tokens by expert; afterwards, in a single workgroup, the order of the pairs
@@ -461,10 +475,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
         auto logits = [&](int e0, float (&l)[kList]) {
 #pragma unroll
             for (int i = 0; i < kList; ++i) l[i] = load_logit<DT>(from, row + (e0 + j) * B + L * i * B);
-            if constexpr (!FULL) {
 #pragma unroll
-                for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
-            }
+            for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
         };
 
         float top = 0, z = 1, rz = 1;
@@ -512,7 +524,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
                 by_score(e0, l, f);
 #pragma unroll
                 for (int i = 0; i < kList; ++i)
-                    if (FULL || e0 + L * i + j < E)
+                    if (e0 + L * i + j < E)
                         keys[e0 + L * i + j] = l[i] == -INFINITY ? -INFINITY : number(f[i], -FLT_MAX);
             }
             // lane g < groups: group g's score; lanes start at places of their own in it (banks)
@@ -714,7 +726,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
 // What it has to move is the gradient of every logit, and the logits where all of them have one (DENSE: softmax, not
 // renormalised); those are read once and their exponentials stay in registers.  L lanes a token, V consecutive experts
 // a lane and access.  What the chosen get passes through LDS, one after the other, so that an expert named twice gets
-// both.
+// both.  65536 tokens of 256 experts, bf16: DENSE 18.4 us (67 MB, 3.7 TB/s; the vector units are busy half the time,
+// with the exponentials and the chosen's 64-bit sums), else 12.3 (34 MB and the chosen logits).
 constexpr int kGradThreads = 256;
 template <int DT, int V>
 __device__ __forceinline__ void load_some(const void *p, int64_t at, float (&v)[V]) {
@@ -838,7 +851,9 @@ hipError_t place(const Id *ids, int64_t P, int E, int k, const PairOrder &o, hip
 
 }  // namespace
 
-// At most kMaxChunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens.
+// At most kMaxChunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens,
+// whose workgroup orders the pairs itself.  Router and order of 64 / 128 / 256 tokens of six pairs by one workgroup 8.8 /
+// 13.6 / 23.1 us, by several and two more launches 13.8 / 13.7 / 14.1.
 int32_t order_chunk(int64_t tokens) {
     const int64_t each = (tokens + kMaxChunks - 1) / kMaxChunks;
     return tokens <= 64 ? 64 : (int32_t)((each < 32 ? 32 : each) + 31) / 32 * 32;
@@ -851,10 +866,11 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
         constexpr int DT = decltype(d)::value;
         auto pick = [&](auto soft) {
             constexpr bool SOFT = decltype(soft)::value;
-            if (a.groups == 1 && a.E % 64 == 0) klaunch(route_kernel<DT, 8, false, SOFT, true>, grid, block, s, a);
-            else if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT, false>, grid, block, s, a);
-            else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT, false>, grid, block, s, a);
-            else klaunch(route_kernel<DT, 64, true, SOFT, false>, grid, block, s, a);
+            // groups are scored by a lane each, and a wave's keys have to fit its LDS: 16 lanes a token up to 256 experts
+            // (8192 x 256 bf16 13.4 us, with 64 lanes 34.4), 64 beyond
+            if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT>, grid, block, s, a);
+            else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT>, grid, block, s, a);
+            else klaunch(route_kernel<DT, 64, true, SOFT>, grid, block, s, a);
         };
         if (a.score == kSoftmax) pick(std::true_type{});
         else pick(std::false_type{});
@@ -870,6 +886,7 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
 hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
     const bool dense = a.score == kSoftmax && !a.renorm;
     const uintptr_t at = (uintptr_t)a.logits | (uintptr_t)a.dlogits;
+    // accesses of four elements: 65536 x 256 bf16 19.2 us against 21.4 (softmax), 12.3 against 13.5 (sigmoid); fp32 none
     const bool four = (a.E | a.ld | a.d_ld) % 4 == 0 && at % (dt == kDtF32 ? 16 : 8) == 0;
     auto go = [&](auto d_c, auto dense_c, auto v_c) {
         constexpr int DT = decltype(d_c)::value, V = decltype(v_c)::value;
@@ -878,6 +895,7 @@ hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
             const int64_t blocks = (a.T + tokens - 1) / tokens;
             klaunch(k, dim3((unsigned)(blocks > 4096 ? 4096 : blocks)), dim3(kGradThreads), s, a);
         };
+        // 65536 x 64 bf16 softmax with 4 / 16 experts a lane: 8.7 / 12.9 us; x 256 with 16 / 64 lanes a token: 18.4 / 48
         if (a.E <= 64) with(route_grad_kernel<DT, 16, 4, V, DENSE>, 16);
         else if (a.E <= 256) with(route_grad_kernel<DT, 16, 16, V, DENSE>, 16);
         else with(route_grad_kernel<DT, 64, 16, V, DENSE>, 4);
