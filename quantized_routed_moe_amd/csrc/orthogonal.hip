@@ -24,13 +24,13 @@
 // is left of it, a factor in (1, 2], goes into the first step's products.
 //
 // What bounds it: the matrix units.  16 x 4096 x 2048 bf16, five steps: 9.7 ms,
-// of which the products 9.3 at up to 1278 TFLOP/s (P X: 2048 tiles of 256 x 256
+// of which the products 9.3 at up to 1310 TFLOP/s (P X: 2048 tiles of 256 x 256
 // and 64 steps in 1255 us, the matrix units busy 74% at the clock that power
 // allows; a library product of random 16-bit matrices reaches 1110 to 1310).
 // The symmetric ones take 413 to 440 us for 288 steps of a CU, as 576 tiles
 // are 2.25 rounds.  Norm, split and join move 1.6 GB at 3.8 to 5.5 TB/s in 330
 // us.  The first step's products of 16-bit input have one part of X: 490 us
-// instead of 650 for X X^T, where the copies then set the pace.
+// instead of 750 for X X^T, where the copies then set the pace.
 #include <algorithm>
 #include <type_traits>
 
