@@ -21,6 +21,7 @@ from .expert_ops import (DT, _dtype, _graph, _hold, _matrix, _new, _output, _pla
 SCORES = {"sigmoid": 1, "softmax": 2}
 MAX_PAIRS = 1 << 20
 MAX_EXPERTS = 1024
+MAX_STEPS = 32
 _FLOATS = tuple(DT)
 
 
@@ -39,8 +40,10 @@ def _rows(t, name, cols=None):
 def _router(n_experts, top_k, score, renormalize, scale, bias=None, groups=1, keep_groups=None, group_best=2):
     if score not in SCORES:
         raise ValueError(f"score: expected one of {', '.join(SCORES)}, got {score!r}")
-    return Router(n_experts, top_k, SCORES[score], groups, groups if keep_groups is None else keep_groups, group_best,
-                  1 if renormalize else 0, scale, bias)
+    keep = groups if keep_groups is None else keep_groups
+    if (top_k | groups | keep | group_best) >> 31:  # would not be what the C call sees
+        raise ValueError(f"top_k, groups, keep_groups, group_best: got {top_k}, {groups}, {keep}, {group_best}")
+    return Router(n_experts, top_k, SCORES[score], groups, keep, group_best, 1 if renormalize else 0, scale, bias)
 
 
 def _order(tokens, top_k, n_experts, like, stream):
@@ -243,6 +246,8 @@ def orthogonalize(g, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, stream=N
         raise ValueError(f"g: expected [.., rows, cols], got {tuple(g.shape)}")
     rows, cols = g.shape[-2:]
     batch = g.numel() // (rows * cols)
+    if not 1 <= steps <= MAX_STEPS:
+        raise ValueError(f"steps: expected 1 to {MAX_STEPS}, got {steps}")
     each = [tuple(coefficients)] * steps if not hasattr(coefficients[0], "__len__") else [tuple(c) for c in coefficients]
     if len(each) != steps or any(len(c) != 3 for c in each):
         raise ValueError(f"coefficients: expected (a, b, c) or {steps} of them, got {coefficients!r}")

@@ -214,3 +214,13 @@ def test_combine_on_the_host_is_differentiable():
     assert torch.allclose(out, want)
     for a, b in zip(torch.autograd.grad(out.square().sum(), (w, y)), torch.autograd.grad(want.square().sum(), (w, y))):
         assert torch.allclose(a, b)
+
+
+def test_numbers_that_do_not_fit_are_refused():
+    from quantized_routed_moe_amd import train_ops
+    for bad in (dict(top_k=1 + (1 << 32)), dict(groups=1 + (1 << 32)), dict(keep_groups=1 << 40), dict(group_best=-1)):
+        with pytest.raises(ValueError):
+            train_ops._router(**{"n_experts": 8, "top_k": 2, "score": "sigmoid", "renormalize": True, "scale": 1.0, **bad})
+    for steps in (0, -1, 33, 5 + (1 << 32)):
+        with pytest.raises(ValueError, match="steps"):
+            qr.orthogonalize(torch.zeros(2, 3), steps=steps)

@@ -536,6 +536,39 @@ def test_nothing_to_do():
     assert (qr.combine(torch.empty(0, 8).cuda(), none, torch.rand(4, 3).cuda()) == 0).all()
 
 
+def test_largest_calls():
+    """As many pairs as there may be: of one expert a token and of eight, of four experts and of 1024."""
+    qr = _qr()
+    P = 1 << 20
+    for T, k, E, dtype in ((P, 1, 4, FP32), (P // 8, 8, 1024, BF16)):
+        g = torch.Generator(device="cuda").manual_seed(k)
+        x = torch.randn(T, E, generator=g, device="cuda").to(dtype)
+        r = qr.Routing.from_logits(x, k)
+        # equal logits: the lower expert first, as a stable sort has it
+        want = torch.cat([c.sort(dim=1, descending=True, stable=True).indices[:, :k] for c in x.split(1 << 14)])
+        assert torch.equal(r.ids.long(), want)
+        del want
+        flat = r.ids.reshape(-1).long()
+        perm = flat.sort(stable=True).indices
+        assert torch.equal(r.perm, perm) and torch.equal(r.rows.long(), perm // k)
+        assert torch.equal(r.place[perm], torch.arange(P, device="cuda"))
+        assert torch.equal(r.offsets[1:].long(), torch.bincount(flat, minlength=E).cumsum(0))
+        y = torch.randn(P, 8, generator=g, device="cuda")
+        w = r.w
+        terms = w.to(FP64)[:, :, None] * y.to(FP64)[r.place.view(T, k)]
+        got = qr.combine(y, r.place.view(T, k), w).to(FP64)
+        assert bool(((got - terms.sum(1)).abs() <= (k + 1) * 2.0**-24 * terms.abs().sum(1) + 2.0**-149).all())
+        d = torch.randn(T, 8, generator=g, device="cuda")
+        dy, dw = qr.combine_grad(d, y, r.place.view(T, k), w)
+        assert torch.equal(dy[r.place].view(T, k, 8), w[:, :, None] * d[:, None])
+        mags = y.to(FP64)[r.place.view(T, k)] * d.to(FP64)[:, None]
+        assert bool(((dw.to(FP64) - mags.sum(2)).abs() <= 12 * 2.0**-24 * mags.abs().sum(2) + 2.0**-149).all())
+    with pytest.raises(ValueError, match="pairs"):
+        qr.sort_pairs(torch.zeros(P // 8 + 1, 8, dtype=torch.int32, device="cuda"), 1024)
+    with pytest.raises(qr.MoEError):
+        qr.route(torch.zeros(P + 1, 4, device="cuda"), 1)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 def test_a_layer_from_logits_to_gradients(dtype):
     """Router, experts and sum together, differentiated to the router's logits, against 64-bit autograd.  At most
@@ -816,6 +849,20 @@ def test_orthogonalize_steep_steps():
         got = _qr().orthogonalize(x.cuda(), steps=5, coefficients=each).cpu().to(FP64)
         tol = (1 + 6 / 8) * UNIT[dtype] + 6 * 2.0**-22 * 6 * 3.75**3
         assert float((got - want).norm()) <= tol * float(want.norm()), dtype
+
+
+def test_orthogonalize_extreme_shapes():
+    """More matrices than a launch takes; the longest rows; a single row; a large square."""
+    qr = _qr()
+    for shape, dtype in (((66000, 2, 3), FP32), ((2, 65536, 24), BF16), ((24, 65536), FP16), ((1, 65536), FP32),
+                         ((3, 4100, 1030), BF16)):
+        g = torch.randn(shape, generator=gen(shape[-1])).to(dtype).cuda()
+        want = newton_schulz(g)
+        got = qr.orthogonalize(g)
+        err = (got.to(FP64) - want).flatten(-2).norm(dim=-1).reshape(-1)
+        size = want.flatten(-2).norm(dim=-1).reshape(-1)
+        one = orthogonal_bound(torch.ones(1, dtype=FP64), dtype, depth=max(shape[-2:])) + 2.0**-22
+        assert bool((err <= one * size).all()), (shape, float((err / size).max()))
 
 
 def test_orthogonalize_in_place_streams_and_graphs():
