@@ -361,8 +361,8 @@ int moe_swiglu_grad(int32_t dtype, const void *dh, int64_t dh_stride, const void
  * is the sum of its group_best largest keys (of those there), and the
  * keep_groups best groups stay.  The top_k largest keys are chosen, in
  * falling order; equal keys and groups: the lower index first.  Keys are
- * compared as real numbers to 64 bits (without a bias as their logits, which
- * have the same order).  NaN ranks behind every number.  Weights are s, or s
+ * compared as real numbers to 64 bits (without a bias, or with the same for
+ * every expert, as their logits, which have the same order).  NaN ranks behind every number.  Weights are s, or s
  * / sum of the chosen s with renormalize (0 where that sum is 0), times
  * scale, to fp32 rounding.  Where fewer than top_k experts are there, the
  * ranks left have expert -1 and weight 0. */

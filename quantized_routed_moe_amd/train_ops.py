@@ -89,8 +89,9 @@ def route(logits, top_k, score="sigmoid", bias=None, groups=1, keep_groups=None,
 
     Scores are "sigmoid" or "softmax" of the logits.  `bias` [E] fp32 is added for the choice only; an expert whose
     logit or bias is -inf is not there.  With groups > 1, of that many equal runs of experts the `keep_groups` with
-    the largest sums of their `group_best` (1 or 2) largest keys stay.  Equal keys go to the lower index.  Weights
-    are the chosen scores, with `renormalize` divided by their sum, times `scale`; where fewer than top_k experts are
+    the largest sums of their `group_best` (1 or 2) largest keys stay.  Equal keys go to the lower index (a bias that
+    is the same for every expert changes no order, nor does it make keys equal).  Weights are the chosen scores, with
+    `renormalize` divided by their sum, times `scale`; where fewer than top_k experts are
     left, ids are -1 and weights 0."""
     graph = _graph("route", None, logits, instead="use Routing.from_logits")
     ids, w, _ = _route("moe_route", logits, top_k, score, bias, groups, keep_groups, group_best, renormalize, scale,
@@ -248,7 +249,8 @@ def orthogonalize(g, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, stream=N
     batch = g.numel() // (rows * cols)
     if not 1 <= steps <= MAX_STEPS:
         raise ValueError(f"steps: expected 1 to {MAX_STEPS}, got {steps}")
-    each = [tuple(coefficients)] * steps if not hasattr(coefficients[0], "__len__") else [tuple(c) for c in coefficients]
+    one = not hasattr(coefficients[0], "__len__")
+    each = [tuple(coefficients)] * steps if one else [tuple(c) for c in coefficients]
     if len(each) != steps or any(len(c) != 3 for c in each):
         raise ValueError(f"coefficients: expected (a, b, c) or {steps} of them, got {coefficients!r}")
     index, raw, side = _target(g, "g", stream)
