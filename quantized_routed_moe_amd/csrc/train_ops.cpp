@@ -1,5 +1,6 @@
 // Host side of the operators around the experts declared in include/moe.h
-// (router, pairs' order, their sum, gradients): argument checks and dispatch.
+// (router, pairs' order, their sum, gradients, the update): argument checks and
+// dispatch.
 // Nothing is allocated and nothing synchronises.
 #include <hip/hip_runtime.h>
 
