@@ -596,7 +596,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
                     const double o = __shfl(score, base + g);
                     before += o > score || (o == score && g < j);
                 }
-                in = j < a.groups && before < a.keep;
+                if (unsure) in = j < a.groups && before < a.keep;  // the wave's other tokens are settled
                 unsure = unsure && ((__ballot(vague) >> base) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) != 0;
             }
             wave_sync();

@@ -892,3 +892,40 @@ def test_orthogonalize_in_place_streams_and_graphs():
     odd = torch.randn(1 + 3 * 35 * 41, generator=gen(11)).to(BF16).cuda()[1:].view(3, 35, 41)  # aligned to an element only
     assert torch.equal(qr.orthogonalize(odd), qr.orthogonalize(odd.clone()))
     assert qr.orthogonalize(torch.empty(0, 4, 5).cuda()).shape == (0, 4, 5)
+
+
+# ------------------------------------------------ where the choice is close
+def check_alone(x, k, **kw):
+    """What a token gets does not depend on the tokens beside it."""
+    qr = _qr()
+    on = {n: v.cuda() if torch.is_tensor(v) else v for n, v in kw.items()}
+    ids, w = qr.route(x.cuda(), k, **on)
+    for t in range(x.shape[0]):
+        one, ow = qr.route(x[t : t + 1].cuda(), k, **on)
+        assert torch.equal(one[0], ids[t]) and torch.equal(ow[0].nan_to_num(), w[t].nan_to_num()), t
+    return ids.cpu()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("even", [0.5, -0.5, 0.0])
+def test_route_groups_beside_a_token_that_ties(score, even):
+    """A token whose groups are far apart is settled in fp32, whatever the tokens of the same wave need."""
+    gone, small = -math.inf, math.log(0.2)
+    x = torch.tensor([[0.0, 0.0, 0.0, 0.0], [0.0, gone, small, small], [0.0, gone, -0.1, -0.1], [gone, gone, 1.0, -3.0],
+                      [-8.0, -9.0, gone, 2.0], [gone] * 4, [1.0, 2.0, 1.0, 2.0]])
+    bias = torch.full((4,), even)
+    check_route(x, 2, score=score, bias=bias, groups=2, keep_groups=1)
+    check_alone(x, 2, score=score, bias=bias, groups=2, keep_groups=1)
+    g = gen(21)
+    x = torch.randn(64, 32, generator=g).repeat(2, 1)
+    x[torch.rand(x.shape, generator=g) < 0.6] = gone
+    x[::3] = 0.25  # ties throughout
+    check_route(x, 4, score=score, bias=torch.full((32,), even), groups=8, keep_groups=3)
+
+
+def test_route_groups_with_a_nan_beside_a_token_that_ties():
+    """A group of a number and a NaN is behind one of two numbers, beside a tie too."""
+    x = torch.tensor([[0.0, 0.0, 0.0, 0.0], [5.0, math.nan, -1.0, -1.0], [-1.0, -2.0, math.nan, 7.0]])
+    for kw in (dict(), dict(bias=torch.zeros(4)), dict(bias=torch.tensor([0.0, 0.25, 0.0, 0.25]))):
+        ids = check_alone(x, 2, groups=2, keep_groups=1, **kw)
+        assert sorted(ids[1].tolist()) == [2, 3] and sorted(ids[2].tolist()) == [0, 1]
