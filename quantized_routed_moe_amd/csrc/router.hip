@@ -187,7 +187,7 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
     }
     auto key_of = [&](int e, bool score) -> double {
         const float lf = load_logit<DT>(a.logits, row + e);
-        const double l = lf, b = a.bias ? (double)a.bias[e] : 0.0;
+        const double l = lf, b = biased ? (double)a.bias[e] : 0.0;
         if (lf == -INFINITY) return -INFINITY;
         if (!score) return number(l, -DBL_MAX);
         return number((soft ? exp(l - (double)top) / z : sigmoid_f64(l)) + b, -DBL_MAX);
@@ -200,6 +200,8 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
     if (a.groups > 1) {
         const int size = a.E / a.groups;
         double mine = -INFINITY;  // of group `lane`
+        int many = 0;             // the keys in it: a bias that is the same for all counts that often
+        const double even = a.bias && !biased ? (double)a.bias[0] : 0.0;
         for (int g = 0; g < a.groups; ++g) {
             double t1 = -INFINITY, t2 = -INFINITY;
             auto add = [&](double x) {
@@ -215,13 +217,19 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
                 add(o1);
                 add(o2);
             }
-            const double v = a.best == 2 && t2 != -INFINITY ? t1 + t2 : t1;
-            if (lane == g) mine = v;
+            const bool two = a.best == 2 && t2 != -INFINITY;
+            const double v = two ? t1 + t2 : t1;
+            if (lane == g) {
+                mine = v;
+                many = two ? 2 : t1 != -INFINITY;
+            }
         }
         int before = 0;
         for (int g = 0; g < a.groups; ++g) {
             const double o = __shfl(mine, g);
-            before += o > mine || (o == mine && g < lane);
+            const int n = __shfl(many, g) - many;
+            const double d = (o == mine ? 0.0 : o - mine) + n * even;
+            before += d > 0 || (d == 0 && g < lane);
         }
         const uint64_t kept = __ballot(lane < a.groups && before < a.keep);
 #pragma unroll 1
@@ -452,8 +460,9 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
     const float ahead = load_logit<DT>(from, (int)(min(wave * TW + lane / L, t_end - first_t - 1) * a.ld + min(j, E - 1)) * B);
     // a bias that is the same for every expert changes no order: then, as without one, the logits are the keys
     bool biased = false;
+    float even = 0;  // what such a bias is
     if (a.bias) {
-        const float first = a.bias[0];
+        const float first = even = a.bias[0];
         bool same = fabsf(first) < INFINITY;
         for (int e0 = 0; e0 < E; e0 += 256) {
             float b[4];
@@ -577,11 +586,16 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
                         else if (x > b2) b2 = x, i2 = n;
                     }
                 }
+                // A bias that is the same for all is left out, and so is a softmax's sum: that orders groups which count it
+                // equally often.  Where they do not, choose_f64 decides.
                 auto exactly = [&](int n) -> double {
                     const double l = load_logit<DT>(from, row + (j * size + n) * B);
-                    return (SOFT ? exp(l - (double)top) : sigmoid_f64(l)) + load_logit<kDtF32>(bias_from, (j * size + n) * 4);
+                    return (SOFT ? exp(l - (double)top) : sigmoid_f64(l)) +
+                           (biased ? load_logit<kDtF32>(bias_from, (j * size + n) * 4) : 0.0f);
                 };
-                const bool two = a.best == 2 && t2 != -INFINITY;
+                const bool two = a.best == 2 && t2 != -INFINITY, some = j < a.groups && t1 != -INFINITY;
+                const bool unlike = !biased && even != 0 && group_max<L>(some && two ? 1.0f : 0.0f) > 0 &&
+                                    group_max<L>(some && !two ? 1.0f : 0.0f) > 0;
                 double score = -INFINITY;
                 if (j < a.groups && t1 > -FLT_MAX) score = exactly(i1);
                 if (j < a.groups && two && t2 > -FLT_MAX) score += exactly(i2);
@@ -589,7 +603,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
                 const bool clear = !biased || next == -INFINITY ||
                                    last - next > 2 * slack + 0x1p-23f * fmaxf(fabsf(last), fabsf(next));
                 // (a NaN among a group's best counts as the least number: left to choose_f64)
-                const bool vague = j < a.groups && (!clear || t1 == -FLT_MAX || (two && t2 == -FLT_MAX));
+                const bool vague = j < a.groups && (unlike || !clear || t1 == -FLT_MAX || (two && t2 == -FLT_MAX));
                 before = 0;
 #pragma unroll 1
                 for (int g = 0; g < a.groups; ++g) {

@@ -929,3 +929,32 @@ def test_route_groups_with_a_nan_beside_a_token_that_ties():
     for kw in (dict(), dict(bias=torch.zeros(4)), dict(bias=torch.tensor([0.0, 0.25, 0.0, 0.25]))):
         ids = check_alone(x, 2, groups=2, keep_groups=1, **kw)
         assert sorted(ids[1].tolist()) == [2, 3] and sorted(ids[2].tolist()) == [0, 1]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+def test_route_groups_of_unlike_counts_that_almost_tie(dtype):
+    """Softmax and one bias for all: a group with one expert left counts the bias once, one with two counts it twice.
+    The bias is put where the scores meet, and the numbers next to that on both sides."""
+    x = torch.tensor([[0.0, -math.inf, -1.0, -1.25], [0.0, -math.inf, -0.5, -0.25], [-math.inf, 0.5, 0.25, 0.25]]).to(dtype)
+    for row in x:
+        p = scores_of(row[None], "softmax")[0]
+        meet = (p[:2].sum() - p[2:].sum()).float()
+        for b in (meet, torch.nextafter(meet, torch.tensor(9.0)), torch.nextafter(meet, torch.tensor(-9.0)), 2 * meet,
+                  meet / 2, -meet):
+            bias = b.expand(4).clone()
+            check_route(x, 1, score="softmax", bias=bias, groups=2, keep_groups=1)
+            check_alone(x, 1, score="softmax", bias=bias, groups=2, keep_groups=1)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_groups_with_a_large_even_bias(score):
+    """One bias for all, beside which the scores vanish even in 64 bits: it decides between groups that count it once and
+    twice, and between others their scores do."""
+    qr = _qr()
+    x = torch.tensor([[0.1, 0.2, 0.3, 0.2, 1.0, -math.inf, 0.2, 0.1], [0.1, 0.2, 0.3, 0.2, 0.2, 0.2, 0.2, 0.1]]).cuda()
+    for even, best, two in ((1e17, [2, 3], [2, 1, 3]), (-1e17, [4, -1], [4, 2, 3])):
+        bias = torch.full((8,), even).cuda()
+        assert qr.route(x[:1], 2, score=score, bias=bias, groups=4, keep_groups=1)[0].tolist() == [best]
+        assert qr.route(x[:1], 3, score=score, bias=bias, groups=4, keep_groups=2)[0].tolist() == [two]
+        assert qr.route(x[1:], 4, score=score, bias=bias, groups=4, keep_groups=2)[0].tolist() == [[2, 3, 4, 5]]
+        check_alone(x.cpu(), 2, score=score, bias=bias.cpu(), groups=4, keep_groups=2)
