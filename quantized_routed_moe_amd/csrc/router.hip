@@ -79,7 +79,9 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// What a NaN key counts as: behind every number, before -inf (an expert that is not there).
+// What a NaN key counts as: behind every number, before -inf (an expert that is not there).  In 64 bits so that two of
+// them can be added.
+constexpr double kLeast = -1e300;
 template <class T>
 __device__ __forceinline__ T number(T key, T least) {
     return key != key ? least : key;
@@ -189,8 +191,8 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
         const float lf = load_logit<DT>(a.logits, row + e);
         const double l = lf, b = biased ? (double)a.bias[e] : 0.0;
         if (lf == -INFINITY) return -INFINITY;
-        if (!score) return number(l, -DBL_MAX);
-        return number((soft ? exp(l - (double)top) / z : sigmoid_f64(l)) + b, -DBL_MAX);
+        if (!score) return number(l, kLeast);
+        return number((soft ? exp(l - (double)top) / z : sigmoid_f64(l)) + b, kLeast);
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) {
@@ -566,10 +568,12 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
                 before += o > mine || (o == mine && g < j);
             }
             bool in = j < a.groups && before < a.keep;
-            // the least of the kept must be clearly above the largest of the others
+            // the least of the kept must be clearly above the largest of the others that are there (their sum may be past
+            // fp32: then size_of is too, and nothing is clear)
             const float least = -group_max<L>(in ? -mine : -INFINITY);
             const float most = group_max<L>(!in && j < a.groups ? mine : -INFINITY);
-            if (most != -INFINITY) unsure = !(least - most > 4 * slack + 0x1p-21f * group_max<L>(size_of));
+            const bool others = group_max<L>(!in && j < a.groups && t1 != -INFINITY ? 1.0f : 0.0f) > 0;
+            unsure = others && !(least - most > 4 * slack + 0x1p-21f * group_max<L>(size_of));
             // Where it is not, the groups' best experts are scored in 64 bits (not with a softmax's sum and a bias: that
             // sum is in fp32).  They have to be the best beyond doubt, else choose_f64 decides.
             if ((!SOFT || !biased) && __ballot(unsure) != 0) {
@@ -692,7 +696,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
         double s = 0;
         if (id >= 0) s = SOFT ? exp((double)l - (double)about) / (a.renorm ? 1.0 : (double)z) : sigmoid_f64(l);
         if (!SOFT && biased) {  // rank by the keys in 64 bits (a token that choose_f64 has ranked stays as it is)
-            const double key = id < 0 ? -INFINITY : number(s + (double)a.bias[id], -DBL_MAX);
+            const double key = id < 0 ? -INFINITY : number(s + (double)a.bias[id], kLeast);
             int before = 0;
 #pragma unroll 1
             for (int i = 0; i < kList; ++i) {

@@ -958,3 +958,22 @@ def test_route_groups_with_a_large_even_bias(score):
         assert qr.route(x[:1], 3, score=score, bias=bias, groups=4, keep_groups=2)[0].tolist() == [two]
         assert qr.route(x[1:], 4, score=score, bias=bias, groups=4, keep_groups=2)[0].tolist() == [[2, 3, 4, 5]]
         check_alone(x.cpu(), 2, score=score, bias=bias.cpu(), groups=4, keep_groups=2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_groups_of_lowest_keys(score):
+    """Two keys whose sum is past fp32: the group is there all the same, and its sum counts."""
+    lowest = torch.finfo(FP32).min
+    x = torch.zeros(3, 8)
+    x[:, :2] = -math.inf
+    x[1] += torch.arange(8)
+    bias = torch.tensor([0, 0, lowest, lowest, -2e38, -2e38, -3e38, -3e38])
+    for keep, kept in ((1, {4, 5}), (2, {4, 5, 6, 7}), (3, {2, 3, 4, 5, 6, 7})):
+        ids = check_route(x, 2 * keep if keep < 3 else 6, score=score, bias=bias, groups=4, keep_groups=keep)
+        assert set(ids[0].tolist()) == kept
+    far = torch.tensor([1e38, 1e38, 3e38, 2e38, 3e38, 1e38, 3e38, 3e38])  # and past it above
+    check_route(x, 2, score=score, bias=far, groups=4, keep_groups=1)
+    x[2, 2:] = math.nan  # a NaN is behind every number and before what is not there
+    for b in (None, bias):
+        ids = check_alone(x[2:], 2, score=score, groups=4, keep_groups=1, **({} if b is None else {"bias": b}))
+        assert (ids >= 2).all()
