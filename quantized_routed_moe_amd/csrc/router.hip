@@ -65,6 +65,17 @@ __device__ __forceinline__ float exp_neg(float x) {
     const float n = rintf(x * kHi), f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
     return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
+// e^x for x <= 0 (or NaN) in 64 bits, to 2^-31: ln 2 is taken out n times, |r| <= ln 2 / 2, the first term left out of the
+// series r^9 / 9!.
+__device__ __forceinline__ double exp_neg(double x) {
+    x = x < -700.0 ? -700.0 : x;
+    const double n = rint(x * 1.4426950408889634), r = __builtin_fma(n, -0.6931471805599453, x);
+    double p = 1.0 / 40320;
+    constexpr double kTerms[] = {1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (double t : kTerms) p = __builtin_fma(p, r, t);
+    return ldexp(p, (int)n);
+}
 // sigmoid, within 2^-22: its argument's rounding, at most .225 |l| 2^-23 / |l|, and a unit each of 2^-23 s (1 - s) for the
 // power, 2^-24 s for the sum and 2^-23 s for the reciprocal
 __device__ __forceinline__ float sigmoid_near(float l) {
@@ -490,8 +501,13 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
             for (int i = 0; i < kList; ++i) l[i] = e0 + L * i + j < E ? l[i] : -INFINITY;
         };
 
-        float top = 0, z = 1, rz = 1;
-        // a key's error: of the score (sigmoid_near; e^x and the sum, against the largest probability, 1 / z)
+        float top = 0, rz = 1;
+        double z = 1;
+        // A key's error is that of its score, the bias's rounding apart.  Sigmoids: sigmoid_near.  Softmax: the sum, in 64
+        // bits, has none to speak of: in one of 1024 terms that fp32 adds, what it loses of each can pass any bound that
+        // leaves much to fp32 (1023 terms of e^-16.6 beside one of 1: 7.5e-6).  Left is e^x / z, to units of 2^-24 of the
+        // largest probability, 1 / z: |x| e^x times 2.5 for the argument's roundings, one at most; two each for the power and
+        // for 1 / z, one for the product.
         float slack = 0x1p-22f;
         if (SOFT && (scored || !a.renorm)) {
             float l[kList];
@@ -503,16 +519,16 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
             }
             top = group_max<L>(top);
             if (top == -INFINITY) top = 0;
-            float part = 0;
+            double part = 0;
             for (int e0 = 0; e0 < E; e0 += kList * L) {
                 logits(e0, l);
 #pragma unroll
-                for (int i = 0; i < kList; ++i) part += exp_neg(l[i] - top);
+                for (int i = 0; i < kList; ++i) part += exp_neg((double)l[i] - (double)top);
             }
-            z = group_sum<L>(part);
+            z = group_reduce<L>(part, [](double x, double y) { return x + y; });
             if (z == 0) z = 1;
-            rz = 1.0f / z;
-            slack = 0x1p-20f * rz;
+            rz = 1.0f / (float)z;
+            slack = 0x1p-21f * rz;
         }
         // fp32 keys by score; a logit of -inf needs its own look
         auto by_score = [&](int e0, const float (&l)[kList], float (&f)[kList]) {
@@ -694,7 +710,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
         const float l = id >= 0 ? load_logit<DT>(from, row + id * B) : -INFINITY;
         const float about = SOFT && a.renorm ? group_max<L>(l) : top;
         double s = 0;
-        if (id >= 0) s = SOFT ? exp((double)l - (double)about) / (a.renorm ? 1.0 : (double)z) : sigmoid_f64(l);
+        if (id >= 0) s = SOFT ? exp((double)l - (double)about) / (a.renorm ? 1.0 : z) : sigmoid_f64(l);
         if (!SOFT && biased) {  // rank by the keys in 64 bits (a token that choose_f64 has ranked stays as it is)
             const double key = id < 0 ? -INFINITY : number(s + (double)a.bias[id], kLeast);
             int before = 0;

@@ -977,3 +977,27 @@ def test_route_groups_of_lowest_keys(score):
     for b in (None, bias):
         ids = check_alone(x[2:], 2, score=score, groups=4, keep_groups=1, **({} if b is None else {"bias": b}))
         assert (ids >= 2).all()
+
+
+@pytest.mark.parametrize("E", [256, 512, 1024])
+@pytest.mark.parametrize("v", [-5.7663784, -16.6443996, -16.75])
+def test_route_softmax_of_many_small_terms(E, v):
+    """One logit of 0, the others so far below that each is lost, in part or whole, when it is added to a running fp32
+    sum: the weights are to fp32 rounding all the same, and the choice is that of real numbers where the bias puts the
+    others just ahead, or just behind."""
+    x = torch.full((3, E), v)
+    x[:, 0] = 0
+    x[1, 3], x[2, E - 1] = -1.0, -0.5
+    want, w = reference(x, 4, score="softmax", renormalize=False)
+    ids, got = _qr().route(x.cuda(), 4, score="softmax", renormalize=False)
+    assert torch.equal(ids.cpu(), want)
+    # 64 bits but for the exponentials' polynomial (2^-30) and one rounding
+    assert bool(((got.cpu().to(FP64) - w).abs() <= 2.0**-24 * (1 + 2.0**-5) * w).all())
+    p = scores_of(x[:1], "softmax")[0]
+    meet = (p[0] - p[1]).float()
+    for b in (meet, torch.nextafter(meet, torch.tensor(9.0)), torch.nextafter(meet, torch.tensor(-9.0))):
+        bias = b.expand(E).clone()
+        bias[0] = 0
+        check_route(x, 2, score="softmax", bias=bias)
+        check_route(x, 1, score="softmax", bias=bias, groups=4, keep_groups=2)
+        check_route(x, 8, score="softmax", bias=bias, renormalize=False)
