@@ -842,7 +842,8 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
             c = (float)(group_reduce<L>(g, [](double x, double y) { return x + y; }) * (double)rz);
         } else {
             double s = 0, rest = 0, g = id >= 0 ? (double)dw * a.scale : 0.0;  // score, its complement, the gradient of the score
-            const float about = soft ? group_max<L>(l) : 0.0f;
+            float about = soft ? group_max<L>(l) : 0.0f;
+            if (about == -INFINITY) about = 0;  // every expert named has logit -inf: scores of 0
             if (id >= 0) {
                 const double x = soft ? (double)l - (double)about : (double)l, e = exp(soft ? x : -fabs(x)), q = 1.0 / (1.0 + e);
                 s = soft ? e : x < 0 ? e * q : q;

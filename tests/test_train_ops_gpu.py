@@ -1001,3 +1001,17 @@ def test_route_softmax_of_many_small_terms(E, v):
         check_route(x, 2, score="softmax", bias=bias)
         check_route(x, 1, score="softmax", bias=bias, groups=4, keep_groups=2)
         check_route(x, 8, score="softmax", bias=bias, renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_grad_of_chosen_experts_that_are_not_there(score, renorm):
+    """Ids that name experts of logit -inf: their scores are 0, and so are the gradients."""
+    x = logits(6, 20, FP32, 3)
+    x[0], x[1, 4:], x[2, :3] = -math.inf, -math.inf, -math.inf
+    ids = torch.tensor([[0, 1, 2], [5, 6, 7], [0, 1, 2], [2, 1, 0], [-1, 20, -1], [3, 3, 3]], dtype=torch.int32)
+    dw = torch.randn(6, 3, generator=gen(2))
+    want, mag = grad_reference(dw, x, ids, score, renorm, 1.0)
+    got = _qr().route_grad(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalize=renorm).cpu().to(FP64)
+    assert (got[0] == 0).all() and (renorm is False or (got[1:3] == 0).all())
+    assert bool(((got - want).abs() <= 2.0**-24 * want.abs() + 2.0**-18 * mag + 2.0**-149).all())
