@@ -759,8 +759,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
 //   softmax: dl_e = s_e (G_e - sum_j G_j s_j); renormalised the sum is 0
 // What it has to move is the gradient of every logit, and the logits where all of them have one (DENSE: softmax, not
 // renormalised); those are read once and their exponentials stay in registers.  L lanes a token, V consecutive experts
-// a lane and access.  What the chosen get passes through LDS, one after the other, so that an expert named twice gets
-// both.  65536 tokens of 256 experts, bf16: DENSE 18.4 us (67 MB, 3.7 TB/s; the vector units are busy half the time,
+// a lane and access.  What the chosen get passes through LDS: an expert named twice has both's, by one after the other or
+// (DENSE) by the first of them.  65536 tokens of 256 experts, bf16: DENSE 18.4 us (67 MB, 3.7 TB/s; the vector units are busy half the time,
 // with the exponentials and the chosen's 64-bit sums), else 12.3 (34 MB and the chosen logits).
 constexpr int kGradThreads = 256;
 template <int DT, int V>
@@ -789,6 +789,28 @@ __device__ __forceinline__ void store_some(void *p, int64_t at, const float (&v)
     }
 }
 
+// f(integral_constant r) for the ranks r < k.
+template <int R = 0, class F>
+__device__ __forceinline__ void each_rank(int k, F &&f) {
+    if constexpr (R < kMaxTopK) {
+        if (R >= k) return;
+        f(std::integral_constant<int, R>{});
+        each_rank<R + 1>(k, f);
+    }
+}
+// What the lane of rank R has: lane R of a row of 16, which is a token's row or, of 64 lanes a token, the one that its
+// pairs are in.
+template <int R>
+__device__ __forceinline__ int of_rank(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x150 + R, 0xf, 0xf, false);  // row_newbcast
+}
+template <int R>
+__device__ __forceinline__ double of_rank(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)of_rank<R>((int)u), hi = (uint32_t)of_rank<R>((int)(u >> 32));
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
 template <int DT, int L, int PER, int V, bool DENSE>
 __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
     constexpr int TW = 64 / L, WAVES = kGradThreads / 64, N = PER / V;  // accesses of a lane
@@ -807,8 +829,10 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
         if ((uint32_t)id >= (uint32_t)E) id = -1;
         const float dw = j < k ? a.dw[tt * k + j] : 0.0f;
         const float l = id >= 0 ? load_logit<DT>(a.logits, row + id) : -INFINITY;
-        float ex[N][V], top = 0, rz = 1;
+        float ex[N][V], top = 0;
+        double rest = 0;  // DENSE: the sum of the exponentials of what is not chosen
         if constexpr (DENSE) {
+            if (id >= 0) mine[id] = 1;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int e = (i * L + j) * V;  // all of the V or none are experts
@@ -823,23 +847,43 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
                 for (int u = 0; u < V; ++u) top = fmaxf(top, ex[i][u]);
             top = group_max<L>(top);
             if (top == -INFINITY) top = 0;
+            wave_sync();
             float z = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    ex[i][u] = exp_neg(ex[i][u] - top);
+                    ex[i][u] = mine[(i * L + j) * V + u] != 0 ? 0.0f : exp_neg(ex[i][u] - top);
                     z += ex[i][u];
                 }
-            z = group_sum<L>(z);
-            rz = z == 0 ? 1.0f : 1.0f / z;
+            rest = group_reduce<L>((double)z, [](double x, double y) { return x + y; });
         }
         float d, c = 0;
         if constexpr (DENSE) {
-            // the sum over the chosen may cancel: in 64 bits, and with it the scores of which it is made
-            const double g = id >= 0 ? (double)dw * a.scale * (exp((double)l - (double)top) * (double)rz) : 0.0;
-            d = (float)g;
-            c = (float)(group_reduce<L>(g, [](double x, double y) { return x + y; }) * (double)rz);
+            // G_j - sum_i G_i s_i = sum over all experts of (G_j - G_e) s_e, which keeps its precision where s_j is near 1.
+            // What is not chosen has G = 0; an expert named twice has both's G, in the first lane that names it.
+            const double g = id >= 0 ? (double)dw * a.scale : 0.0;
+            double both = 0, s = id >= 0 ? exp((double)l - (double)top) : 0.0;
+            bool first = id >= 0;
+            each_rank(k, [&](auto r) {
+                const bool same = of_rank<decltype(r)::value>(id) == id;
+                both += same ? of_rank<decltype(r)::value>(g) : 0.0;
+                first &= !same || decltype(r)::value >= j;
+            });
+            auto add = [](double x, double y) { return x + y; };
+            s = first ? s : 0.0;
+            const double z = rest + group_reduce<L>(s, add), rz = z == 0 ? 1.0 : 1.0 / z;
+            s *= rz;
+            c = (float)(group_reduce<L>(both * s, add) * rz);
+            double sum = both * (rest * rz);
+            each_rank(k, [&](auto r) {
+                sum += (both - of_rank<decltype(r)::value>(both)) * of_rank<decltype(r)::value>(s);
+            });
+            d = (float)(s * sum);
+            if (!first) id = -1;
+            wave_sync();  // all have read what is named
+            if (id >= 0) mine[id] = d;
+            wave_sync();
         } else {
             double s = 0, rest = 0, g = id >= 0 ? (double)dw * a.scale : 0.0;  // score, its complement, the gradient of the score
             float about = soft ? group_max<L>(l) : 0.0f;
@@ -856,7 +900,7 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
             }
             d = (float)(g * s * rest);
         }
-        for (int r = 0; r < k; ++r) {
+        for (int r = 0; !DENSE && r < k; ++r) {
             if (j == r && id >= 0) mine[id] += d;
             wave_sync();
         }

@@ -1015,3 +1015,25 @@ def test_route_grad_of_chosen_experts_that_are_not_there(score, renorm):
     got = _qr().route_grad(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalize=renorm).cpu().to(FP64)
     assert (got[0] == 0).all() and (renorm is False or (got[1:3] == 0).all())
     assert bool(((got - want).abs() <= 2.0**-24 * want.abs() + 2.0**-18 * mag + 2.0**-149).all())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("E,k", [(8, 1), (60, 3), (256, 1), (256, 8), (700, 4)])
+def test_route_grad_of_a_confident_token(dtype, E, k):
+    """A softmax's gradient at the chosen is p_j sum_e (G_j - G_e) p_e, to a relative error, however near p_j is to 1:
+    p (G - sum G p) would lose it.  An exponential's is two units of 2^-24 and its argument's, |x| <= 30, more; the sum
+    of a lane's sixteen and of lanes is in 64 bits or shorter than that: 2^-18.  Then the output's rounding."""
+    qr = _qr()
+    x = 0.25 * torch.randn(8, E, generator=gen(E))
+    x[torch.arange(8), torch.arange(8) % E] += torch.tensor([0.0, 4, 8, 12, 16, 20, 24, 28])
+    x = x.to(dtype)
+    ids, _ = reference(x, k, score="softmax")
+    dw = torch.randn(8, k, generator=gen(1))
+    p = scores_of(x, "softmax")
+    G = torch.zeros(8, E, dtype=FP64).scatter_(1, ids.long(), 1.5 * dw.to(FP64))
+    terms = p[:, :, None] * (G[:, :, None] - G[:, None, :]) * p[:, None, :]
+    want, mag = terms.sum(2), terms.abs().sum(2)
+    got = qr.route_grad(dw.cuda(), x.cuda(), ids.cuda(), score="softmax", renormalize=False, scale=1.5).cpu().to(FP64)
+    err = (got - want).abs()
+    tol = UNIT[dtype] * (1 + 2.0**-10) * want.abs() + 2.0**-18 * mag + TINY[dtype]
+    assert bool((err <= tol).all()), float((err / tol).max())
