@@ -894,9 +894,14 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a) {
                 rest = soft ? 1.0 : x < 0 ? q : e * q;
             }
             auto add = [](double x, double y) { return x + y; };
-            if (a.renorm) {
-                const double gs = group_reduce<L>(g * s, add), sum = group_reduce<L>(s, add), r = sum == 0 ? 1.0 : 1.0 / sum;
-                g = (g - gs * r) * r;
+            if (a.renorm) {  // of s / S, and G_j - sum_i G_i s_i / S = sum_i (G_j - G_i) s_i / S, as above
+                const double sum = group_reduce<L>(s, add);
+                s = sum == 0 ? 0.0 : s / sum;
+                double to = 0;
+                each_rank(k, [&](auto i) {
+                    to += (g - of_rank<decltype(i)::value>(g)) * of_rank<decltype(i)::value>(s);
+                });
+                g = to;
             }
             d = (float)(g * s * rest);
         }

@@ -1037,3 +1037,30 @@ def test_route_grad_of_a_confident_token(dtype, E, k):
     err = (got - want).abs()
     tol = UNIT[dtype] * (1 + 2.0**-10) * want.abs() + 2.0**-18 * mag + TINY[dtype]
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [1, 2, 8])
+def test_route_grad_where_one_of_the_chosen_has_all_the_weight(dtype, score, k):
+    """Renormalised, a weight's gradient is q_j sum_i (G_j - G_i) q_i over the chosen, to a relative error of 64 bits,
+    however near a q is to 1, and the output's rounding."""
+    qr = _qr()
+    x = 0.25 * torch.randn(9, 40, generator=gen(k)) - (60 if score == "sigmoid" else 0)
+    x[torch.arange(9), torch.arange(9)] += torch.tensor([0.0, 4, 8, 16, 20, 28, 36, 44, 52])
+    x = x.to(dtype)
+    ids, _ = reference(x, k, score=score)
+    dw = torch.randn(9, k, generator=gen(1))
+    s = scores_of(x, score).gather(1, ids.long())
+    q, G = s / s.sum(1, keepdim=True), 1.5 * dw.to(FP64)
+    terms = q[:, :, None] * (G[:, :, None] - G[:, None, :]) * q[:, None, :]
+    if score == "sigmoid":
+        terms = terms * scores_of(-x.to(FP64), score).gather(1, ids.long())[:, :, None]
+    want, mag = (torch.zeros(9, 40, dtype=FP64).scatter_(1, ids.long(), v) for v in (terms.sum(2), terms.abs().sum(2)))
+    got = qr.route_grad(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalize=True, scale=1.5).cpu().to(FP64)
+    tol = UNIT[dtype] * (1 + 2.0**-10) * want.abs() + 2.0**-24 * (want != 0) * mag + TINY[dtype]
+    assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol.clamp_min(1e-300)).max())
+    # scores at the end of what 64 bits hold
+    x = -709.0 - torch.arange(40.0)[None] / 2 if score == "sigmoid" else 1000 * torch.randn(1, 40, generator=gen(2))
+    ids = torch.arange(k, dtype=torch.int32)[None]
+    assert qr.route_grad(dw[:1].cuda(), x.cuda(), ids.cuda(), score=score, renormalize=True).isfinite().all()
