@@ -11,6 +11,8 @@
 // MB, 4.95 TB/s; to fp32 110 us, 4.9), both gradients from fp32 191 us (940
 // MB, 4.9 TB/s), as a large copy.  32 tokens: 3.9 and 7.0 us, launch and the
 // latency of two loads in a row (the place, then the row).
+#include <algorithm>
+
 #include "mxfp4.hpp"
 #include "ops.hpp"
 
@@ -136,6 +138,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineArgs a) {
     }
 }
 
+constexpr int64_t kMaxBlocks = (((int64_t)1 << 32) - 1) / kThreads;  // of a launch of kThreads each
+
 // f(integral_constant k) for k of at most MOST, else f(0).
 template <int MOST, class F>
 hipError_t by_pairs(int k, F &&f) {
@@ -145,15 +149,26 @@ hipError_t by_pairs(int k, F &&f) {
 
 }  // namespace
 
-hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &a, hipStream_t s) {
-    const int per = (int)(a.H / 8);
-    const int64_t blocks = per >= kThreads ? a.T * ((per + kThreads - 1) / kThreads)
-                                           : (a.T + kThreads / per - 1) / (kThreads / per);
+hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &all, hipStream_t s) {
+    const int per = (int)(all.H / 8);
+    const int64_t wide = (per + kThreads - 1) / kThreads;  // workgroups of a token, where it fills one
+    // A launch has fewer than 2^32 threads (2^20 tokens of 30728 columns would be more): tokens are taken in turns.
+    const int64_t most = kMaxBlocks / wide;
     auto go = [&](auto dt_c, auto out_c) {
-        return by_pairs<7>(a.k, [&](auto k_c) {
-            klaunch(combine_kernel<decltype(dt_c)::value, decltype(out_c)::value, decltype(k_c)::value>,
-                    dim3((unsigned)blocks), dim3(kThreads), s, a);
-            return hipGetLastError();
+        return by_pairs<7>(all.k, [&](auto k_c) {
+            for (int64_t t = 0; t < all.T; t += most) {
+                CombineArgs a = all;
+                a.T = std::min(most, all.T - t);
+                a.place += t * a.k;
+                if (a.w) a.w += t * a.k;
+                a.out = (uint8_t *)a.out + t * a.out_ld * dt_bytes(out_dt);
+                const int64_t blocks = per >= kThreads ? a.T * wide : (a.T + kThreads / per - 1) / (kThreads / per);
+                klaunch(combine_kernel<decltype(dt_c)::value, decltype(out_c)::value, decltype(k_c)::value>,
+                        dim3((unsigned)blocks), dim3(kThreads), s, a);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
+            return hipSuccess;
         });
     };
     constexpr std::integral_constant<int, kDtF32> f32{};

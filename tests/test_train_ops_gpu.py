@@ -1064,3 +1064,19 @@ def test_route_grad_where_one_of_the_chosen_has_all_the_weight(dtype, score, k):
     x = -709.0 - torch.arange(40.0)[None] / 2 if score == "sigmoid" else 1000 * torch.randn(1, 40, generator=gen(2))
     ids = torch.arange(k, dtype=torch.int32)[None]
     assert qr.route_grad(dw[:1].cuda(), x.cuda(), ids.cuda(), score=score, renormalize=True).isfinite().all()
+
+
+def test_combine_of_more_than_one_launch():
+    """As many tokens as there may be of rows so long that their threads pass 2^32; exact: one pair a token, weights that
+    are powers of two."""
+    qr = _qr()
+    T, n = 1 << 20, 30728
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randn(5, n, generator=g, device="cuda").to(BF16)
+    place = torch.randint(0, 5, (T, 1), generator=g, device="cuda")
+    w = 2.0 ** torch.randint(-2, 3, (T, 1), generator=g, device="cuda")
+    out = qr.combine(y, place, w, dtype=BF16)
+    for t in range(0, T, 1 << 14):
+        assert torch.equal(out[t : t + (1 << 14)], y[place[t : t + (1 << 14), 0]] * w[t : t + (1 << 14)].to(BF16)), t
+    del out
+    torch.cuda.empty_cache()
