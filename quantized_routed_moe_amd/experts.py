@@ -124,6 +124,8 @@ class Routing:
     def combine(self, y: torch.Tensor) -> torch.Tensor:
         """out [T, n] of the pairs' results y [T * k, n]: sum over a token's pairs of w * y.  Differentiable in w and
         y."""
+        if y.dim() != 2 or y.shape[0] != self.place.numel():
+            raise ValueError(f"y: expected a row for each of {self.place.numel()} pairs, got {tuple(y.shape)}")
         graph = torch.is_grad_enabled() and (y.requires_grad or self.w.requires_grad)
         if graph or forward_ad._current_level >= 0 or not self._by_kernel(y, self.w) or y.shape[1] % 8 != 0 or (
                 y.dtype not in DT):

@@ -224,3 +224,12 @@ def test_numbers_that_do_not_fit_are_refused():
     for steps in (0, -1, 33, 5 + (1 << 32)):
         with pytest.raises(ValueError, match="steps"):
             qr.orthogonalize(torch.zeros(2, 3), steps=steps)
+
+
+def test_combine_wants_a_row_for_each_pair():
+    """A missing row is no pair without an expert: the kernel would leave it out of the sum."""
+    r = qr.Routing.from_ids(torch.tensor([[0, 2], [1, 0], [2, 1]]), torch.rand(3, 2), 3)
+    for y in (torch.ones(5, 8), torch.ones(7, 8), torch.ones(3, 2, 8), torch.ones(6)):
+        with pytest.raises(ValueError, match="row for each of 6 pairs"):
+            r.combine(y)
+    assert r.combine(torch.ones(6, 8)).shape == (3, 8)
