@@ -73,10 +73,15 @@ class Routing:
         return cls(debug["perm"], debug["offsets"], debug["w"])
 
     @classmethod
-    def from_ids(cls, ids: torch.Tensor, w: torch.Tensor, n_experts: int) -> "Routing":
+    def from_ids(cls, ids: torch.Tensor, w: torch.Tensor, n_experts: int, strict: bool = False) -> "Routing":
         """Of the experts [T, k] that a router chose and their weights [T, k]; pairs whose expert is outside
         [0, n_experts) are of none.  On the GPU the order is made by sort_pairs, without synchronising, for as many
-        pairs and experts as the grouped products take."""
+        pairs and experts as the grouped products take.
+
+        `strict` reads the ids first, which synchronises, and raises for one outside [-1, n_experts), which no router
+        gives."""
+        if strict and bool(((ids < -1) | (ids >= n_experts)).any()):
+            raise ValueError(f"ids: expected experts below {n_experts}, or -1 for none")
         if ids.is_cuda and ids.numel() <= MAX_PAIRS and 1 <= n_experts <= MAX_EXPERTS:
             with torch.cuda.device(ids.device):
                 choice = ids if ids.dtype in (torch.int32, torch.int64) else ids.long()

@@ -233,3 +233,14 @@ def test_combine_wants_a_row_for_each_pair():
         with pytest.raises(ValueError, match="row for each of 6 pairs"):
             r.combine(y)
     assert r.combine(torch.ones(6, 8)).shape == (3, 8)
+
+
+def test_from_ids_strict():
+    """An id that no router gives is reported where that is asked for; -1 stands for none."""
+    w = torch.rand(2, 2)
+    for bad in ([[0, 4], [1, 2]], [[0, -2], [1, 2]], [[0, 1 << 40], [1, 2]]):
+        with pytest.raises(ValueError, match="experts below 4"):
+            qr.Routing.from_ids(torch.tensor(bad), w, 4, strict=True)
+        assert qr.Routing.from_ids(torch.tensor(bad), w, 4).offsets.tolist()[-1] == 3
+    r = qr.Routing.from_ids(torch.tensor([[0, -1], [3, 2]]), w, 4, strict=True)
+    assert r.offsets.tolist() == [0, 1, 1, 2, 3]
