@@ -1080,3 +1080,27 @@ def test_combine_of_more_than_one_launch():
         assert torch.equal(out[t : t + (1 << 14)], y[place[t : t + (1 << 14), 0]] * w[t : t + (1 << 14)].to(BF16)), t
     del out
     torch.cuda.empty_cache()
+
+
+def test_routing_combine_gradients():
+    """Through Routing.combine, in y and in w, against 64 bits; pairs of no expert among them."""
+    qr = _qr()
+    ids = torch.stack([torch.randperm(9, generator=gen(i))[:3] for i in range(20)])
+    ids[3, 1] = -1
+    w, y = torch.rand(20, 3, generator=gen(1)), torch.randn(60, 48, generator=gen(2))
+    d = torch.randn(20, 48, generator=gen(3))
+    for dtype in ALL:
+        leaf, wl = y.to(dtype).cuda().requires_grad_(), w.cuda().requires_grad_()
+        r = qr.Routing.from_ids(ids.cuda(), wl, 9)
+        out = r.combine(leaf)
+        got = torch.autograd.grad(out, (leaf, wl), d.cuda())
+        place = order_of(ids, 9)[3].view(20, 3)
+        at = y.to(dtype).to(FP64)[place]
+        dy = torch.empty(60, 48, dtype=FP64)
+        dy[place] = w.to(FP64)[:, :, None] * d.to(FP64)[:, None]
+        terms = at * d.to(FP64)[:, None]
+        assert bool(((got[0].cpu().to(FP64) - dy).abs() <= (UNIT[dtype] + 2.0**-24) * 1.01 * dy.abs() + TINY[dtype]).all())
+        assert bool(((got[1].cpu().to(FP64) - terms.sum(2)).abs() <= 48 * 2.0**-24 * terms.abs().sum(2)).all())
+        mags = (at * w.to(FP64)[:, :, None]).abs().sum(1)
+        want = (at * w.to(FP64)[:, :, None]).sum(1)
+        assert bool(((out.detach().cpu().to(FP64) - want).abs() <= 4 * 2.0**-24 * mags).all())
