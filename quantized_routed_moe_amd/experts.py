@@ -80,7 +80,7 @@ class Routing:
 
         `strict` reads the ids first, which synchronises, and raises for one outside [-1, n_experts), which no router
         gives."""
-        if strict and bool(((ids < -1) | (ids >= n_experts)).any()):
+        if strict and bool(((ids.long() < -1) | (ids.long() >= n_experts)).any()):
             raise ValueError(f"ids: expected experts below {n_experts}, or -1 for none")
         if ids.is_cuda and ids.numel() <= MAX_PAIRS and 1 <= n_experts <= MAX_EXPERTS:
             with torch.cuda.device(ids.device):

@@ -244,3 +244,5 @@ def test_from_ids_strict():
         assert qr.Routing.from_ids(torch.tensor(bad), w, 4).offsets.tolist()[-1] == 3
     r = qr.Routing.from_ids(torch.tensor([[0, -1], [3, 2]]), w, 4, strict=True)
     assert r.offsets.tolist() == [0, 1, 1, 2, 3]
+    byte = torch.tensor([[0, 1], [3, 2]], dtype=torch.uint8)
+    assert qr.Routing.from_ids(byte, w, 4, strict=True).offsets.tolist() == [0, 1, 2, 3, 4]
