@@ -362,10 +362,12 @@ int moe_swiglu_grad(int32_t dtype, const void *dh, int64_t dh_stride, const void
  * keep_groups best groups stay.  The top_k largest keys are chosen, in
  * falling order; equal keys and groups: the lower index first.  Keys are
  * compared as real numbers to 64 bits (without a bias, or with the same for
- * every expert, as their logits, which have the same order).  NaN ranks behind every number.  Weights are s, or s
- * / sum of the chosen s with renormalize (0 where that sum is 0), times
- * scale, to fp32 rounding.  Where fewer than top_k experts are there, the
- * ranks left have expert -1 and weight 0. */
+ * every expert, as their logits, which have the same order; a group's score
+ * counts such a bias as often as it has keys).  NaN ranks behind every number
+ * and before what is not there.  Weights are s, or s / sum of the chosen s
+ * with renormalize (0 where that sum is 0), times scale, to fp32 rounding.
+ * Where fewer than top_k experts are there, the ranks left have expert -1 and
+ * weight 0. */
 enum { MOE_SCORE_SIGMOID = 1, MOE_SCORE_SOFTMAX = 2 };
 typedef struct moe_router {
     int32_t n_experts;   /* 1..1024 */
@@ -392,14 +394,16 @@ typedef struct moe_pair_order {
 size_t moe_pair_order_bytes(int64_t tokens, int32_t n_experts);
 
 /* ids[tokens][top_k] and w[tokens][top_k] from logits[tokens][n_experts]
- * (fp32, bf16 or fp16, rows at any stride of at least n_experts elements);
+ * (fp32, bf16 or fp16, rows at any stride of at least n_experts and at most
+ * 2^21 elements; tokens / 512 of them, rounded up to 32, within 2^31 bytes);
  * order: NULL, or the pairs' order too.  At most MOE_MAX_PAIRS pairs. */
 int moe_route(const moe_router *router, int32_t dtype, const void *logits, int64_t stride, int64_t tokens, int32_t *ids,
               float *w, const moe_pair_order *order, void *stream);
 /* dlogits[tokens][n_experts] (the logits' type) from dw[tokens][top_k]: the
  * gradient through the weights, the choice ids being given.  Entries of ids
- * outside [0, n_experts) have none; one named twice has both's.  Of router,
- * groups and bias are not looked at. */
+ * outside [0, n_experts) have none; one named twice has both's.  What the
+ * named get keeps its precision where one of them has all the weight.  Of
+ * router, groups and bias are not looked at. */
 int moe_route_grad(const moe_router *router, int32_t dtype, const void *logits, int64_t stride, int64_t tokens,
                    const int32_t *ids, const float *dw, void *dlogits, int64_t d_stride, void *stream);
 /* The order of any choice ids[tokens][top_k] (top_k >= 1), int32 or int64 by

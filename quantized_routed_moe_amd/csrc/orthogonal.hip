@@ -105,8 +105,9 @@ struct Tile {
 
 // XL, YL: whether the operand has a lo part.  A workgroup a CU, eight waves of 128 x 64 (four of 64 x 64 in the small
 // tile), walks its tiles; copies run RING - 1 steps ahead of the arithmetic, across tiles: what LDS holds beside the
-// block that results leave through.  The small tile with four stages rather than two: 13 x 1000 x 519 608 -> 459 us
-// (and tails cut).
+// block that results leave through.  The small tile has four stages; with two 4 x 1024 x 1024 takes 514 us instead of
+// 502, but 13 x 1000 x 519 483 instead of 487 and 64 x 128 x 128 175 instead of 191: in short products filling them costs
+// what they hide.
 template <int MODE, bool XL, bool YL, int BM, int BN, int WM, int WN, int RING>  // RING: stages of the LDS ring
 __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void split_gemm_kernel(GemmArgs a) {
     constexpr bool YCOL = MODE == kApply, TRI = !YCOL;

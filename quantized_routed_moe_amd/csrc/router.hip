@@ -19,14 +19,18 @@
 // make it is kept beside the list: it is the ninth.
 //
 // What bounds it: vector instructions, 1360 for a wave's eight tokens of 256
-// experts, half of them the network's (65536 tokens of fp32: 29 us, the vector
-// units busy 58% of it; reading the logits takes 14).  Eight lanes a token
-// rather than more, as each doubling of the lanes adds a merge.  Arguments stay
+// experts, half of them the network's, each waiting for the one before
+// (65536 tokens of fp32: 29 us, the vector units busy 57% of it; reading the
+// logits takes 14).  Eight lanes a token rather than more, as each doubling of
+// the lanes adds a merge.  A softmax that is not renormalised, or has a bias,
+// reads the logits three times and forms its sum in 64 bits (65536 x 256 bf16
+// 36 and 47 us, the same renormalised sigmoids with a bias 26).  Arguments stay
 // in scalar registers and logits come through buffer loads, whose addresses
 // cost one instruction (63 -> 46 us); two workgroups of 512 threads have to fit
 // a CU (128 registers), or the launch itself takes longer than the work
-// (8192 tokens of eight groups 44 -> 25 us).  One token: 7.5 us, a wave's
-// latency.  The order of many pairs is two launches behind it, 4 and 7 us.
+// (8192 tokens of eight groups 44 -> 25 us).  One token: 7.6 us, a wave's
+// latency.  The order of many pairs is two launches behind it, 5 and 5 to 10
+// us.
 #include <cfloat>
 #include <type_traits>
 
@@ -423,8 +427,8 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const Id *ids, int6
     place_pairs<kSortThreads>(ids, p0, p1, E, k, o, sh);
 }
 
-// The order of few pairs by comparing each with all; `few` has the pairs' buckets.  Router and order of 1 / 4 / 10 tokens of
-// six pairs so 6.1 / 6.6 / 8.1 us, by counting 7.2 / 7.2 / 7.4.
+// The order of few pairs by comparing each with all; `few` has the pairs' buckets.  Router and order of 1 / 4 / 5 tokens of
+// six pairs, a hundred calls in a graph: so 7.7 / 8.1 / 8.6 us each, by counting 8.6 / 8.6 / 8.6.
 constexpr int kFewPairs = 32;
 __device__ __forceinline__ void order_few(const int *few, int P, int E, int k, const PairOrder &o) {
     const int tid = threadIdx.x;
@@ -760,8 +764,9 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
 // What it has to move is the gradient of every logit, and the logits where all of them have one (DENSE: softmax, not
 // renormalised); those are read once and their exponentials stay in registers.  L lanes a token, V consecutive experts
 // a lane and access.  What the chosen get passes through LDS: an expert named twice has both's, by one after the other or
-// (DENSE) by the first of them.  65536 tokens of 256 experts, bf16: DENSE 18.4 us (67 MB, 3.7 TB/s; the vector units are busy half the time,
-// with the exponentials and the chosen's 64-bit sums), else 12.3 (34 MB and the chosen logits).
+// (DENSE) by the first of them.  What those get is summed over pairs of experts, so that nothing is lost where one has all
+// the weight.  65536 tokens of 256 experts, six chosen, bf16: DENSE 21.6 us (67 MB, 3.1 TB/s; the vector units are busy
+// two thirds of the time, with the exponentials and the chosen's 64-bit sums), else 12.3 (34 MB and the chosen logits).
 constexpr int kGradThreads = 256;
 template <int DT, int V>
 __device__ __forceinline__ void load_some(const void *p, int64_t at, float (&v)[V]) {
@@ -935,8 +940,8 @@ hipError_t place(const Id *ids, int64_t P, int E, int k, const PairOrder &o, hip
 
 }  // namespace
 
-// At most kMaxChunks of whole passes of a workgroup (32 tokens with groups, 64 without); a single one of up to 64 tokens,
-// whose workgroup orders the pairs itself.  Router and order of 64 / 128 / 256 tokens of six pairs by one workgroup 8.8 /
+// At most kMaxChunks of multiples of 32 tokens: a pass of a workgroup with groups of up to 256 experts, four passes with
+// more, half of one without groups; a single one of up to 64 tokens, whose workgroup orders the pairs itself.  Router and order of 64 / 128 / 256 tokens of six pairs by one workgroup 8.8 /
 // 13.6 / 23.1 us, by several and two more launches 13.8 / 13.7 / 14.1.
 int32_t order_chunk(int64_t tokens) {
     const int64_t each = (tokens + kMaxChunks - 1) / kMaxChunks;
@@ -951,7 +956,7 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
         auto pick = [&](auto soft) {
             constexpr bool SOFT = decltype(soft)::value;
             // groups are scored by a lane each, and a wave's keys have to fit its LDS: 16 lanes a token up to 256 experts
-            // (8192 x 256 bf16 13.4 us, with 64 lanes 34.4), 64 beyond
+            // (8192 x 256 bf16 12.9 us, with 64 lanes 34.4), 64 beyond
             if (a.groups == 1) klaunch(route_kernel<DT, 8, false, SOFT>, grid, block, s, a);
             else if (a.E <= 256) klaunch(route_kernel<DT, 16, true, SOFT>, grid, block, s, a);
             else klaunch(route_kernel<DT, 64, true, SOFT>, grid, block, s, a);
@@ -970,7 +975,7 @@ hipError_t launch_route(int dt, const RouteArgs &a, hipStream_t s) {
 hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
     const bool dense = a.score == kSoftmax && !a.renorm;
     const uintptr_t at = (uintptr_t)a.logits | (uintptr_t)a.dlogits;
-    // accesses of four elements: 65536 x 256 bf16 19.2 us against 21.4 (softmax), 12.3 against 13.5 (sigmoid); fp32 none
+    // accesses of four elements: 65536 x 256 bf16 21.6 us against 25.5 (softmax), 12.2 against 14.2 (sigmoid)
     const bool four = (a.E | a.ld | a.d_ld) % 4 == 0 && at % (dt == kDtF32 ? 16 : 8) == 0;
     auto go = [&](auto d_c, auto dense_c, auto v_c) {
         constexpr int DT = decltype(d_c)::value, V = decltype(v_c)::value;
@@ -979,7 +984,7 @@ hipError_t launch_route_grad(int dt, const RouteArgs &a, hipStream_t s) {
             const int64_t blocks = (a.T + tokens - 1) / tokens;
             klaunch(k, dim3((unsigned)(blocks > 4096 ? 4096 : blocks)), dim3(kGradThreads), s, a);
         };
-        // 65536 x 64 bf16 softmax with 4 / 16 experts a lane: 8.7 / 12.9 us; x 256 with 16 / 64 lanes a token: 18.4 / 48
+        // 65536 x 64 bf16 softmax with 4 / 16 experts a lane: 11.7 / 17.0 us; x 256 with 16 / 64 lanes a token: 21.6 / 67
         if (a.E <= 64) with(route_grad_kernel<DT, 16, 4, V, DENSE>, 16);
         else if (a.E <= 256) with(route_grad_kernel<DT, 16, 16, V, DENSE>, 16);
         else with(route_grad_kernel<DT, 64, 16, V, DENSE>, 4);

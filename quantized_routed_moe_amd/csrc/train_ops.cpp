@@ -147,8 +147,8 @@ int32_t scale_of(double most) { return most > 0 ? std::min(15, (int)std::floor(s
 // the largest grows by P^2 a step, and is c1 / c0 of P's own value there.  A run ends before that passes an eighth of
 // the result's rounding: with the quintic after three steps for 16-bit results, after one for fp32.  Norm of the error
 // that runs of 1 / 3 / 5 add to the quintic's five steps: normal matrices 3e-6 / 1.2e-5 / 5.6e-5, one singular value of
-// 1 and 511 of 1e-4 4e-5 / 4e-5 / 9e-3 (the rounding of bf16: 1.7e-3, of fp16: 2e-4).  16 x 4096 x 2048 bf16: 12.2 /
-// 10.0 / 9.3 ms.
+// 1 and 511 of 1e-4 4e-5 / 4e-5 / 9e-3 (the rounding of bf16: 1.7e-3, of fp16: 2e-4).  16 x 4096 x 2048 bf16: 11.9 /
+// 9.7 / 9.0 ms.
 int plan_orthogonal(const float *c, int32_t steps, int32_t dtype, bool gram, OrthogonalArgs &o) {
     const double half_step = dtype == MOE_DT_F32 ? 0x1p-24 : dtype == MOE_DT_F16 ? 0x1p-11 : 0x1p-8;
     double u = 1, q = 1, lost = 0;

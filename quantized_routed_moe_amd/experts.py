@@ -128,7 +128,7 @@ class Routing:
 
     def combine(self, y: torch.Tensor) -> torch.Tensor:
         """out [T, n] of the pairs' results y [T * k, n]: sum over a token's pairs of w * y.  Differentiable in w and
-        y."""
+        y, by torch's operations; the kernel runs where no gradient is asked for."""
         if y.dim() != 2 or y.shape[0] != self.place.numel():
             raise ValueError(f"y: expected a row for each of {self.place.numel()} pairs, got {tuple(y.shape)}")
         graph = torch.is_grad_enabled() and (y.requires_grad or self.w.requires_grad)

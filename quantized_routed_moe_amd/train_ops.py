@@ -6,7 +6,8 @@ Argument checks and marshalling only, with the conventions of expert_ops: HIP
 kernels behind the C ABI of include/moe.h, enqueued on `stream` (the current
 one by default) without synchronising, results allocated for that stream.
 The calls build no graph; Routing.from_logits, Routing.combine and expert_ffn
-are the differentiable ones.
+are the differentiable ones (Routing.combine by torch's operations where a
+gradient is asked for, not by the kernels).
 """
 from __future__ import annotations
 
@@ -230,7 +231,8 @@ def combine_grad(dout, y, place, w=None, dy=None, dw=None, stream=None):
     return tuple(_Refusal.apply(graph, t, *operands) for t in (dy, dw))
 
 
-QUINTIC = (3.4445, -4.7750, 2.0315)  # small singular values grow 3.4445 a step; all end in about 0.7 .. 1.2
+# The odd quintic published by K. Jordan (2024): small singular values grow 3.4445 a step; all end in about 0.7 .. 1.2
+QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
 def orthogonalize(g, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, stream=None):
