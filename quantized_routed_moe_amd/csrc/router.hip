@@ -186,6 +186,15 @@ __device__ __forceinline__ void merge_lanes(double (&v)[kList], double &ninth, b
     }
 }
 
+// a - b + c with the right sign, so that comparing by it is an order: rounded differences could say that x is before y, y
+// before z and z before x.  The roundings of both sums are added to the result.
+__device__ __forceinline__ double difference(double a, double b, double c) {
+    const double s = a - b, t = s + c;
+    if (!(fabs(s) < INFINITY)) return s;  // one of them is not there
+    const double u = s - a, v = t - s;
+    return t + (((s - (t - v)) + (c - v)) + ((a - (s - u)) - (b + u)));
+}
+
 // ------------------------------------------------- one token in 64 bits
 // The whole wave decides for token t: lanes r < k get the expert of rank r
 // (-1: none left).  top, z: the row's largest logit and sum of e^(l - top).
@@ -245,7 +254,7 @@ __device__ __attribute__((noinline)) int choose_f64(const RouteArgs &a, int64_t 
         for (int g = 0; g < a.groups; ++g) {
             const double o = __shfl(mine, g);
             const int n = __shfl(many, g) - many;
-            const double d = (o == mine ? 0.0 : o - mine) + n * even;
+            const double d = o == mine ? n * even : difference(o, mine, n * even);
             before += d > 0 || (d == 0 && g < lane);
         }
         const uint64_t kept = __ballot(lane < a.groups && before < a.keep);
@@ -595,7 +604,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
             const bool others = group_max<L>(!in && j < a.groups && t1 != -INFINITY ? 1.0f : 0.0f) > 0;
             unsure = others && !(least - most > 4 * slack + 0x1p-21f * group_max<L>(size_of));
             // Where it is not, the groups' best experts are scored in 64 bits (not with a softmax's sum and a bias: that
-            // sum is in fp32).  They have to be the best beyond doubt, else choose_f64 decides.
+            // sum has 31).  They have to be the best beyond doubt, else choose_f64 decides.
             if ((!SOFT || !biased) && __ballot(unsure) != 0) {
                 // the best two by key (the third may be too near to tell), or without a bias by logit, which is exact
                 int i1 = 0, i2 = 0;
@@ -688,7 +697,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
         if (biased) {
             // Keys by score may be off.  Sigmoids: the candidates are the right ones if a clear step comes between rank
             // k and what is not among them, and their order is settled below.  (Behind a softmax's key is a sum that
-            // only choose_f64 forms in 64 bits: all steps have to be clear.)
+            // only choose_f64 has to the last bit: all steps have to be clear.)
             bool any = false, all = true;
 #pragma unroll
             for (int i = 0; i < kList; ++i) {

@@ -1104,3 +1104,14 @@ def test_routing_combine_gradients():
         mags = (at * w.to(FP64)[:, :, None]).abs().sum(1)
         want = (at * w.to(FP64)[:, :, None]).sum(1)
         assert bool(((out.detach().cpu().to(FP64) - want).abs() <= 4 * 2.0**-24 * mags).all())
+
+
+def test_route_groups_whose_differences_round_to_ties():
+    """Group sums of 2 + 7e-18, 2 and 2 + 1.6e-17, which 64 bits hold without the bias but not beside it: in this order
+    the first and the second, and the second and the third, seem to tie, but the third is ahead of the first."""
+    qr = _qr()
+    gone = -math.inf
+    x = torch.tensor([[gone, gone, -40.0, -40.5, 40.0, gone, -39.0, -40.0]]).cuda()
+    bias = torch.ones(8).cuda()
+    for keep, want in ((1, [6, 7]), (2, [6, 2, 7, 3])):
+        assert qr.route(x, 2 * keep, bias=bias, groups=4, keep_groups=keep)[0].tolist() == [want]
