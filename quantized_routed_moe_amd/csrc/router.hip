@@ -604,7 +604,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a) {
             const bool others = group_max<L>(!in && j < a.groups && t1 != -INFINITY ? 1.0f : 0.0f) > 0;
             unsure = others && !(least - most > 4 * slack + 0x1p-21f * group_max<L>(size_of));
             // Where it is not, the groups' best experts are scored in 64 bits (not with a softmax's sum and a bias: that
-            // sum has 31).  They have to be the best beyond doubt, else choose_f64 decides.
+            // sum is good to 2^-31 only).  They have to be the best beyond doubt, else choose_f64 decides.
             if ((!SOFT || !biased) && __ballot(unsure) != 0) {
                 // the best two by key (the third may be too near to tell), or without a bias by logit, which is exact
                 int i1 = 0, i2 = 0;

@@ -2,7 +2,7 @@
 of its pairs and its gradient, and the sum of a token's pairs with its gradients.
 
 Tolerances, relative unless said otherwise.  A router's weights come from 64 bits and are rounded once: 2^-24 (a softmax
-that is not renormalised has a sum of exponentials to 2^-31 below it; the older tests allow it 2^-19).  The gradient of
+that is not renormalised has a sum of exponentials to 2^-31 below it; check_route allows it 2^-19).  The gradient of
 such a softmax has fp32 exponentials: e^x is within 2 units of 2^-24 and, its argument being rounded, |x| <= 30 more, a
 lane's sum has 16 additions: 2 + 30 + 16 < 2^6 units, 2^-18 of the magnitudes that it adds, and the output's rounding.
 Weighted sums are in fp32: a unit for each term and one for the product, of the sum of magnitudes, and the output's
