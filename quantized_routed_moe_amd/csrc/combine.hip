@@ -152,7 +152,7 @@ hipError_t by_pairs(int k, F &&f) {
 hipError_t launch_combine_pairs(int dt, int out_dt, const CombineArgs &all, hipStream_t s) {
     const int per = (int)(all.H / 8);
     const int64_t wide = (per + kThreads - 1) / kThreads;  // workgroups of a token, where it fills one
-    // A launch has fewer than 2^32 threads (2^20 tokens of 30728 columns would be more): tokens are taken in turns.
+    // A launch has fewer than 2^32 threads (2^20 tokens of 30736 columns would be more): tokens are taken in turns.
     const int64_t most = kMaxBlocks / wide;
     auto go = [&](auto dt_c, auto out_c) {
         return by_pairs<7>(all.k, [&](auto k_c) {

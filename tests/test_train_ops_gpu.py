@@ -1070,7 +1070,7 @@ def test_combine_of_more_than_one_launch():
     """As many tokens as there may be of rows so long that their threads pass 2^32; exact: one pair a token, weights that
     are powers of two."""
     qr = _qr()
-    T, n = 1 << 20, 30728
+    T, n = 1 << 20, 30736
     g = torch.Generator(device="cuda").manual_seed(1)
     y = torch.randn(5, n, generator=g, device="cuda").to(BF16)
     place = torch.randint(0, 5, (T, 1), generator=g, device="cuda")
