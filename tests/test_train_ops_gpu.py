@@ -1115,3 +1115,22 @@ def test_route_groups_whose_differences_round_to_ties():
     bias = torch.ones(8).cuda()
     for keep, want in ((1, [6, 7]), (2, [6, 2, 7, 3])):
         assert qr.route(x, 2 * keep, bias=bias, groups=4, keep_groups=keep)[0].tolist() == [want]
+
+
+@pytest.mark.parametrize("T,k", [(64, 1024), (64, 1025), (1, 1 << 16), (3, 40000), (70, 2000)])
+def test_from_ids_of_many_pairs_a_token(T, k):
+    """By the kernels and by torch's operations, which the longest of these take: the same order."""
+    ids = torch.randint(-1, 12, (T, k), generator=gen(k))
+    check_order(_qr().Routing.from_ids(ids.cuda(), torch.rand(T, k).cuda(), 12)._tensors(), ids, 12)
+
+
+def test_from_ids_leaves_long_rows_to_torch(monkeypatch):
+    """One workgroup orders the pairs of up to 64 tokens: beyond 2^16 of them torch's operations are faster."""
+    qr = _qr()
+    from quantized_routed_moe_amd import experts
+    seen = []
+    kernel = experts.sort_pairs
+    monkeypatch.setattr(experts, "sort_pairs", lambda ids, n: seen.append(tuple(ids.shape)) or kernel(ids, n))
+    for T, k in ((64, 1024), (64, 1025), (1, 1 << 16), (1, (1 << 16) + 1), (100000, 8), (500, 2000)):
+        qr.Routing.from_ids(torch.zeros(T, k, dtype=torch.int64).cuda(), torch.rand(T, k).cuda(), 12)
+    assert seen == [(64, 1024), (1, 1 << 16), (100000, 8)]
